@@ -108,6 +108,20 @@ _SIGS = {
 }
 
 
+def declare(sigs: dict) -> None:
+    """Adds entry points of the library to what lib() binds."""
+    _SIGS.update(sigs)
+    if _lib is not None:
+        _bind(_lib, sigs)
+
+
+def _bind(L: ctypes.CDLL, sigs: dict) -> None:
+    for name, (args, res) in sigs.items():
+        fn = getattr(L, name)
+        fn.argtypes = args
+        fn.restype = res
+
+
 def lib() -> ctypes.CDLL:
     """Load libmoe_fp4.so; raises if it has not been built."""
     global _lib
@@ -116,15 +130,12 @@ def lib() -> ctypes.CDLL:
             raise RuntimeError(f"{LIB_PATH} is missing: build it with "
                                "`python -m block_scaled_fp4_gather_amd.build`")
         L = ctypes.CDLL(LIB_PATH)
-        for name, (args, res) in _SIGS.items():
-            fn = getattr(L, name)
-            fn.argtypes = args
-            fn.restype = res
+        _bind(L, _SIGS)
         _lib = L
     return _lib
 
 
-def _check(fn: str, status: int) -> None:
+def check(fn: str, status: int) -> None:
     if status != 0:
         raise MoeFp4Error(fn, status)
 
@@ -148,24 +159,24 @@ def status_string(s: int) -> str:
 
 def prepared_bytes(desc: Desc) -> int:
     n = _SZ()
-    _check("moe_fp4_prepared_bytes", lib().moe_fp4_prepared_bytes(ctypes.byref(desc.c()), ctypes.byref(n)))
+    check("moe_fp4_prepared_bytes", lib().moe_fp4_prepared_bytes(ctypes.byref(desc.c()), ctypes.byref(n)))
     return n.value
 
 
 def workspace_bytes(desc: Desc, M: int) -> int:
     n = _SZ()
-    _check("moe_fp4_workspace_bytes", lib().moe_fp4_workspace_bytes(ctypes.byref(desc.c()), M, ctypes.byref(n)))
+    check("moe_fp4_workspace_bytes", lib().moe_fp4_workspace_bytes(ctypes.byref(desc.c()), M, ctypes.byref(n)))
     return n.value
 
 
 def prepare(desc: Desc, w13_codes, w13_scales, w2_codes, w2_scales, g13, g2, prepared, stream=None):
-    _check("moe_fp4_prepare", lib().moe_fp4_prepare(
+    check("moe_fp4_prepare", lib().moe_fp4_prepare(
         ctypes.byref(desc.c()), _ptr(w13_codes), _ptr(w13_scales), _ptr(w2_codes), _ptr(w2_scales),
         _ptr(g13), _ptr(g2), _ptr(prepared), prepared.numel() * prepared.element_size(), _stream(stream)))
 
 
 def unprepare(desc: Desc, prepared, w13_codes, w13_scales, w2_codes, w2_scales, g13, g2, stream=None):
-    _check("moe_fp4_unprepare", lib().moe_fp4_unprepare(
+    check("moe_fp4_unprepare", lib().moe_fp4_unprepare(
         ctypes.byref(desc.c()), _ptr(prepared), _ptr(w13_codes), _ptr(w13_scales), _ptr(w2_codes),
         _ptr(w2_scales), _ptr(g13), _ptr(g2), _stream(stream)))
 
@@ -181,20 +192,20 @@ def forward(desc: Desc, prepared, x, ids, w, out, workspace, stream=None, tuning
     if tuning is not None or phases is not None:
         assert ids.dtype == torch.int32
         tp = ctypes.byref(tuning) if tuning is not None else None
-        _check("moe_fp4_forward_ex", lib().moe_fp4_forward_ex(*args, tp, 3 if phases is None else phases,
+        check("moe_fp4_forward_ex", lib().moe_fp4_forward_ex(*args, tp, 3 if phases is None else phases,
                                                                _stream(stream)))
     elif ids.dtype == torch.int64:
-        _check("moe_fp4_forward_i64", lib().moe_fp4_forward_i64(*args, _stream(stream)))
+        check("moe_fp4_forward_i64", lib().moe_fp4_forward_i64(*args, _stream(stream)))
     else:
         assert ids.dtype == torch.int32
-        _check("moe_fp4_forward", lib().moe_fp4_forward(*args, _stream(stream)))
+        check("moe_fp4_forward", lib().moe_fp4_forward(*args, _stream(stream)))
 
 
 def forward_noalloc(desc: Desc, prepared, x, ids, w, out, stream=None):
     """moe_fp4_forward with the library's own 64 MiB workspace (int32 ids):
     the entry point for callers that cannot allocate."""
     assert ids.dtype == torch.int32
-    _check("moe_fp4_forward_noalloc", lib().moe_fp4_forward_noalloc(
+    check("moe_fp4_forward_noalloc", lib().moe_fp4_forward_noalloc(
         ctypes.byref(desc.c()), _ptr(prepared), _ptr(x), x.shape[0], _ptr(ids), _ptr(w), _ptr(out),
         _stream(stream)))
 
@@ -203,14 +214,14 @@ def plan(desc: Desc, M: int, tuning: Tuning | None = None) -> Tuning:
     """The path and launch shape a forward call with M tokens takes (every
     field resolved; path is PATH_DECODE or PATH_GROUPED)."""
     out = Tuning()
-    _check("moe_fp4_plan", lib().moe_fp4_plan(ctypes.byref(desc.c()), M,
+    check("moe_fp4_plan", lib().moe_fp4_plan(ctypes.byref(desc.c()), M,
                                               ctypes.byref(tuning) if tuning is not None else None,
                                               ctypes.byref(out)))
     return out
 
 
 def dequant_export(desc: Desc, prepared, expert: int, which: int, out, stream=None):
-    _check("moe_fp4_dequant_export", lib().moe_fp4_dequant_export(
+    check("moe_fp4_dequant_export", lib().moe_fp4_dequant_export(
         ctypes.byref(desc.c()), _ptr(prepared), expert, which, _ptr(out), _stream(stream)))
 
 
@@ -221,7 +232,7 @@ def mxfp8_quantize(x, codes=None, scales=None, stream=None):
         codes = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
     if scales is None:
         scales = torch.empty((rows, cols // 32), dtype=torch.uint8, device=x.device)
-    _check("moe_fp4_mxfp8_quantize", lib().moe_fp4_mxfp8_quantize(
+    check("moe_fp4_mxfp8_quantize", lib().moe_fp4_mxfp8_quantize(
         _ptr(x), rows, cols, _ptr(codes), _ptr(scales), _stream(stream)))
     return codes, scales
 

@@ -317,6 +317,150 @@ moe_fp4_status moe_fp4_plan(const moe_fp4_desc* desc, int32_t M, const moe_fp4_t
 moe_fp4_status moe_fp4_mxfp8_quantize(const uint16_t* x, int64_t rows, int32_t cols, uint8_t* codes,
                                       uint8_t* scales, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Operators around the layer: the router that gives it ids and weights, the
+ * FP8 linear map of shared experts and projections, and the norms before and
+ * after the block.  The conventions above hold for them too (caller-owned
+ * device memory, no allocation, no synchronisation, checks before any
+ * launch); calls that share a workspace must be ordered on one stream. */
+
+typedef enum {
+  MOE_FP4_TYPE_BF16 = 0,
+  MOE_FP4_TYPE_F32 = 1
+} moe_fp4_type;
+
+typedef enum {
+  MOE_FP4_SCORE_SOFTMAX = 0, /* p = softmax over all E logits */
+  MOE_FP4_SCORE_SIGMOID = 1  /* p = 1 / (1 + exp(-z)) per expert */
+} moe_fp4_scoring;
+
+/* Router of a layer.  For a token x and router weights Wr [E][H]:
+ *     z_e = sum_h x[h] * Wr[e][h],   p = softmax(z) or sigmoid(z),
+ *     t_e = p_e + bias[e]                 (a bias is used for the choice only)
+ *   groups: with num_groups > 1 the experts are num_groups runs of E /
+ *     num_groups, a group's score is the sum of its two largest t, and only
+ *     the top_groups best groups' experts can be taken;
+ *   ids: the top_k experts of largest t (without a bias, of largest z, which
+ *     is the same order), largest first, ties to the lowest index;
+ *   weights: p of the taken experts, divided by their sum with renormalize,
+ *     times scale.
+ * The choice is that of z in exact arithmetic and t in 64 bits, whatever M:
+ * logits are fp32 matrix products, and those that decide something within
+ * their error bound are recomputed in 64 bits.  An expert whose t is NaN or
+ * -infinity (a bias of -infinity masks one) is never taken; a token with
+ * fewer than top_k experts to take gets id -1 and weight 0 in the slots
+ * left, which the layer's calls skip.  Weights that sum to 0 stay 0. */
+typedef struct {
+  int32_t num_experts; /* E, at most 512 */
+  int32_t hidden;      /* H, a multiple of 8, at most 65536 */
+  int32_t top_k;       /* at most 64 and the experts of top_groups groups */
+  int32_t max_tokens;  /* capacity for workspace sizing, at most 2^20 */
+  int32_t weight_type; /* moe_fp4_type of Wr */
+  int32_t scoring;     /* moe_fp4_scoring */
+  int32_t num_groups;  /* 1 (no groups) to 64, divides E, 2 experts or more each */
+  int32_t top_groups;  /* 1 to num_groups */
+  int32_t renormalize; /* 0 or 1 */
+  float scale;         /* finite */
+} moe_fp4_router_desc;
+
+/* Bytes of the prepared router weights, and the preparation, once per
+ * router: a permutation of Wr ([E][H], device, 16-byte aligned; fp32 as three
+ * bf16 terms that sum to it) and the experts' 2-norms, into `prepared`
+ * (device, 256-byte aligned). */
+moe_fp4_status moe_fp4_router_prepared_bytes(const moe_fp4_router_desc* desc, size_t* bytes);
+moe_fp4_status moe_fp4_router_prepare(const moe_fp4_router_desc* desc, const void* weight, void* prepared,
+                                      size_t prepared_bytes, void* stream);
+
+/* Workspace bytes for route calls on `desc` (device, 256-byte aligned),
+ * enough for every M <= max_tokens; M is checked against max_tokens. */
+moe_fp4_status moe_fp4_router_workspace_bytes(const moe_fp4_router_desc* desc, int32_t M, size_t* bytes);
+
+/* Routes M tokens.  x: bf16 [M][H], 16-byte aligned; bias: fp32 [E] or NULL;
+ * topk_ids: int32 [M][k] and topk_w: fp32 [M][k], overwritten; logits: fp32
+ * [M][E], overwritten, or NULL.  M may be 0 (nothing is launched). */
+moe_fp4_status moe_fp4_route(const moe_fp4_router_desc* desc, const void* prepared, const uint16_t* x, int32_t M,
+                             const float* bias, int32_t* topk_ids, float* topk_w, float* logits, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* act_fn of moe_fp4_fp8_desc besides the layer's activations */
+#define MOE_FP4_FN_NONE (-1)
+
+/* Linear map with E4M3 weights and an fp32 scale per block of 128 x 128:
+ *     y[n] = sum_k q(x)[k] * codes[n][k] * scales[n / 128][k / 128],
+ * where q(x) is x quantised in blocks of 128 along K: the least power of two
+ * s >= 2^-127 with |x| <= 448 s over the block, values x / s rounded to
+ * nearest-even E4M3, times s.  Sums in fp32, an activation where asked for
+ * (moe_fp4_act_fn, the gated ones over gate and up rows), one rounding to
+ * bf16.  A block of x that holds a NaN or an infinity makes its token's
+ * outputs NaN; other tokens are not touched. */
+typedef struct {
+  int32_t in_features;  /* K, a multiple of 8 */
+  int32_t out_features; /* N, a multiple of 8; K * N at most 2^30 */
+  int32_t max_tokens;   /* capacity for workspace sizing, at most 2^20 */
+  int32_t act_fn;       /* MOE_FP4_FN_NONE or a moe_fp4_act_fn */
+  float act_alpha;      /* SWIGLUOAI only, else ignored */
+  float act_beta;
+  float act_limit;
+} moe_fp4_fp8_desc;
+
+/* Bytes of the prepared weights, and the preparation, once per map: a
+ * permutation of the bytes into `prepared` (device, 256-byte aligned).
+ * codes: E4M3 bytes [N][K] (device, 16-byte aligned), scales: fp32
+ * [ceil(N / 128)][ceil(K / 128)]; for a gated activation both hold the gate's
+ * and then the up's ([2N][K], [2 ceil(N / 128)][ceil(K / 128)]). */
+moe_fp4_status moe_fp4_fp8_prepared_bytes(const moe_fp4_fp8_desc* desc, size_t* bytes);
+moe_fp4_status moe_fp4_fp8_prepare(const moe_fp4_fp8_desc* desc, const uint8_t* codes, const float* scales,
+                                   void* prepared, size_t prepared_bytes, void* stream);
+
+/* Workspace bytes for calls on `desc` (device, 256-byte aligned), enough for
+ * every M <= max_tokens; M is checked against max_tokens. */
+moe_fp4_status moe_fp4_fp8_workspace_bytes(const moe_fp4_fp8_desc* desc, int32_t M, size_t* bytes);
+
+/* The map on M tokens.  x: bf16 [M][K], out: bf16 [M][N], overwritten; both
+ * 16-byte aligned, not overlapping.  M may be 0 (nothing is launched). */
+moe_fp4_status moe_fp4_fp8_linear(const moe_fp4_fp8_desc* desc, const void* prepared, const uint16_t* x, int32_t M,
+                                  uint16_t* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* What multiplies the branch before it joins the residual. */
+typedef enum {
+  MOE_FP4_GATE_NONE = 0,
+  MOE_FP4_GATE_CHANNEL = 1, /* [H] */
+  MOE_FP4_GATE_TOKEN = 2,   /* [M] */
+  MOE_FP4_GATE_FULL = 3     /* [M][H] */
+} moe_fp4_gate;
+
+/* Norms before and after a block, fused with its gate and residual:
+ *     b  = y + y2                                            (y2 may be absent)
+ *     n  = b / sqrt(mean(b^2) + eps) * (post_weight + weight_offset)
+ *                                                 (n = b without post_weight)
+ *     h' = residual_scale * h + branch_scale * g * n     g: gate, sigmoid(gate)
+ *                                                        or 1 without a gate
+ *     x  = h' / sqrt(mean(h'^2) + eps) * (pre_weight + weight_offset)
+ * in fp32, h' rounded once to the residual's type and x, which takes h' as
+ * stored, once to bf16.  Without y, x is the norm of h itself. */
+typedef struct {
+  int32_t hidden;        /* H, a multiple of 8, at most 32768 */
+  int32_t residual_type; /* moe_fp4_type of h and h_out */
+  int32_t weight_type;   /* moe_fp4_type of post_weight, pre_weight and gate */
+  int32_t gate;          /* moe_fp4_gate */
+  int32_t gate_sigmoid;  /* 0 or 1 */
+  float eps;             /* >= 0 */
+  float residual_scale;  /* all finite */
+  float branch_scale;
+  float weight_offset;
+} moe_fp4_norm_desc;
+
+/* h: [M][H]; y, y2: bf16 [M][H] or NULL; gate: by desc->gate, NULL for
+ * MOE_FP4_GATE_NONE; post_weight, pre_weight: [H] or NULL; h_out: [M][H],
+ * given exactly when y is; x_out: bf16 [M][H], given exactly when pre_weight
+ * is.  Device pointers, 16-byte aligned (a token gate: its element's size).
+ * An output may be one of the [M][H] inputs itself where the types agree
+ * (h_out = h updates the residual in place); any other overlap is refused.
+ * M may be 0 (nothing is launched). */
+moe_fp4_status moe_fp4_block_norm(const moe_fp4_norm_desc* desc, int32_t M, const void* h, const uint16_t* y,
+                                  const uint16_t* y2, const void* gate, const void* post_weight,
+                                  const void* pre_weight, void* h_out, uint16_t* x_out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,142 @@
+"""Refusals of the operators around the expert layer: bad arguments are
+rejected before any HIP call (so these run without a GPU)."""
+from __future__ import annotations
+
+import ctypes
+
+import pytest
+import torch
+
+from block_scaled_fp4_gather_amd import block, moe
+
+EINVAL, EUNSUPPORTED, EWORKSPACE = 1, 2, 3
+
+
+@pytest.fixture(scope="module")
+def L():
+    return moe.lib()
+
+
+def _router(**kw):
+    base = dict(E=64, H=256, k=4, max_tokens=8)
+    return block.RouterDesc(**{**base, **kw})
+
+
+def _sized(fn, desc):
+    n = ctypes.c_size_t()
+    return fn(ctypes.byref(desc.c()), ctypes.byref(n)), n.value
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(), 0), (dict(E=0), EINVAL), (dict(H=0), EINVAL), (dict(H=252), EINVAL), (dict(k=0), EINVAL),
+    (dict(k=65), EINVAL), (dict(E=128, k=65), EUNSUPPORTED), (dict(E=513), EUNSUPPORTED), (dict(E=512), 0),
+    (dict(H=65544), EUNSUPPORTED), (dict(max_tokens=-1), EINVAL), (dict(max_tokens=(1 << 20) + 1), EUNSUPPORTED),
+    (dict(weight=2), EINVAL), (dict(scoring=2), EINVAL), (dict(groups=0), EINVAL), (dict(groups=3), EINVAL),
+    (dict(groups=64), EINVAL), (dict(groups=8, top_groups=9), EINVAL), (dict(groups=8, top_groups=0), EINVAL),
+    (dict(groups=32, top_groups=1, k=4), EINVAL), (dict(groups=32, top_groups=2, k=4), 0),
+    (dict(E=512, groups=128, k=1), EUNSUPPORTED), (dict(scale=float("nan")), EINVAL),
+    (dict(scale=float("inf")), EINVAL),
+])
+def test_router_descriptor(L, kw, status):
+    assert _sized(L.moe_fp4_router_prepared_bytes, _router(**kw))[0] == status
+
+
+def test_router_sizes(L):
+    """bf16 bytes once, fp32 as three planes; the workspace covers every M."""
+    _, n = _sized(L.moe_fp4_router_prepared_bytes, _router(E=100, H=264))
+    assert n >= 2 * 112 * 288 + 4 * 100
+    _, n3 = _sized(L.moe_fp4_router_prepared_bytes, _router(E=100, H=264, weight="fp32"))
+    assert n3 >= 6 * 112 * 288 + 4 * 100
+    last = 0
+    for cap in (1, 5, 16, 17, 100, 1000, 4096, 20000, 40000):
+        ws = block.router_workspace_bytes(_router(E=256, H=7168, max_tokens=cap), 1)
+        assert ws >= last and ws >= 4 * cap * 257
+        last = ws
+
+
+def test_route_rejects_before_launch(L):
+    d = _router()
+    ref = ctypes.byref(d.c())
+    need = block.router_workspace_bytes(d, 8)
+
+    def call(M=8, prepared=256, x=512, bias=None, ids=1024, w=2048, logits=None, ws=4096, n=need):
+        return L.moe_fp4_route(ref, prepared, x, M, bias, ids, w, logits, ws, n, None)
+
+    assert call(M=0) == 0
+    assert call(M=9) == EINVAL and call(M=-1) == EINVAL
+    for name in ("prepared", "x", "ids", "w", "ws"):
+        assert call(**{name: None}) == EINVAL
+    assert call(prepared=128) == EINVAL and call(x=520) == EINVAL and call(ids=1026) == EINVAL
+    assert call(w=2050) == EINVAL and call(bias=6) == EINVAL and call(logits=6) == EINVAL and call(ws=4224) == EINVAL
+    assert call(n=need - 1) == EWORKSPACE
+    assert L.moe_fp4_router_prepare(ref, None, 256, 1 << 30, None) == EINVAL
+    assert L.moe_fp4_router_prepare(ref, 8, 256, 1 << 30, None) == EINVAL
+    assert L.moe_fp4_router_prepare(ref, 16, 256, 16, None) == EWORKSPACE
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(), 0), (dict(K=0), EINVAL), (dict(N=0), EINVAL), (dict(K=124), EINVAL), (dict(N=20), EINVAL),
+    (dict(max_tokens=-1), EINVAL), (dict(max_tokens=(1 << 20) + 1), EUNSUPPORTED), (dict(fn=4), EINVAL),
+    (dict(fn=-2), EINVAL), (dict(fn="swigluoai"), EINVAL), (dict(fn="swigluoai", alpha=1.0, limit=7.0), 0),
+    (dict(fn="swigluoai", alpha=1.0, beta=float("nan"), limit=7.0), EINVAL), (dict(K=1 << 16, N=1 << 15), EUNSUPPORTED),
+])
+def test_fp8_descriptor(L, kw, status):
+    desc = block.Fp8Desc(**{**dict(K=128, N=64, max_tokens=8), **kw})
+    assert _sized(L.moe_fp4_fp8_prepared_bytes, desc)[0] == status
+
+
+def test_fp8_linear_rejects_before_launch(L):
+    d = block.Fp8Desc(128, 64, 8)
+    ref = ctypes.byref(d.c())
+    need = block.fp8_workspace_bytes(d, 8)
+
+    def call(M=8, prepared=256, x=1 << 14, out=1 << 16, ws=1 << 18, n=need):
+        return L.moe_fp4_fp8_linear(ref, prepared, x, M, out, ws, n, None)
+
+    assert call(M=0) == 0
+    assert call(M=9) == EINVAL and call(M=-1) == EINVAL
+    for name in ("prepared", "x", "out", "ws"):
+        assert call(**{name: None}) == EINVAL
+    assert call(prepared=128) == EINVAL and call(x=(1 << 14) + 8) == EINVAL and call(out=(1 << 16) + 8) == EINVAL
+    assert call(ws=(1 << 18) + 128) == EINVAL
+    assert call(out=1 << 14) == EINVAL and call(out=(1 << 14) + 2 * 8 * 128 - 16) == EINVAL  # overlaps x
+    assert call(n=need - 1) == EWORKSPACE
+    assert L.moe_fp4_fp8_prepare(ref, 16, None, 256, 1 << 30, None) == EINVAL
+    assert L.moe_fp4_fp8_prepare(ref, 16, 16, 256, 16, None) == EWORKSPACE
+
+
+def test_block_norm_rejects_before_launch(L):
+    H, M = 64, 4
+    n = M * H
+
+    def call(M=M, h=1 << 12, y=1 << 14, y2=None, gate=None, post=None, pre=1 << 20, ho=1 << 16, xo=1 << 18, **kw):
+        d = dict(H=H, rt=0, wt=0, kind=0, sig=0, eps=1e-6, rs=1.0, bs=1.0, off=0.0)
+        d.update(kw)
+        c = block._NormDesc(*d.values())
+        return L.moe_fp4_block_norm(ctypes.byref(c), M, h, y, y2, gate, post, pre, ho, xo, None)
+
+    assert call(M=0) == 0
+    for bad in (dict(M=-1), dict(H=0), dict(H=60), dict(rt=2), dict(wt=2), dict(kind=4), dict(sig=2),
+                dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf")), dict(rs=float("inf")), dict(bs=float("nan")),
+                dict(off=float("inf")), dict(h=None), dict(ho=None), dict(xo=None), dict(pre=None),
+                dict(y=None), dict(y=None, ho=None, y2=1 << 15), dict(y=None, ho=None, post=1 << 21),
+                dict(y=None, ho=None, pre=None, xo=None), dict(kind=1), dict(gate=1 << 22),
+                dict(h=(1 << 12) + 8), dict(xo=(1 << 18) + 2), dict(kind=1, gate=(1 << 22) + 2),
+                dict(kind=2, gate=(1 << 22) + 1), dict(kind=2, wt=1, gate=(1 << 22) + 2),
+                dict(ho=(1 << 12) + 16),              # a shifted residual
+                dict(rt=1, ho=1 << 14),               # fp32 residual over the bf16 branch
+                dict(xo=1 << 16),                     # both outputs in one place
+                dict(ho=(1 << 20) - 2 * n + 16)):     # over the weights
+        assert call(**bad) == EINVAL, bad
+    assert call(H=32776) == EUNSUPPORTED
+    assert L.moe_fp4_block_norm(None, M, 16, None, None, None, None, 16, None, 16, None) == EINVAL
+
+
+def test_binding_refuses_what_does_not_fit():
+    h = torch.zeros(2, 64)
+    with pytest.raises(ValueError):
+        block.block_norm(h.double(), pre_weight=torch.ones(64))
+    with pytest.raises(ValueError):
+        block.block_norm(h, pre_weight=torch.ones(64))  # not on a GPU
+    with pytest.raises(ValueError):
+        block.block_norm(h, h.bfloat16(), gate=torch.ones(3), pre_weight=torch.ones(64))
