@@ -86,93 +86,287 @@ __global__ void __launch_bounds__(256)
 
 // ---- logits
 
-// How a call of M tokens is cut: 16 tt tokens and 128 experts per workgroup,
-// H in `splits` slices of `per` K blocks.
+// The matrix instruction's accumulator takes this many instructions before it
+// is added to a second one and cleared: the roundings of a chain grow with its
+// length and so does the bound on the logits' error, on which it hangs how
+// many have to be recomputed.
+constexpr int kChain = 8;
+
+// How a call of M tokens is cut.
+//   few tokens: 16 tt tokens x 16 experts per workgroup, H in `splits` slices
+//     of `per` K blocks, a slice dealt to the workgroup's 4 waves;
+//   many: BM x BE tiles (route_gemm), H in `splits` slices of `per` K blocks.
 struct LogitPlan {
-  int tt, splits, per;
+  bool gemm;
+  int tt, bm, be, splits, per;
 };
 
+// K blocks (of 32) of a step of the tiled kernel
+constexpr int gemm_step(int planes) { return planes == 1 ? 2 : 1; }
+
 LogitPlan logit_plan(const RouterShape& s, int64_t M) {
-  LogitPlan p;
-  p.tt = M <= 16 ? 1 : M <= 32 ? 2 : 4;
-  const int64_t groups = ((M + 16 * p.tt - 1) / (16 * p.tt)) * ((s.E + 127) / 128);
-  int64_t splits = 512 / groups;
-  splits = splits < 1 ? 1 : splits > 16 ? 16 : splits;
+  LogitPlan p{};
   const int kb = s.kblocks();
-  if (splits > kb) splits = kb;
-  p.per = (int)((kb + splits - 1) / splits);
+  p.gemm = M > 256;
+  int64_t splits;
+  if (!p.gemm) {
+    p.tt = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+    splits = (kb + 31) / 32;
+  } else {
+    p.be = s.E <= 128 || s.planes == 3 ? 128 : 256;
+    p.bm = p.be == 256 || s.planes == 3 ? 128 : 64;
+    const int64_t tiles = ((M + p.bm - 1) / p.bm) * ((s.E + p.be - 1) / p.be);
+    splits = (p.be == 256 ? 256 : 512) / tiles;
+    splits = splits < 1 ? 1 : splits > 8 ? 8 : splits;
+  }
+  const int unit = p.gemm ? gemm_step(s.planes) : 4;
+  const int64_t units = (kb + unit - 1) / unit;
+  if (splits > units) splits = units;
+  p.per = (int)((units + splits - 1) / splits) * unit;
   p.splits = (kb + p.per - 1) / p.per;
   return p;
 }
 
-// Partial logits f32 [split][M][16 subtiles] and partial sums of x^2
+// Partial logits f32 [split][M][16 subtiles] and partial sums of (2^32 x)^2
 // f32 [split][M].
 int64_t partial_floats(const RouterShape& s, int64_t M) {
   const LogitPlan p = logit_plan(s, M);
   return p.splits * M * (16 * (int64_t)s.subtiles() + 1);
 }
 
-// Wave w of a workgroup takes expert subtiles 2 w and 2 w + 1 of its 128
-// experts, the 16 TT tokens and the K blocks of its slice.
+// Squares of 2^32 x: those of |x| from 2^-95 to 2^31 neither vanish nor
+// overflow.
+__device__ __forceinline__ float add_squares(bf16x8_t v, float sq) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float f = (float)v[j] * 0x1p32f;
+    sq = fmaf(f, f, sq);
+  }
+  return sq;
+}
+
+// Few tokens: the weights are read once (per 64 tokens), straight into
+// registers.  Four waves share a slice of H and join their sums in LDS.
 template <int TT, int NP>
 __global__ void __launch_bounds__(256)
-    route_logits_kernel(RouterShape s, const uint8_t* __restrict__ prepared, const uint16_t* __restrict__ x, int M,
-                        int per, float* __restrict__ part, float* __restrict__ xx) {
+    route_few_kernel(RouterShape s, const uint8_t* __restrict__ prepared, const uint16_t* __restrict__ x, int M,
+                     int per, float* __restrict__ part, float* __restrict__ xx) {
+  __shared__ f32x4_t sums[4][TT][64];
+  __shared__ float squares[4][TT][16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r = lane & 15, g = lane >> 4;
-  const int kb = s.kblocks(), ns = s.subtiles(), Ep = 16 * ns;
-  const int64_t tok0 = (int64_t)blockIdx.x * (16 * TT);
-  const int sub0 = blockIdx.y * 8 + 2 * wave;
-  const int b0 = blockIdx.z * per, b1 = min(kb, b0 + per);
-  if (sub0 >= ns) return;
-  const bool two = sub0 + 1 < ns;
+  const int kb = s.kblocks(), Ep = 16 * s.subtiles();
+  const int sub = blockIdx.x;
+  const int64_t split = blockIdx.y, tok0 = (int64_t)blockIdx.z * (16 * TT);
+  const int b0 = (int)split * per + wave, b1 = min(kb, (int)(split + 1) * per);
+  const bool norms = sub == 0;
   const int64_t plane = s.plane_bytes();
-  const bool norms = blockIdx.y == 0 && wave == 0;
-  f32x4_t acc[2][TT];
+  const uint8_t* const w0 = prepared + (int64_t)sub * kb * 1024 + lane * 16;
+  f32x4_t acc[TT], chain[TT];
   float sq[TT];
   const uint16_t* xr[TT];
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
-    acc[0][t] = acc[1][t] = f32x4_t{};
+    acc[t] = chain[t] = f32x4_t{};
     sq[t] = 0.0f;
     xr[t] = x + min(tok0 + 16 * t + r, (int64_t)M - 1) * s.H + g * 8;
   }
-  for (int b = b0; b < b1; ++b) {
-    bf16x8_t bop[TT];
+  // the slice's blocks of this wave, kAhead at a time: all loads first
+  constexpr int kAhead = TT == 4 || NP == 3 ? 2 : 4;
+  static_assert(kAhead * NP <= kChain, "chain length");
+  int in_chain = 0;
+#pragma unroll 1
+  for (int b = b0; b < b1; b += 4 * kAhead) {
+    uint4 wv[kAhead][NP], xv[kAhead][TT];
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (b * 32 + g * 8 < s.H) v = *(const uint4*)(xr[t] + b * 32);
-      bop[t] = __builtin_bit_cast(bf16x8_t, v);
-      if (norms)
+    for (int i = 0; i < kAhead; ++i) {
+      const int bi = b + 4 * i;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float v = (float)bop[t][j] * 0x1p32f;  // squares of 2^-95 .. 2^31 neither vanish nor overflow
-          sq[t] = fmaf(v, v, sq[t]);
-        }
-    }
+      for (int q = 0; q < NP; ++q) wv[i][q] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      const int64_t at = ((int64_t)(f && two ? sub0 + 1 : sub0) * kb + b) * 1024 + lane * 16;
+      for (int t = 0; t < TT; ++t) xv[i][t] = make_uint4(0, 0, 0, 0);
+      if (bi < b1) {
 #pragma unroll
-      for (int q = 0; q < NP; ++q) {
-        const bf16x8_t a = __builtin_bit_cast(bf16x8_t, *(const uint4*)(prepared + q * plane + at));
+        for (int q = 0; q < NP; ++q) wv[i][q] = *(const uint4*)(w0 + q * plane + (int64_t)bi * 1024);
+        if (bi * 32 + g * 8 < s.H)
 #pragma unroll
-        for (int t = 0; t < TT; ++t)
-          acc[f][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, bop[t], acc[f][t], 0, 0, 0);
+          for (int t = 0; t < TT; ++t) xv[i][t] = *(const uint4*)(xr[t] + bi * 32);
       }
     }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        const bf16x8_t bop = __builtin_bit_cast(bf16x8_t, xv[i][t]);
+        if (norms) sq[t] = add_squares(bop, sq[t]);
+#pragma unroll
+        for (int q = 0; q < NP; ++q)
+          chain[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, wv[i][q]), bop, chain[t], 0,
+                                                             0, 0);
+      }
+    in_chain += kAhead * NP;
+    if (in_chain + kAhead * NP > kChain) {
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        acc[t] += chain[t];
+        chain[t] = f32x4_t{};
+      }
+      in_chain = 0;
+    }
   }
-  const int64_t split = blockIdx.z;
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
+    sums[wave][t][lane] = acc[t] + chain[t];
+    if (norms) {
+      float v = sq[t];
+      v += __shfl_xor(v, 16);
+      v += __shfl_xor(v, 32);
+      if (g == 0) squares[wave][t][r] = v;
+    }
+  }
+  __syncthreads();
+  for (int t = wave; t < TT; t += 4) {
     const int64_t m = tok0 + 16 * t + r;
     if (m < M) {
-      float* o = part + (split * M + m) * Ep + sub0 * 16 + 4 * g;
-      *(f32x4_t*)o = acc[0][t];
-      if (two) *(f32x4_t*)(o + 16) = acc[1][t];
+      const f32x4_t v = (sums[0][t][lane] + sums[1][t][lane]) + (sums[2][t][lane] + sums[3][t][lane]);
+      *(f32x4_t*)(part + (split * M + m) * Ep + sub * 16 + 4 * g) = v;
+      if (norms && g == 0)
+        xx[split * M + m] = squares[0][t][r] + squares[1][t][r] + squares[2][t][r] + squares[3][t][r];
     }
-    if (norms) {
+  }
+}
+
+// Many tokens: BM tokens x BE experts per workgroup, so that x is read once
+// for up to BE experts; x and the weights go to LDS by direct copies, two
+// steps ahead in a ring of three slots, one barrier per step.  WM x WE waves.
+//
+// An x slot holds BM rows of 32 S values; the 16-byte chunk c of row r is at
+// position c ^ swizzle(r), which spreads the 16 rows that a fragment read
+// takes one chunk of over the LDS banks.
+template <int BM, int BE, int NP>
+struct RouteGemm {
+  static constexpr int S = gemm_step(NP);           // K blocks of 32 per step
+  static constexpr int kWaves = 8;
+  static constexpr int WE = BE / 64, WM = kWaves / WE;  // waves over experts and tokens: 64 experts each
+  static constexpr int TT = BM / 16 / WM;           // token tiles of a wave
+  static constexpr int kRow = 64 * S;               // bytes of an x row in a slot
+  static constexpr int kX = BM * kRow, kW = NP * S * (BE / 16) * 1024;
+  static constexpr int kSlot = kX + kW;
+  static constexpr int kXCopies = kX / 1024 / kWaves, kWCopies = kW / 1024 / kWaves;
+  static constexpr int kCopies = kXCopies + kWCopies;
+  static constexpr int kLds = 3 * kSlot;
+  static_assert(kX % (1024 * kWaves) == 0 && kW % (1024 * kWaves) == 0 && TT >= 1, "whole copies per wave");
+};
+
+template <int S>
+__device__ __forceinline__ int row_swizzle(int r) {
+  return S == 2 ? a_swz(r) : ((r >> 1) ^ (r >> 3)) & 3;
+}
+
+template <int BM, int BE, int NP>
+__global__ void __launch_bounds__(512)
+    route_gemm_kernel(RouterShape s, const uint8_t* __restrict__ prepared, const uint16_t* __restrict__ x, int M,
+                      int per, float* __restrict__ part, float* __restrict__ xx) {
+  using G = RouteGemm<BM, BE, NP>;
+  constexpr int S = G::S, TT = G::TT, kChunks = G::kRow / 16;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int r = lane & 15, g = lane >> 4;
+  const int we = wave % G::WE, wm = wave / G::WE;
+  const int kb = s.kblocks(), ns = s.subtiles(), Ep = 16 * ns;
+  const int64_t split = blockIdx.z, tok0 = (int64_t)blockIdx.x * BM;
+  const int b0 = (int)split * per, b1 = min(kb, b0 + per);
+  const int nsteps = (b1 - b0 + S - 1) / S;
+  const int sub0 = blockIdx.y * (BE / 16);
+  const int64_t plane = s.plane_bytes();
+
+  // copy c of a step (the same number for every wave; past the last step and
+  // past the data they repeat what is there and are not used)
+  auto copy = [&](int step, int c) {
+    const int b = b0 + min(step, nsteps - 1) * S;
+    uint8_t* const slot = smem + (step % 3) * G::kSlot;
+    if (c < G::kXCopies) {
+      const int kib = c * G::kWaves + wave;  // 1 KiB: 64 / kChunks rows
+      const int row = kib * (64 / kChunks) + lane / kChunks;
+      const int chunk = (lane % kChunks) ^ row_swizzle<S>(row);
+      const int64_t m = min(tok0 + row, (int64_t)M - 1);
+      const int k = min(b * 32 + chunk * 8, s.H - 8);
+      dma16(x + m * s.H + k, lds_addr(slot + kib * 1024));
+    } else {
+      const int kib = (c - G::kXCopies) * G::kWaves + wave;  // [plane][subtile][block of the step]
+      const int j = kib % S, sub = kib / S % (BE / 16), q = kib / S / (BE / 16);
+      const int64_t at = ((int64_t)min(sub0 + sub, ns - 1) * kb + min(b + j, kb - 1)) * 1024;
+      dma16(prepared + q * plane + at + lane * 16, lds_addr(slot + G::kX + kib * 1024));
+    }
+  };
+  auto copies = [&](int step) {
+#pragma unroll
+    for (int c = 0; c < G::kCopies; ++c) copy(step, c);
+  };
+
+  f32x4_t acc[4][TT], chain[4][TT];
+  float sq[TT];
+#pragma unroll
+  for (int t = 0; t < TT; ++t) {
+    sq[t] = 0.0f;
+#pragma unroll
+    for (int f = 0; f < 4; ++f) acc[f][t] = chain[f][t] = f32x4_t{};
+  }
+  const bool norms = blockIdx.y == 0;
+  copies(0);
+  copies(1);
+  constexpr int kFlush = kChain / (S * NP) > 0 ? kChain / (S * NP) : 1;  // steps of a chain
+#pragma unroll 1
+  for (int step = 0; step < nsteps; ++step) {
+    vm_wait<G::kCopies>();  // this wave's copies of the step have landed, those of the next may not have
+    __syncthreads();        // everyone's have, and everyone is done with the step before
+    copies(step + 2);
+    const uint8_t* const slot = smem + (step % 3) * G::kSlot;
+    const int b = b0 + step * S;
+#pragma unroll
+    for (int j = 0; j < S; ++j) {
+      bf16x8_t bop[TT];
+      const bool in = b + j < b1 && (b + j) * 32 + g * 8 < s.H;
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        const int row = (wm * TT + t) * 16 + r;
+        uint4 v = *(const uint4*)(slot + row * G::kRow + ((4 * j + g) ^ row_swizzle<S>(row)) * 16);
+        if (!in) v = make_uint4(0, 0, 0, 0);
+        bop[t] = __builtin_bit_cast(bf16x8_t, v);
+        if (norms && t % G::WE == we) sq[t] = add_squares(bop[t], sq[t]);
+      }
+#pragma unroll
+      for (int q = 0; q < NP; ++q)
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+          const int kib = (q * (BE / 16) + we * 4 + f) * S + j;
+          const bf16x8_t a = __builtin_bit_cast(bf16x8_t, *(const uint4*)(slot + G::kX + kib * 1024 + lane * 16));
+#pragma unroll
+          for (int t = 0; t < TT; ++t)
+            chain[f][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, bop[t], chain[f][t], 0, 0, 0);
+        }
+    }
+    if (step % kFlush == kFlush - 1) {
+#pragma unroll
+      for (int f = 0; f < 4; ++f)
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          acc[f][t] += chain[f][t];
+          chain[f][t] = f32x4_t{};
+        }
+    }
+  }
+  vm_wait<0>();  // no copy may land after the workgroup's LDS is released
+#pragma unroll
+  for (int t = 0; t < TT; ++t) {
+    const int64_t m = tok0 + (wm * TT + t) * 16 + r;
+    if (m < M)
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        const int sub = sub0 + we * 4 + f;
+        if (sub < ns) *(f32x4_t*)(part + (split * M + m) * Ep + sub * 16 + 4 * g) = acc[f][t] + chain[f][t];
+      }
+    if (norms && t % G::WE == we) {
       float v = sq[t];
       v += __shfl_xor(v, 16);
       v += __shfl_xor(v, 32);
@@ -181,7 +375,7 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// ---- selection: one wave per token, lane l holds experts l + 64 i
+// ---- selection: one wave per token, lane l holds experts NI l .. NI l + NI - 1
 
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
@@ -220,9 +414,10 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k ^ ((uint32_t)((int32_t)~k >> 31) | 0x80000000u));
 }
 
-// Largest key of the wave (each lane's NI) and its lowest expert.
+// Largest key of the wave (each lane's NI) and its lowest expert: that of the
+// lowest lane, which holds the lowest experts.
 template <int NI>
-__device__ __forceinline__ uint32_t wave_best_key(const uint32_t (&key)[NI], int lane, int& e) {
+__device__ __forceinline__ uint32_t wave_best_key(const uint32_t (&key)[NI], int& e) {
   uint32_t v = key[0];
   int at = 0;
 #pragma unroll
@@ -232,13 +427,8 @@ __device__ __forceinline__ uint32_t wave_best_key(const uint32_t (&key)[NI], int
       at = i;
     }
   const uint32_t best = wave_max_u32(v);
-  const uint64_t owners = __ballot(v == best);
-  if (__popcll(owners) == 1) {
-    const int l = __ffsll((unsigned long long)owners) - 1;
-    e = __builtin_amdgcn_readlane(at, l) * 64 + l;
-  } else {
-    e = 0x7FFF - (int)wave_max_u32(v == best ? (uint32_t)(0x7FFF - (at * 64 + lane)) : 0u);
-  }
+  const int l = __ffsll((unsigned long long)__ballot(v == best)) - 1;
+  e = l * NI + __builtin_amdgcn_readlane(at, l);
   return best;
 }
 
@@ -270,22 +460,37 @@ __device__ __forceinline__ int renew(int v) {
   return v;
 }
 
-// Logit of expert e in 64 bits: products of bf16 values are exact.
+// Logit of expert e in 64 bits: products of bf16 values are exact.  Four
+// chunks of 8 values per lane are loaded before they are used.
 __device__ __forceinline__ double exact_logit(const RouterShape& s, const uint8_t* __restrict__ prepared,
                                               const uint16_t* __restrict__ xr, int e, int lane) {
-  const int kb = s.kblocks();
+  constexpr int kAhead = 4;
+  const int chunks = s.H / 8;
+  const uint8_t* const row = prepared + (int64_t)(e >> 4) * s.kblocks() * 1024 + (e & 15) * 16;
   double sum = 0.0;
-  for (int c = lane; c * 8 < s.H; c += 64) {
-    const uint4 xv = *(const uint4*)(xr + c * 8);
-    const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
-    const int64_t at = ((int64_t)(e >> 4) * kb + (c >> 2)) * 1024 + ((c & 3) * 16 + (e & 15)) * 16;
-    for (int q = 0; q < s.planes; ++q) {
-      const uint4 wv = *(const uint4*)(prepared + q * s.plane_bytes() + at);
-      const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
+#pragma unroll 1
+  for (int q = 0; q < s.planes; ++q) {
+#pragma unroll 1
+    for (int c0 = lane; c0 < chunks; c0 += 64 * kAhead) {
+      uint4 xv[kAhead], wv[kAhead];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        sum = fma((double)__uint_as_float(xw[j] << 16), (double)__uint_as_float(ww[j] << 16), sum);
-        sum = fma((double)__uint_as_float(xw[j] & 0xFFFF0000u), (double)__uint_as_float(ww[j] & 0xFFFF0000u), sum);
+      for (int i = 0; i < kAhead; ++i) {
+        const int c = c0 + 64 * i;
+        xv[i] = wv[i] = make_uint4(0, 0, 0, 0);
+        if (c < chunks) {
+          xv[i] = *(const uint4*)(xr + c * 8);
+          wv[i] = *(const uint4*)(row + q * s.plane_bytes() + c * 256);  // 16 rows of 16 bytes per chunk
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const uint32_t xw[4] = {xv[i].x, xv[i].y, xv[i].z, xv[i].w};
+        const uint32_t ww[4] = {wv[i].x, wv[i].y, wv[i].z, wv[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          sum = fma((double)__uint_as_float(xw[j] << 16), (double)__uint_as_float(ww[j] << 16), sum);
+          sum = fma((double)__uint_as_float(xw[j] & 0xFFFF0000u), (double)__uint_as_float(ww[j] & 0xFFFF0000u), sum);
+        }
       }
     }
   }
@@ -309,8 +514,7 @@ struct SelectLds {
   float *w, *logits;
 };
 
-// Recomputes the logits of the experts in `want` (bit i: this lane's expert
-// lane + 64 i).
+// Recomputes the logits of the experts in `want` (bit i: this lane's i-th).
 template <int NI>
 __device__ __forceinline__ void refine(const RouterShape& s, SelectLds<NI>& L, const uint8_t* __restrict__ prepared,
                                        const uint16_t* __restrict__ xr, uint32_t want, int lane) {
@@ -320,11 +524,26 @@ __device__ __forceinline__ void refine(const RouterShape& s, SelectLds<NI>& L, c
     while (todo) {
       const int l = __ffsll((unsigned long long)todo) - 1;
       todo &= todo - 1;
-      const double v = exact_logit(s, prepared, xr, l + 64 * i, lane);
-      if (lane == l) L.z[lane + 64 * i] = v;
+      const double v = exact_logit(s, prepared, xr, l * NI + i, lane);
+      if (lane == l) L.z[l * NI + i] = v;
     }
   }
   wave_sync();
+}
+
+// Sum of the two largest of L.t in group q, and the second of them; -inf
+// where fewer than two may be taken.
+template <int NI>
+__device__ __forceinline__ double group_top2(const SelectLds<NI>& L, int q, int size, double& second) {
+  double v1 = kNone, v2 = kNone;
+#pragma unroll 1
+  for (int c = 0; c < size; ++c) {
+    const double v = L.t[q * size + c];
+    v2 = fmax(v2, fmin(v1, v));
+    v1 = fmax(v1, v);
+  }
+  second = v2;
+  return v2 > kNone ? v1 + v2 : kNone;
 }
 
 // Which experts a token takes, best first, into L.taken; returns how many.
@@ -349,7 +568,7 @@ __device__ __forceinline__ int select_experts(const RouterShape& s, SelectLds<NI
     if (s.sigmoid) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) t[i] = 1.0f / (1.0f + expf(-z[i]));
-      err = 0.25f * bound;
+      err = 0.25f * bound + 0x1p-20f;  // scores are at most 1, with a few roundings of 2^-24 each
     } else {
       uint32_t key = 0;
 #pragma unroll
@@ -363,16 +582,16 @@ __device__ __forceinline__ int select_experts(const RouterShape& s, SelectLds<NI
       }
 #pragma unroll
       for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
+      const float top = 1.0f / sum;  // the largest score
 #pragma unroll
-      for (int i = 0; i < NI; ++i) t[i] /= sum;
-      err = 2.0f * bound;
+      for (int i = 0; i < NI; ++i) t[i] *= top;
+      err = (2.0f * bound + 0x1p-20f) * top;  // exp(z - zmax) / sum, each part within `bound` of itself
     }
-    err += 0x1p-20f;  // scores are at most 1, with a few roundings of 2^-24 each
     if (bias) {
       float most = 0.0f;
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const float b = lane + 64 * i < E ? bias[lane + 64 * i] : 0.0f;
+        const float b = lane * NI + i < E ? bias[lane * NI + i] : 0.0f;
         t[i] += b;
         if (fabsf(b) < __builtin_inff()) most = fmaxf(most, fabsf(b));
       }
@@ -383,11 +602,12 @@ __device__ __forceinline__ int select_experts(const RouterShape& s, SelectLds<NI
     for (int i = 0; i < NI; ++i) t[i] = z[i];
   }
   lane = renew(lane);
-  uint32_t key[NI], open = 0;
+  uint32_t key[NI], zk[NI], open = 0;
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
-    const bool in = lane + 64 * i < E;
+    const bool in = lane * NI + i < E;
     key[i] = in && t[i] > -__builtin_inff() ? order_key(t[i]) : 0u;  // not NaN
+    zk[i] = order_key(z[i]);
     if (in) open |= 1u << i;
   }
   // With a bias on a softmax a recomputed score still carries the other
@@ -395,15 +615,30 @@ __device__ __forceinline__ int select_experts(const RouterShape& s, SelectLds<NI
   // the sum is a common factor.)
   const bool whole = bias != nullptr && !s.sigmoid;
   bool all = !(bound < __builtin_inff());
+  // Passes: each recomputes what the one before found missing (all logits;
+  // the groups' largest; the unsure runs') and decides anew.
+  uint32_t want = all ? open : 0u;
+  bool have_groups = all, have_runs = all;
+  const int size = GROUPS ? E / s.groups : E;
+  const int lanes_per_group = GROUPS && size % NI == 0 && ((size / NI) & (size / NI - 1)) == 0 ? size / NI : 0;
+  int group[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) group[i] = GROUPS ? renew((lane * NI + i) / size & 63) : 0;
   int n = 0;
-  bool runs = false;
 
 #pragma unroll 1
   while (true) {
     lane = renew(lane);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {  // nothing derived from these is worth a register from pass to pass
+      key[i] = (uint32_t)renew((int)key[i]);
+      group[i] = renew(group[i]);
+      zk[i] = (uint32_t)renew((int)zk[i]);
+    }
+    if (bound != 0.0f) refine<NI>(s, L, prepared, xr, want, lane);  // logits of a zero row are exact
+    want = 0u;
     double total = 1.0;
     if (all) {
-      if (bound != 0.0f) refine<NI>(s, L, prepared, xr, open, lane);
       double mx = kNone, sum = 0.0;
 #pragma unroll 1
       for (int e = lane; e < E; e += 64) mx = fmax(mx, L.z[e]);
@@ -426,27 +661,41 @@ __device__ __forceinline__ int select_experts(const RouterShape& s, SelectLds<NI
     };
 
     uint64_t in_groups = ~0ull;
-    const int size = GROUPS ? E / s.groups : E;
     if constexpr (GROUPS) {
       float score = -__builtin_inff();  // lane q: that of group q
       uint32_t near = 0;                // could be among the two largest of their groups
+      if (lanes_per_group > 0) {        // groups of whole lanes, a power of two of them: all groups at once
+        uint32_t k1 = 0u, k2 = 0u;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          k2 = max(k2, min(k1, key[i]));
+          k1 = max(k1, key[i]);
+        }
 #pragma unroll 1
-      for (int q = 0; q < s.groups; ++q) {
-        lane = renew(lane);
-        uint32_t in[NI];
-#pragma unroll
-        for (int i = 0; i < NI; ++i) in[i] = (lane + 64 * i) / size == q ? key[i] : 0u;
-        int e1, e2;
-        const uint32_t k1 = wave_best_key<NI>(in, lane, e1);
-        uint32_t rest[NI];
-#pragma unroll
-        for (int i = 0; i < NI; ++i) rest[i] = lane + 64 * i == e1 ? 0u : in[i];
-        const uint32_t k2 = wave_best_key<NI>(rest, lane, e2);
-        if (lane == q && k2 != 0u) score = key_value(k1) + key_value(k2);
+        for (int d = 1; d < lanes_per_group; d <<= 1) {
+          const uint32_t o1 = (uint32_t)__shfl_xor((int)k1, d), o2 = (uint32_t)__shfl_xor((int)k2, d);
+          k2 = max(max(k2, o2), min(k1, o1));
+          k1 = max(k1, o1);
+        }
+        const float own = k2 != 0u ? key_value(k1) + key_value(k2) : -__builtin_inff();
+        score = __shfl(own, lane * lanes_per_group & 63);
         const float floor = k2 != 0u ? key_value(k2) - 2.0f * err : -__builtin_inff();
 #pragma unroll
         for (int i = 0; i < NI; ++i)
-          if (in[i] != 0u && !(key_value(in[i]) < floor)) near |= 1u << i;
+          if (key[i] != 0u && !(key_value(key[i]) < floor)) near |= 1u << i;
+      } else {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) L.t[lane * NI + i] = key[i] != 0u ? (double)key_value(key[i]) : kNone;
+        wave_sync();
+        double second;
+        const double both = group_top2<NI>(L, lane < s.groups ? lane : 0, size, second);
+        if (lane < s.groups) score = (float)both;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const float floor = (float)__shfl(second, group[i]) - 2.0f * err;
+          if (key[i] != 0u && !(key_value(key[i]) < floor)) near |= 1u << i;
+        }
+        wave_sync();
       }
       uint32_t gk[1] = {lane < s.groups ? (score == score ? order_key(score) : 1u) : 0u};
       float last = 0.0f, next = -__builtin_inff();
@@ -454,7 +703,7 @@ __device__ __forceinline__ int select_experts(const RouterShape& s, SelectLds<NI
 #pragma unroll 1
       for (int q = 0; q <= s.top_groups && q < s.groups; ++q) {
         int e;
-        const float v = key_value(wave_best_key<1>(gk, lane, e));
+        const float v = key_value(wave_best_key<1>(gk, e));
         if (q == s.top_groups) {
           next = v;
           break;
@@ -464,39 +713,29 @@ __device__ __forceinline__ int select_experts(const RouterShape& s, SelectLds<NI
         if (lane == e) gk[0] = 0u;
       }
       // two sums of two scores, and the sums' own roundings
-      if (all || (s.top_groups < s.groups &&
-                  !(last - next > 4.0f * err + 0x1p-22f * (fabsf(last) + fabsf(next))))) {
-        if (whole && !all) {
-          all = true;
+      const float apart = 4.0f * err + 0x1p-22f * (fabsf(last) + fabsf(next));
+      if (all || (s.top_groups < s.groups && !(last - next > apart))) {
+        // groups that are surely taken or surely left need no exact score
+        const bool in = !all && score - next > apart, out = !all && last - score > apart;
+        const uint64_t clear = __ballot(in || out);
+        if (all) near = open;
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+          if (clear >> group[i] & 1ull) near &= ~(1u << i);
+        if (!have_groups) {
+          have_groups = true;
+          all = whole;
+          have_runs = whole;
+          want = all ? open : near;
           continue;
         }
-        if (all) near = open;
-        if (!all && bound != 0.0f) refine<NI>(s, L, prepared, xr, near, lane);
 #pragma unroll 1
-        for (int i = 0; i < NI; ++i) {
-          const int e = lane + 64 * i;
-          L.t[e] = near >> i & 1u ? exact_score(e, true) : kNone;
-        }
+        for (int i = 0; i < NI; ++i)
+          L.t[lane * NI + i] = near >> i & 1u ? exact_score(lane * NI + i, true) : kNone;
         wave_sync();
-        double gs = kNone;
-#pragma unroll 1
-        for (int q = 0; q < s.groups; ++q) {
-          double v1 = kNone, v2 = kNone;
-          int e1 = kNobody, e2 = kNobody;
-          for (int e = q * size + lane; e < (q + 1) * size; e += 64)
-            if (L.t[e] > v1) {
-              v1 = L.t[e];
-              e1 = e;
-            }
-          wave_best(v1, e1);
-          for (int e = q * size + lane; e < (q + 1) * size; e += 64)
-            if (e != e1 && L.t[e] > v2) {
-              v2 = L.t[e];
-              e2 = e;
-            }
-          wave_best(v2, e2);
-          if (lane == q && e2 != kNobody) gs = v1 + v2;
-        }
+        double gs = in ? -kNone : kNone;
+        double second;
+        if (lane < s.groups && !in && !out) gs = group_top2<NI>(L, lane, size, second);
         in_groups = 0;
 #pragma unroll 1
         for (int q = 0; q < s.top_groups; ++q) {
@@ -513,20 +752,20 @@ __device__ __forceinline__ int select_experts(const RouterShape& s, SelectLds<NI
     // the list: key of expert e in the groups taken; within them, without a
     // bias, the order is that of the logits
     lane = renew(lane);
-    uint32_t left[NI];
+    uint32_t left[NI], may = 0;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      left[i] = GROUPS && !(in_groups >> ((lane + 64 * i) / size & 63) & 1ull) ? 0u : key[i];
-      if (!bias && left[i] != 0u) left[i] = order_key(z[i]);
+      if (!GROUPS || (in_groups >> group[i] & 1ull)) may |= 1u << i;
+      left[i] = may >> i & 1u ? key[i] : 0u;
+      if (!bias && left[i] != 0u) left[i] = zk[i];
     }
     n = 0;
-    runs = all;
+    bool runs = all;
     if (all) {  // one run of all that may be taken, in any order
 #pragma unroll 1
       for (int i = 0; i < NI; ++i) {
-        const int e = lane + 64 * i;
-        const bool in = e < E && (!GROUPS || (in_groups >> (e / size & 63) & 1ull)) &&
-                        exact_score(e, false) > kNone;
+        const int e = lane * NI + i;
+        const bool in = e < E && (may >> i & 1u) && exact_score(e, false) > kNone;
         const uint64_t who = __ballot(in);
         if (in) {
           const int at = n + __popcll(who & ((1ull << lane) - 1ull));
@@ -543,7 +782,7 @@ __device__ __forceinline__ int select_experts(const RouterShape& s, SelectLds<NI
       while (true) {
         lane = renew(lane);
         int e;
-        const uint32_t best = wave_best_key<NI>(left, lane, e);
+        const uint32_t best = wave_best_key<NI>(left, e);
         if (best == 0u) break;
         const float v = key_value(best);
         const bool unsure = n > 0 && apart > 0.0f && !(prev - v > apart);
@@ -556,28 +795,28 @@ __device__ __forceinline__ int select_experts(const RouterShape& s, SelectLds<NI
         }
 #pragma unroll
         for (int i = 0; i < NI; ++i)
-          if (lane + 64 * i == e) left[i] = 0u;
+          if (lane * NI + i == e) left[i] = 0u;
         prev = v;
         ++n;
       }
     }
     wave_sync();
-    if (runs && whole && !all) {
-      all = true;
-      continue;
-    }
 
     if (!runs) {
       if (lane < n) L.taken[lane] = L.e[lane];
     } else {
-      if (!all && bound != 0.0f) {
-        uint32_t want = 0;
+      if (!have_runs) {
+        have_runs = true;
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
           const int e = L.e[j], r = L.run[j];
-          if (e % 64 == lane && (r != j || (j + 1 < n && L.run[j + 1] == r))) want |= 1u << (e / 64);
+          if (e / NI == lane && (r != j || (j + 1 < n && L.run[j + 1] == r))) want |= 1u << (e % NI);
         }
-        refine<NI>(s, L, prepared, xr, want, lane);
+        if (whole) {
+          all = true;
+          want = open;
+        }
+        continue;
       }
 #pragma unroll 1
       for (int j = lane; j < n; j += 64) L.t[j] = exact_score(L.e[j], false);
@@ -610,26 +849,24 @@ __global__ void __launch_bounds__(256)
   const int E = s.E, Ep = 16 * s.subtiles(), k = s.k;
   const float* const norms = (const float*)(prepared + s.norms_offset());
 
-  float z[NI];
+  typedef float vec_t __attribute__((ext_vector_type(NI)));
+  vec_t zv = {};
   uint32_t wn = 0;
 #pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    z[i] = 0.0f;
-    if (lane + 64 * i < E) wn = max(wn, __float_as_uint(norms[lane + 64 * i]));  // norms are not negative
-  }
+  for (int i = 0; i < NI; ++i)
+    if (lane * NI + i < E) wn = max(wn, __float_as_uint(norms[lane * NI + i]));  // norms are not negative
   float x2 = 0.0f;
-  const float* p0 = part + m * Ep + lane;
-#pragma unroll 4
+  const float* p0 = part + m * Ep + lane * NI;  // a lane's experts are all below Ep (a multiple of 16) or none is
+#pragma unroll 8
   for (int q = 0; q < splits; ++q) {
     x2 += xx[(int64_t)q * M + m];  // of 2^32 x
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
-      if (lane + 64 * i < E) z[i] += p0[(int64_t)q * M * Ep + 64 * i];
+    if (lane * NI < Ep) zv += *(const vec_t*)(p0 + (int64_t)q * M * Ep);
   }
+  float z[NI];
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
-    if (lane + 64 * i >= E) z[i] = -__builtin_inff();
-    L.z[lane + 64 * i] = (double)z[i];
+    z[i] = lane * NI + i < E ? zv[i] : -__builtin_inff();
+    L.z[lane * NI + i] = (double)z[i];
   }
   if (lane == 0) {
     L.ids = ids + m * k;
@@ -656,7 +893,7 @@ __global__ void __launch_bounds__(256)
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < NI; ++i)
-        if (lane + 64 * i < E) sum += expf((float)(L.z[lane + 64 * i] - mx));
+        if (lane * NI + i < E) sum += expf((float)(L.z[lane * NI + i] - mx));
 #pragma unroll
       for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
       p /= (double)sum;
@@ -674,7 +911,7 @@ __global__ void __launch_bounds__(256)
   if (lo)
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int e = lane + 64 * i;
+      const int e = lane * NI + i;
       if (e < E) lo[e] = (float)L.z[e];
     }
 }
@@ -713,28 +950,43 @@ hipError_t launch_route(const RouterShape& s, const uint8_t* prepared, const uin
   const LogitPlan p = logit_plan(s, M);
   float* const part = (float*)ws;
   float* const xx = part + (int64_t)p.splits * M * 16 * s.subtiles();
-  const dim3 grid((unsigned)((M + 16 * p.tt - 1) / (16 * p.tt)), (unsigned)((s.E + 127) / 128), (unsigned)p.splits);
-#define MOE_LOGITS(TT, NP) \
-  hipLaunchKernelGGL((route_logits_kernel<TT, NP>), grid, dim3(256), 0, st, s, prepared, x, M, p.per, part, xx)
-  if (s.planes == 3) {
-    if (p.tt == 1) MOE_LOGITS(1, 3);
-    else if (p.tt == 2) MOE_LOGITS(2, 3);
-    else MOE_LOGITS(4, 3);
+  if (p.gemm) {
+    const dim3 grid((unsigned)((M + p.bm - 1) / p.bm), (unsigned)((s.E + p.be - 1) / p.be), (unsigned)p.splits);
+    if (s.planes == 3)
+      hipLaunchKernelGGL((route_gemm_kernel<128, 128, 3>), grid, dim3(512), (RouteGemm<128, 128, 3>::kLds), st, s,
+                         prepared, x, M, p.per, part, xx);
+    else if (p.be == 256)
+      hipLaunchKernelGGL((route_gemm_kernel<128, 256, 1>), grid, dim3(512), (RouteGemm<128, 256, 1>::kLds), st, s,
+                         prepared, x, M, p.per, part, xx);
+    else
+      hipLaunchKernelGGL((route_gemm_kernel<64, 128, 1>), grid, dim3(512), (RouteGemm<64, 128, 1>::kLds), st, s,
+                         prepared, x, M, p.per, part, xx);
   } else {
-    if (p.tt == 1) MOE_LOGITS(1, 1);
-    else if (p.tt == 2) MOE_LOGITS(2, 1);
-    else MOE_LOGITS(4, 1);
-  }
+    const dim3 grid((unsigned)s.subtiles(), (unsigned)p.splits, (unsigned)((M + 16 * p.tt - 1) / (16 * p.tt)));
+#define MOE_LOGITS(TT, NP) \
+  hipLaunchKernelGGL((route_few_kernel<TT, NP>), grid, dim3(256), 0, st, s, prepared, x, M, p.per, part, xx)
+    if (s.planes == 3) {
+      if (p.tt == 1) MOE_LOGITS(1, 3);
+      else if (p.tt == 2) MOE_LOGITS(2, 3);
+      else MOE_LOGITS(4, 3);
+    } else {
+      if (p.tt == 1) MOE_LOGITS(1, 1);
+      else if (p.tt == 2) MOE_LOGITS(2, 1);
+      else MOE_LOGITS(4, 1);
+    }
 #undef MOE_LOGITS
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const dim3 sgrid((unsigned)((M + 3) / 4));
-  // Error bound of a logit, over ||x|| ||w||.  A matrix instruction adds 32
-  // products to its accumulator C with an error of at most 2^-22 (|C| + the
-  // sum of their magnitudes); a slice has `per` of them for each plane, C is
-  // at most the magnitudes so far, and sum |x w| <= ||x|| ||w||.  The slices
-  // are then added in fp32.
-  const float coef = (float)((0.5 * p.per * s.planes + 1.0) * 0x1p-22 + p.splits * 0x1p-24);
+  // Error bound of a logit, over ||x|| ||w||, which is at least the sum A of
+  // the magnitudes |x w|.  v_mfma_f32_16x16x32_bf16 adds its 32 products in
+  // four groups of 8 (measured): within a group they are cut to multiples of
+  // 2^-24 of the largest's power of two (at most 7 * 2^-24 of the group's
+  // magnitudes), and each group's sum is added to the accumulator C, at most
+  // the magnitudes of its chain of kChain instructions, with one rounding.
+  // The chains, the waves' sums and the slices are added in fp32.
+  const float coef = (float)((4.0 * kChain + 8.0 + (p.per * s.planes / (kChain / 2) + 4.0) + p.splits) * 0x1p-24);
 #define MOE_SELECT_G(NI, G)                                                                                         \
   hipLaunchKernelGGL((route_select_kernel<NI, G>), sgrid, dim3(256), 0, st, s, prepared, x, M, p.splits, coef, part, \
                      xx, bias, ids, w, logits)

@@ -80,6 +80,11 @@ ROUTES = [
     (200, 2048, 384, 6, "fp32", "softmax", False, 64, 3, False, 0.5),
     (300, 328, 512, 8, "bf16", "sigmoid", True, 16, 1, False, 1.0),
     (1500, 520, 256, 8, "bf16", "sigmoid", True, 8, 4, True, 1.5),
+    (257, 776, 96, 8, "bf16", "softmax", False, 1, 1, True, 1.0),
+    (700, 1000, 100, 4, "fp32", "softmax", False, 1, 1, False, 1.0),
+    (1000, 72, 300, 8, "fp32", "sigmoid", True, 1, 1, True, 1.0),
+    (2000, 1096, 64, 2, "bf16", "softmax", True, 1, 1, True, 1.0),
+    (1025, 40, 512, 5, "bf16", "sigmoid", False, 8, 2, True, 1.0),
 ]
 
 
