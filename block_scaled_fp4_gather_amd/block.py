@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 
 import torch
 
@@ -126,13 +127,20 @@ def fp8_workspace_bytes(desc: Fp8Desc, M: int) -> int:
     return _sized("moe_fp4_fp8_workspace_bytes", desc.c(), M)
 
 
-def _need(t: torch.Tensor, what: str, dtype, shape, device=None) -> int:
+# A call of a few tokens takes about as long on the host as on the GPU, so the
+# checks below look things up by index (the current stream's address and the
+# current device) instead of through objects made for each call.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
+def _need(t: torch.Tensor, what: str, dtype, shape, index: int) -> int:
     """Address of a dense tensor after checking its type, shape and device."""
     if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what}: want contiguous {dtype} {list(shape)}, "
                          f"got {'' if t.is_contiguous() else 'strided '}{t.dtype} {list(t.shape)}")
-    if t.device.type != "cuda" or (device is not None and t.device != device):
-        raise ValueError(f"{what} is on {t.device}, not on {device or 'a GPU'}")
+    if t.get_device() != index or not t.is_cuda:
+        raise ValueError(f"{what} is on {t.device}, not on {'a GPU' if index < 0 else f'cuda:{index}'}")
     return t.data_ptr()
 
 
@@ -151,17 +159,17 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _on(device, stream, name: str, call, tensors):
-    """call(stream address) with `device` current, which launches go by.
-    `tensors` are kept until an explicitly given stream is past the call."""
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    if torch.cuda.current_device() == device.index:
-        status = call(s.cuda_stream)
+def _launch(index: int, stream, fn, args, tensors) -> None:
+    """fn(*args, stream address) with device `index` current, which launches go
+    by.  `tensors` are kept until an explicitly given stream is past the call."""
+    s = _raw_stream(index) if stream is None else stream.cuda_stream
+    if _current_device() == index:
+        status = fn(*args, s)
     else:
-        with torch.cuda.device(device):
-            status = call(s.cuda_stream)
+        with torch.cuda.device(index):
+            status = fn(*args, s)
     if status != 0:
-        moe.check(name, status)
+        moe.check(fn.__name__, status)
     if stream is not None:
         for t in tensors:
             if t is not None:
@@ -188,33 +196,33 @@ class Router:
         if weight.dtype is not dtype:
             raise ValueError(f"router weights are {weight.dtype}, the descriptor says {dtype}")
         weight = weight.to(dev).contiguous()
-        at = _need(weight, "weight", dtype, (desc.E, desc.H))
+        at = _need(weight, "weight", dtype, (desc.E, desc.H), dev.index)
         self.bias = None if bias is None else bias.to(device=dev, dtype=torch.float32).contiguous()
-        self._bias_at = None if bias is None else _need(self.bias, "bias", torch.float32, (desc.E,))
+        self._bias_at = None if bias is None else _need(self.bias, "bias", torch.float32, (desc.E,), dev.index)
         self.prepared = torch.empty(router_prepared_bytes(desc), dtype=torch.uint8, device=dev)
         self.workspace = torch.empty(router_workspace_bytes(desc, desc.max_tokens), dtype=torch.uint8, device=dev)
         self._at = self.prepared.data_ptr(), self.workspace.data_ptr(), self.workspace.numel()
-        _on(dev, stream, "moe_fp4_router_prepare", lambda s: moe.lib().moe_fp4_router_prepare(
-            self._ref, at, self._at[0], self.prepared.numel(), s), (weight, self.prepared))
+        _launch(dev.index, stream, moe.lib().moe_fp4_router_prepare,
+                (self._ref, at, self._at[0], self.prepared.numel()), (weight, self.prepared))
         self._route = moe.lib().moe_fp4_route
 
     def __call__(self, x, ids=None, w=None, logits=None, stream=None):
         """ids int32 [M][k] and w fp32 [M][k] of x bf16 [M][H]; fills `logits`
         fp32 [M][E] if given."""
         d, dev = self.desc, self.device
+        at = dev.index
         M = x.shape[0]
-        stream = _stream(stream, dev)
+        if stream is not None:
+            stream = _stream(stream, dev)
         if ids is None:
             ids = _empty((M, d.k), torch.int32, dev, stream)
         if w is None:
             w = _empty((M, d.k), torch.float32, dev, stream)
-        xa = _need(x, "x", torch.bfloat16, (M, d.H), dev)
-        ia = _need(ids, "ids", torch.int32, (M, d.k), dev)
-        wa = _need(w, "w", torch.float32, (M, d.k), dev)
-        la = None if logits is None else _need(logits, "logits", torch.float32, (M, d.E), dev)
         pa, sa, sn = self._at
-        _on(dev, stream, "moe_fp4_route",
-            lambda s: self._route(self._ref, pa, xa, M, self._bias_at, ia, wa, la, sa, sn, s),
+        _launch(at, stream, self._route, (
+            self._ref, pa, _need(x, "x", torch.bfloat16, (M, d.H), at), M, self._bias_at,
+            _need(ids, "ids", torch.int32, (M, d.k), at), _need(w, "w", torch.float32, (M, d.k), at),
+            None if logits is None else _need(logits, "logits", torch.float32, (M, d.E), at), sa, sn),
             (x, ids, w, logits, self.bias, self.prepared, self.workspace))
         return ids, w
 
@@ -233,28 +241,34 @@ class Fp8Linear:
         if codes.dtype is torch.float8_e4m3fn:
             codes = codes.view(torch.uint8)
         codes, scales = codes.to(dev).contiguous(), scales.to(dev).contiguous()
-        ca = _need(codes, "codes", torch.uint8, (desc.rows, desc.K))
-        sa = _need(scales, "scales", torch.float32, (halves * (-(-desc.N // 128)), -(-desc.K // 128)))
+        ca = _need(codes, "codes", torch.uint8, (desc.rows, desc.K), dev.index)
+        sa = _need(scales, "scales", torch.float32, (halves * (-(-desc.N // 128)), -(-desc.K // 128)), dev.index)
         self.prepared = torch.empty(fp8_prepared_bytes(desc), dtype=torch.uint8, device=dev)
         self.workspace = torch.empty(fp8_workspace_bytes(desc, desc.max_tokens), dtype=torch.uint8, device=dev)
         self._at = self.prepared.data_ptr(), self.workspace.data_ptr(), self.workspace.numel()
-        _on(dev, stream, "moe_fp4_fp8_prepare", lambda s: moe.lib().moe_fp4_fp8_prepare(
-            self._ref, ca, sa, self._at[0], self.prepared.numel(), s), (codes, scales, self.prepared))
+        _launch(dev.index, stream, moe.lib().moe_fp4_fp8_prepare,
+                (self._ref, ca, sa, self._at[0], self.prepared.numel()), (codes, scales, self.prepared))
         self._linear = moe.lib().moe_fp4_fp8_linear
 
     def __call__(self, x, out=None, stream=None):
         """bf16 [M][N] of x bf16 [M][K]."""
         d, dev = self.desc, self.device
+        at = dev.index
         M = x.shape[0]
-        stream = _stream(stream, dev)
+        if stream is not None:
+            stream = _stream(stream, dev)
         if out is None:
             out = _empty((M, d.N), torch.bfloat16, dev, stream)
-        xa = _need(x, "x", torch.bfloat16, (M, d.K), dev)
-        oa = _need(out, "out", torch.bfloat16, (M, d.N), dev)
         pa, sa, sn = self._at
-        _on(dev, stream, "moe_fp4_fp8_linear", lambda s: self._linear(self._ref, pa, xa, M, oa, sa, sn, s),
-            (x, out, self.prepared, self.workspace))
+        _launch(at, stream, self._linear, (
+            self._ref, pa, _need(x, "x", torch.bfloat16, (M, d.K), at), M,
+            _need(out, "out", torch.bfloat16, (M, d.N), at), sa, sn), (x, out, self.prepared, self.workspace))
         return out
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_desc(*fields):
+    return ctypes.byref(_NormDesc(*fields))
 
 
 def block_norm(h, y=None, y2=None, *, gate=None, post_weight=None, pre_weight=None, eps=1e-6, residual_scale=1.0,
@@ -267,15 +281,15 @@ def block_norm(h, y=None, y2=None, *, gate=None, post_weight=None, pre_weight=No
     new residual (None without y) and the normed hidden states (None without
     pre_weight).  h_out may be h."""
     M, H = h.shape
-    dev = h.device
-    stream = _stream(stream, dev)
-    typed = [t for t in (post_weight, pre_weight, gate) if t is not None]
-    wt = typed[0].dtype if typed else torch.bfloat16
+    dev, at = h.device, h.get_device()
+    if stream is not None:
+        stream = _stream(stream, dev)
+    wt = next((t.dtype for t in (pre_weight, post_weight, gate) if t is not None), torch.bfloat16)
     if h.dtype not in _TORCH_TYPES or wt not in _TORCH_TYPES:
         raise ValueError(f"block_norm takes bf16 and fp32, got {h.dtype} and {wt}")
-    kind = GATE_NONE
+    kind, shape = GATE_NONE, None
     if gate is not None:
-        shape = tuple(gate.shape)
+        shape = gate.shape
         if shape == (H,):
             kind = GATE_CHANNEL
         elif shape == (M, H):
@@ -284,22 +298,23 @@ def block_norm(h, y=None, y2=None, *, gate=None, post_weight=None, pre_weight=No
             kind = GATE_TOKEN
         else:
             raise ValueError(f"gate {list(shape)}: want [{H}], [{M}, 1] or [{M}, {H}]")
+    rows = (M, H)
     if y is not None and h_out is None:
-        h_out = _empty((M, H), h.dtype, dev, stream)
+        h_out = _empty(rows, h.dtype, dev, stream)
     if pre_weight is not None and x_out is None:
-        x_out = _empty((M, H), torch.bfloat16, dev, stream)
-
-    def at(t, what, dtype, shape):
-        return None if t is None else _need(t, what, dtype, shape, dev)
-
-    args = (_need(h, "h", h.dtype, (M, H), dev), at(y, "y", torch.bfloat16, (M, H)),
-            at(y2, "y2", torch.bfloat16, (M, H)), at(gate, "gate", wt, gate.shape if gate is not None else None),
-            at(post_weight, "post_weight", wt, (H,)), at(pre_weight, "pre_weight", wt, (H,)),
-            at(h_out, "h_out", h.dtype, (M, H)), at(x_out, "x_out", torch.bfloat16, (M, H)))
-    c = _NormDesc(H, _TORCH_TYPES[h.dtype], _TORCH_TYPES[wt], kind, int(gate_sigmoid), eps, residual_scale,
-                  branch_scale, weight_offset)
-    fn = moe.lib().moe_fp4_block_norm
-    _on(dev, stream, "moe_fp4_block_norm", lambda s: fn(ctypes.byref(c), M, *args, s),
+        x_out = _empty(rows, torch.bfloat16, dev, stream)
+    bf16 = torch.bfloat16
+    _launch(at, stream, moe.lib().moe_fp4_block_norm, (
+        _norm_desc(H, _TORCH_TYPES[h.dtype], _TORCH_TYPES[wt], kind, int(gate_sigmoid), eps, residual_scale,
+                   branch_scale, weight_offset), M,
+        _need(h, "h", h.dtype, rows, at),
+        None if y is None else _need(y, "y", bf16, rows, at),
+        None if y2 is None else _need(y2, "y2", bf16, rows, at),
+        None if gate is None else _need(gate, "gate", wt, shape, at),
+        None if post_weight is None else _need(post_weight, "post_weight", wt, (H,), at),
+        None if pre_weight is None else _need(pre_weight, "pre_weight", wt, (H,), at),
+        None if h_out is None else _need(h_out, "h_out", h.dtype, rows, at),
+        None if x_out is None else _need(x_out, "x_out", bf16, rows, at)),
         (h, y, y2, gate, post_weight, pre_weight, h_out, x_out))
     return h_out, x_out
 
