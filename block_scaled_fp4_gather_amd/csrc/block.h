@@ -70,12 +70,12 @@ struct Fp8Shape {
   MOE_HD int64_t codes_bytes() const { return (int64_t)subtiles() * kblocks() * 2048; }
   MOE_HD int64_t prepared_bytes() const { return align256(codes_bytes() + 4ll * subtiles() * kblocks()); }
   // quantised activations: codes [M][128 kblocks], then one scale byte per
-  // row and K block, rows of whole dwords
-  MOE_HD int scale_row() const { return (kblocks() + 3) / 4 * 4; }
+  // row and K block, as dwords of 4 K blocks: [kblocks / 4][scale_rows]
+  MOE_HD int64_t scale_rows(int64_t M) const { return (M + 255) / 256 * 256; }
   MOE_HD int64_t code_bytes(int64_t M) const { return align256(M * kblocks() * 128); }
   MOE_HD int64_t workspace(int64_t max_tokens) const {
     const int64_t M = max_tokens < 1 ? 1 : max_tokens;
-    return code_bytes(M) + align256(M * scale_row());
+    return code_bytes(M) + (kblocks() + 3) / 4 * 4 * scale_rows(M);
   }
 };
 

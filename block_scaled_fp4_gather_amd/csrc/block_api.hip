@@ -59,7 +59,7 @@ moe_fp4_status fp8_shape(const moe_fp4_fp8_desc* d, moe::Fp8Shape* s) {
   if (d->act_fn == MOE_FP4_FN_SWIGLUOAI &&
       (!std::isfinite(d->act_alpha) || !std::isfinite(d->act_beta) || !(d->act_limit > 0.0f)))
     return MOE_FP4_EINVAL;
-  if ((int64_t)d->in_features * d->out_features > (int64_t)1 << 30 || d->max_tokens > kMaxTokens)
+  if (d->in_features > 1 << 20 || (int64_t)d->in_features * d->out_features > (int64_t)1 << 30 || d->max_tokens > kMaxTokens)
     return MOE_FP4_EUNSUPPORTED;
   const bool act = d->act_fn != MOE_FP4_FN_NONE;
   *s = moe::Fp8Shape{d->in_features, d->out_features, act && d->act_fn != MOE_FP4_FN_RELU2,

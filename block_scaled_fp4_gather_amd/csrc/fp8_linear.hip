@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(256)
 
 __global__ void __launch_bounds__(256)
     fp8_quantize_rows(const uint16_t* __restrict__ x, int64_t items, int K, int kb, uint8_t* __restrict__ codes,
-                      uint8_t* __restrict__ scales, int sstride) {
+                      uint8_t* __restrict__ scales, int64_t rows) {
   const int64_t stride = (int64_t)gridDim.x * blockDim.x;
   // items is a multiple of 16 and so is the stride: a block's lanes stay together
   for (int64_t it = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; it < items; it += stride) {
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(256)
       }
     }
     *(uint2*)(codes + it * 8) = make_uint2(lo, hi);
-    if ((c & 15) == 0) scales[row * sstride + (c >> 4)] = (uint8_t)sb;
+    if ((c & 15) == 0) scales[((c >> 6) * rows + row) * 4 + ((c >> 4) & 3)] = (uint8_t)sb;
   }
 }
 
@@ -124,7 +124,8 @@ __global__ void __launch_bounds__(NW * 64)
                     const uint8_t* __restrict__ xscale, int M, uint16_t* __restrict__ out) {
   __shared__ f32x4_t part[NW][FS * TT][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int kb = s.kblocks(), ns = s.subtiles(), srow = s.scale_row();
+  const int kb = s.kblocks(), ns = s.subtiles();
+  const int64_t mp = s.scale_rows(M);
   const int sub0 = blockIdx.x * FS;
   const int64_t tok0 = (int64_t)blockIdx.y * (16 * TT);
   const int r = lane & 15, g = lane >> 4;
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(NW * 64)
   for (int t = 0; t < TT; ++t) {
     const int64_t m = min(tok0 + 16 * t + r, (int64_t)M - 1);  // rows past M repeat the last one and are not stored
     xrow[t] = codes + m * kb * 128 + g * 16;
-    srows[t] = xscale + m * srow;
+    srows[t] = xscale + m * 4;
   }
   for (int b = wave; b < kb; b += NW) {
     i32x8_t bop[TT];
@@ -149,7 +150,7 @@ __global__ void __launch_bounds__(NW * 64)
     for (int t = 0; t < TT; ++t) {
       const i32x4_t lo = *(const i32x4_t*)(xrow[t] + b * 128), hi = *(const i32x4_t*)(xrow[t] + b * 128 + 64);
       bop[t] = i32x8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-      sx[t] = srows[t][b];
+      sx[t] = srows[t][(b >> 2) * mp * 4 + (b & 3)];
     }
 #pragma unroll
     for (int f = 0; f < FS; ++f) {
@@ -191,6 +192,188 @@ __global__ void __launch_bounds__(NW * 64)
   }
 }
 
+// ---- many tokens: BM tokens x BN weight rows per workgroup of 8 waves
+// (WT x WF), one K block per step.  Tokens go to LDS by direct copies (a row
+// of 128 codes: the 16-byte chunk c of row r at position c ^ a_swz(r)), the
+// weights, which only two or four waves share, straight to registers in the
+// layout they were prepared in; both one step ahead, and a step of the large
+// tile takes about as long as the copies (1024 matrix-unit cycles for each of
+// a SIMD's two waves).  Every 4 steps the scale dwords of the tokens' next 4
+// K blocks follow.
+template <int BM, int BN, int WT, int WF>
+struct Fp8Tile {
+  static constexpr int FS = BN / 16 / WF, TT = BM / 16 / WT;
+  static constexpr int kSlot = BM * 128;
+  static constexpr int kCopies = kSlot / 1024 / 8;
+  static constexpr int kLds = 2 * kSlot + 2 * 4 * BM;
+  static_assert(WT * WF == 8 && FS % 2 == 0 && BM % 64 == 0, "8 waves, whole gate and up pairs, whole copies");
+};
+
+template <int BM, int BN, int WT, int WF, bool GATED>
+__global__ void __launch_bounds__(512, 2)
+    fp8_tile_kernel(Fp8Shape s, const uint8_t* __restrict__ prepared, const uint8_t* __restrict__ codes,
+                    const uint8_t* __restrict__ xscale, int M, int tiles_m, int tiles_n, uint16_t* __restrict__ out) {
+  using T = Fp8Tile<BM, BN, WT, WF>;
+  constexpr int FS = T::FS, TT = T::TT;
+  extern __shared__ __align__(16) uint8_t smem[];
+  uint8_t* const sring = smem + 2 * T::kSlot;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  // Workgroups are dealt to the 8 XCDs in turn: give each XCD a contiguous
+  // range of tiles, in bands of 4 token tiles, so that what runs together on
+  // it shares token and weight tiles in its L2.
+  const int per = gridDim.x / 8;
+  const int logical = (blockIdx.x % 8) * per + blockIdx.x / 8;
+  if (logical >= tiles_m * tiles_n) return;
+  const int band = logical / (4 * tiles_n), in_band = logical - band * 4 * tiles_n;
+  const int bm = min(4, tiles_m - 4 * band);
+  const int tn = in_band / bm, tm = 4 * band + in_band % bm;
+
+  const int kb = s.kblocks(), ns = s.subtiles();
+  const int64_t mp = s.scale_rows(M), tok0 = (int64_t)tm * BM;
+  const int wf = wave % WF, wt = wave / WF;
+  const int sub0 = tn * (BN / 16) + wf * FS;
+  const float* const ws = (const float*)(prepared + s.codes_bytes());
+
+  // token copies of this wave: rows of the tile past the last token repeat it
+  const uint8_t* const tile = codes + tok0 * kb * 128;
+  const int rows = (int)min((int64_t)M - tok0, (int64_t)BM);
+  uint32_t src[T::kCopies];  // at most 255 rows of 2^20 bytes
+#pragma unroll
+  for (int c = 0; c < T::kCopies; ++c) {
+    const int row = (c * 8 + wave) * 8 + lane / 8;
+    src[c] = (uint32_t)min(row, rows - 1) * (kb * 128u) + ((lane & 7) ^ a_swz(row)) * 16;
+  }
+  auto copy_tokens = [&](int b, int ring) {
+#pragma unroll
+    for (int c = 0; c < T::kCopies; ++c)
+      dma16_at(tile + (int64_t)b * 128, src[c], lds_addr(smem + ring * T::kSlot + (c * 8 + wave) * 1024));
+  };
+  auto copy_scales = [&](int q) {  // scale dwords of K blocks 4q..; the scale rows are padded to whole tiles
+    if (wave * 64 < BM)
+      dma4(xscale + (q * mp + tok0 + wave * 64 + lane) * 4, lds_addr(sring + (q & 1) * 4 * BM + wave * 256));
+  };
+  const uint8_t* wsrc[FS];
+#pragma unroll
+  for (int f = 0; f < FS; ++f) wsrc[f] = prepared + (int64_t)min(sub0 + f, ns - 1) * kb * 2048;
+  const float* const wscale = ws + (int64_t)min(sub0 + lane % FS, ns - 1) * kb;
+  auto load_weights = [&](int b, i32x8_t (&a)[FS], float& w) {
+#pragma unroll
+    for (int f = 0; f < FS; ++f) {
+      const uint8_t* const at = wsrc[f] + (int64_t)b * 2048;
+      const i32x4_t lo = *(const i32x4_t*)(at + (uint32_t)lane * 16);
+      const i32x4_t hi = *(const i32x4_t*)(at + (uint32_t)lane * 16 + 1024);
+      a[f] = i32x8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    }
+    w = wscale[b];
+  };
+
+  f32x4_t acc[FS][TT];
+#pragma unroll
+  for (int f = 0; f < FS; ++f)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) acc[f][t] = f32x4_t{};
+
+  const int swz = a_swz(r);  // the same for every 16th row: rows 16 t + r
+  const int brow = (wt * TT * 16 + r) * 128, bs = (wt * TT * 16 + r) * 4;
+  auto step = [&](int b, i32x8_t (&a)[FS], const float w, i32x8_t (&an)[FS], float& wn) {
+    vm_wait<0>();     // this wave's copies and loads for step b are here
+    __syncthreads();  // everyone's are, and everyone is done with step b - 1
+    const int next = min(b + 1, kb - 1);  // past the last block it is loaded again, and not used
+    copy_tokens(next, (b + 1) & 1);
+    if ((b & 3) == 0 && b + 4 < kb) copy_scales((b >> 2) + 1);
+    load_weights(next, an, wn);
+    __builtin_amdgcn_sched_barrier(0);
+    float wf_[FS];
+#pragma unroll
+    for (int f = 0; f < FS; ++f) wf_[f] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), f));
+    const uint8_t* const slot = smem + (b & 1) * T::kSlot + brow;
+    const uint8_t* const sc = sring + ((b >> 2) & 1) * 4 * BM + bs + (b & 3);
+    // One token tile at a time, the next one's operand read ahead: left alone,
+    // the compiler keeps so many tiles in flight that registers spill.  The
+    // other wave of the SIMD fills the matrix unit during the multiply-adds.
+    auto read = [&](int t, i32x8_t& bop, int& sx) {
+      const i32x4_t lo = *(const i32x4_t*)(slot + t * 2048 + (g ^ swz) * 16);
+      const i32x4_t hi = *(const i32x4_t*)(slot + t * 2048 + ((4 + g) ^ swz) * 16);
+      bop = i32x8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      sx = sc[t * 64];
+    };
+    i32x8_t bop[2];
+    int sx[2];
+    read(0, bop[0], sx[0]);
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      if (t + 1 < TT) read(t + 1, bop[(t + 1) & 1], sx[(t + 1) & 1]);
+      f32x4_t p[FS];
+#pragma unroll
+      for (int f = 0; f < FS; ++f)
+        p[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[f], bop[t & 1], f32x4_t{}, 0, 0, 0, 127, 0,
+                                                               sx[t & 1]);
+#pragma unroll
+      for (int f = 0; f < FS; ++f)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[f][t][i] = fmaf(wf_[f], p[f][i], acc[f][t][i]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  i32x8_t a0[FS], a1[FS];
+  float w0, w1;
+  copy_tokens(0, 0);
+  copy_scales(0);
+  load_weights(0, a0, w0);
+  int b = 0;
+  for (; b + 1 < kb; b += 2) {
+    step(b, a0, w0, a1, w1);
+    step(b + 1, a1, w1, a0, w0);
+  }
+  if (b < kb) step(b, a0, w0, a1, w1);
+  vm_wait<0>();  // no copy may land after the workgroup's LDS is released
+
+#pragma unroll
+  for (int t = 0; t < TT; ++t) {
+    const int64_t m = tok0 + (wt * TT + t) * 16 + r;
+    if (m >= M) continue;
+    auto epilogue = [&](auto kind) {
+#pragma unroll
+      for (int f = 0; f < FS; f += GATED ? 2 : 1) {
+        const int n = (GATED ? (sub0 + f) / 2 : sub0 + f) * 16 + 4 * g;
+        if (n >= s.N) continue;  // N % 8 == 0: the lane's four outputs are all in or all out
+        uint32_t o16[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float v = acc[f][t][i];
+          if constexpr (decltype(kind)::value >= 0) v = act_of<decltype(kind)::value>(s.act, v, GATED ? acc[f + (GATED ? 1 : 0)][t][i] : 0.0f);
+          o16[i] = f32_to_bf16_rne(v);
+        }
+        *(uint2*)(out + m * s.N + n) = make_uint2(o16[0] | (o16[1] << 16), o16[2] | (o16[3] << 16));
+      }
+    };
+    if constexpr (GATED) {
+      if (s.act.kind == kActGeluTanh) epilogue(std::integral_constant<int, kActGeluTanh>{});
+      else if (s.act.kind == kActSwigluOai) epilogue(std::integral_constant<int, kActSwigluOai>{});
+      else epilogue(std::integral_constant<int, kActSilu>{});
+    } else {
+      if (s.has_act) epilogue(std::integral_constant<int, kActRelu2>{});
+      else epilogue(std::integral_constant<int, -1>{});
+    }
+  }
+}
+
+template <int BM, int BN, int WT, int WF>
+hipError_t launch_tile(const Fp8Shape& s, const uint8_t* prepared, const uint8_t* codes, const uint8_t* xscale, int M,
+                       uint16_t* out, hipStream_t st) {
+  using T = Fp8Tile<BM, BN, WT, WF>;
+  const int tm = (M + BM - 1) / BM, tn = (s.subtiles() + BN / 16 - 1) / (BN / 16);
+  const dim3 grid(grid8((int64_t)tm * tn));
+  if (s.gated)
+    hipLaunchKernelGGL((fp8_tile_kernel<BM, BN, WT, WF, true>), grid, dim3(512), T::kLds, st, s, prepared, codes,
+                       xscale, M, tm, tn, out);
+  else
+    hipLaunchKernelGGL((fp8_tile_kernel<BM, BN, WT, WF, false>), grid, dim3(512), T::kLds, st, s, prepared, codes,
+                       xscale, M, tm, tn, out);
+  return hipGetLastError();
+}
+
 template <int FS, int TT, int NW>
 hipError_t launch_rows(const Fp8Shape& s, const uint8_t* prepared, const uint8_t* codes, const uint8_t* xscale, int M,
                        uint16_t* out, hipStream_t st) {
@@ -221,11 +404,14 @@ hipError_t launch_fp8_linear(const Fp8Shape& s, const uint8_t* prepared, const u
   const int64_t items = (int64_t)M * s.kblocks() * 16;
   const int64_t blocks = (items + 255) / 256;
   hipLaunchKernelGGL(fp8_quantize_rows, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, st, x, items,
-                     s.K, s.kblocks(), codes, xscale, s.scale_row());
+                     s.K, s.kblocks(), codes, xscale, s.scale_rows(M));
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (M <= 16) return launch_rows<2, 1, 8>(s, prepared, codes, xscale, M, out, st);
-  return launch_rows<4, 4, 4>(s, prepared, codes, xscale, M, out, st);
+  if (M <= 128) return launch_rows<4, 4, 4>(s, prepared, codes, xscale, M, out, st);
+  const int64_t big = (int64_t)((M + 255) / 256) * ((s.subtiles() + 15) / 16);
+  if (big >= 192) return launch_tile<256, 256, 2, 4>(s, prepared, codes, xscale, M, out, st);
+  return launch_tile<128, 128, 2, 4>(s, prepared, codes, xscale, M, out, st);
 }
 
 }  // namespace moe

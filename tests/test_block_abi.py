@@ -79,6 +79,7 @@ def test_route_rejects_before_launch(L):
     (dict(max_tokens=-1), EINVAL), (dict(max_tokens=(1 << 20) + 1), EUNSUPPORTED), (dict(fn=4), EINVAL),
     (dict(fn=-2), EINVAL), (dict(fn="swigluoai"), EINVAL), (dict(fn="swigluoai", alpha=1.0, limit=7.0), 0),
     (dict(fn="swigluoai", alpha=1.0, beta=float("nan"), limit=7.0), EINVAL), (dict(K=1 << 16, N=1 << 15), EUNSUPPORTED),
+    (dict(K=(1 << 20) + 8, N=8), EUNSUPPORTED), (dict(K=1 << 20, N=8), 0),
 ])
 def test_fp8_descriptor(L, kw, status):
     desc = block.Fp8Desc(**{**dict(K=128, N=64, max_tokens=8), **kw})
