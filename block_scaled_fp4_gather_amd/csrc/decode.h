@@ -58,6 +58,13 @@ __device__ __forceinline__ uint16_t f32_to_bf16_rne(float f) {
   return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
 }
 
+// Two fp32 values rounded to bf16, nearest-even (v_cvt_pk_bf16_f32), a in the
+// low half.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const bf16x2_t v = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
 // Scale of unit (chunk) c of a lane, from its packed scale dwords.
 // MXFP4: byte c%4 of dword c/4.  NVFP4: bytes 2(c%2), 2(c%2)+1 of dword c/2.
 __device__ __forceinline__ float mx_scale(uint32_t dword, int c) {

@@ -185,16 +185,16 @@ __global__ void __launch_bounds__(NW * 64)
     const int n = (GATED ? sub0 / 2 + f : sub0 + f) * 16 + 4 * g;
     const int64_t m = tok0 + 16 * t + r;
     if (n >= s.N || m >= M) continue;  // N % 8 == 0: the lane's four outputs are all in or all out
-    uint32_t o16[4];
+    if (s.has_act)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o16[i] = f32_to_bf16_rne(s.has_act ? gated_act(s.act, v[i], u[i]) : v[i]);
-    *(uint2*)(out + m * s.N + n) = make_uint2(o16[0] | (o16[1] << 16), o16[2] | (o16[3] << 16));
+      for (int i = 0; i < 4; ++i) v[i] = gated_act(s.act, v[i], u[i]);
+    *(uint2*)(out + m * s.N + n) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
   }
 }
 
 // ---- many tokens: BM tokens x BN weight rows per workgroup of 8 waves
 // (WT x WF), one K block per step.  Tokens go to LDS by direct copies (a row
-// of 128 codes: the 16-byte chunk c of row r at position c ^ a_swz(r)), the
+// of 128 codes: the 16-byte chunk c of row r at position c ^ row_swz(r)), the
 // weights, which only two or four waves share, straight to registers in the
 // layout they were prepared in; both one step ahead, and a step of the large
 // tile takes about as long as the copies (1024 matrix-unit cycles for each of
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(512, 2)
 #pragma unroll
   for (int c = 0; c < T::kCopies; ++c) {
     const int row = (c * 8 + wave) * 8 + lane / 8;
-    src[c] = (uint32_t)min(row, rows - 1) * (kb * 128u) + ((lane & 7) ^ a_swz(row)) * 16;
+    src[c] = (uint32_t)min(row, rows - 1) * (kb * 128u) + ((lane & 7) ^ row_swz<128>(row)) * 16;
   }
   auto copy_tokens = [&](int b, int ring) {
 #pragma unroll
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(512, 2)
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[f][t] = f32x4_t{};
 
-  const int swz = a_swz(r);  // the same for every 16th row: rows 16 t + r
+  const int swz = row_swz<128>(r);  // the same for every 16th row: rows 16 t + r
   const int brow = (wt * TT * 16 + r) * 128, bs = (wt * TT * 16 + r) * 4;
   auto step = [&](int b, i32x8_t (&a)[FS], const float w, i32x8_t (&an)[FS], float& wn) {
     vm_wait<0>();     // this wave's copies and loads for step b are here
@@ -338,14 +338,12 @@ __global__ void __launch_bounds__(512, 2)
       for (int f = 0; f < FS; f += GATED ? 2 : 1) {
         const int n = (GATED ? (sub0 + f) / 2 : sub0 + f) * 16 + 4 * g;
         if (n >= s.N) continue;  // N % 8 == 0: the lane's four outputs are all in or all out
-        uint32_t o16[4];
+        f32x4_t v = acc[f][t];
+        if constexpr (decltype(kind)::value >= 0)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float v = acc[f][t][i];
-          if constexpr (decltype(kind)::value >= 0) v = act_of<decltype(kind)::value>(s.act, v, GATED ? acc[f + (GATED ? 1 : 0)][t][i] : 0.0f);
-          o16[i] = f32_to_bf16_rne(v);
-        }
-        *(uint2*)(out + m * s.N + n) = make_uint2(o16[0] | (o16[1] << 16), o16[2] | (o16[3] << 16));
+          for (int i = 0; i < 4; ++i)
+            v[i] = act_of<decltype(kind)::value>(s.act, v[i], GATED ? acc[f + (GATED ? 1 : 0)][t][i] : 0.0f);
+        *(uint2*)(out + m * s.N + n) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
       }
     };
     if constexpr (GATED) {

@@ -61,6 +61,20 @@ __device__ __forceinline__ void vm_wait() {
 // Position of 16-byte chunk c in row r of an A slot.
 __device__ __forceinline__ int a_swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
 
+// Position of 16-byte chunk c, c ^ row_swz(r), in row r of an LDS tile whose
+// rows of 128 bytes (8 chunks) or 64 bytes (4) are read as operands of the
+// 16 x 16 matrix instructions: lane r + 16 g takes the chunk of group g of row
+// r, 16 bytes each.  The LDS serves 16 lanes of such a read per cycle if their
+// banks differ: lanes 0-3, 12-15, 20-27 together, then 4-11, 16-19, 28-31 (and
+// 32 on alike).  Within either set, and within 16 consecutive lanes, the rows
+// that share a bank half (128-byte rows: those of one parity) land in distinct
+// chunks.  With the plain order of a_swz each read took two cycles for one.
+template <int BYTES>
+__device__ __forceinline__ int row_swz(int r) {
+  static_assert(BYTES == 128 || BYTES == 64, "row bytes");
+  return BYTES == 128 ? (r >> 1) & 7 : (0x78 >> (2 * ((r >> 2) & 3))) & 3;
+}
+
 // Row (within the 32x32 block) of accumulator register r of this lane.
 __device__ __forceinline__ int acc_row(int r, int lane) { return (r >> 2) * 8 + (lane >> 5) * 4 + (r & 3); }
 

@@ -241,8 +241,7 @@ __global__ void __launch_bounds__(256)
 // steps ahead in a ring of three slots, one barrier per step.  WM x WE waves.
 //
 // An x slot holds BM rows of 32 S values; the 16-byte chunk c of row r is at
-// position c ^ swizzle(r), which spreads the 16 rows that a fragment read
-// takes one chunk of over the LDS banks.
+// position c ^ row_swz(r).
 template <int BM, int BE, int NP>
 struct RouteGemm {
   static constexpr int S = gemm_step(NP);           // K blocks of 32 per step
@@ -257,11 +256,6 @@ struct RouteGemm {
   static constexpr int kLds = 3 * kSlot;
   static_assert(kX % (1024 * kWaves) == 0 && kW % (1024 * kWaves) == 0 && TT >= 1, "whole copies per wave");
 };
-
-template <int S>
-__device__ __forceinline__ int row_swizzle(int r) {
-  return S == 2 ? a_swz(r) : ((r >> 1) ^ (r >> 3)) & 3;
-}
 
 template <int BM, int BE, int NP>
 __global__ void __launch_bounds__(512)
@@ -288,7 +282,7 @@ __global__ void __launch_bounds__(512)
     if (c < G::kXCopies) {
       const int kib = c * G::kWaves + wave;  // 1 KiB: 64 / kChunks rows
       const int row = kib * (64 / kChunks) + lane / kChunks;
-      const int chunk = (lane % kChunks) ^ row_swizzle<S>(row);
+      const int chunk = (lane % kChunks) ^ row_swz<G::kRow>(row);
       const int64_t m = min(tok0 + row, (int64_t)M - 1);
       const int k = min(b * 32 + chunk * 8, s.H - 8);
       dma16(x + m * s.H + k, lds_addr(slot + kib * 1024));
@@ -330,7 +324,7 @@ __global__ void __launch_bounds__(512)
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
         const int row = (wm * TT + t) * 16 + r;
-        uint4 v = *(const uint4*)(slot + row * G::kRow + ((4 * j + g) ^ row_swizzle<S>(row)) * 16);
+        uint4 v = *(const uint4*)(slot + row * G::kRow + ((4 * j + g) ^ row_swz<G::kRow>(row)) * 16);
         if (!in) v = make_uint4(0, 0, 0, 0);
         bop[t] = __builtin_bit_cast(bf16x8_t, v);
         if (norms && t % G::WE == we) sq[t] = add_squares(bop[t], sq[t]);
