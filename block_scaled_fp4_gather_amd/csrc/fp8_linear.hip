@@ -289,30 +289,36 @@ __global__ void __launch_bounds__(512, 2)
     for (int f = 0; f < FS; ++f) wf_[f] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), f));
     const uint8_t* const slot = smem + (b & 1) * T::kSlot + brow;
     const uint8_t* const sc = sring + ((b >> 2) & 1) * 4 * BM + bs + (b & 3);
-    // One token tile at a time, the next one's operand read ahead: left alone,
-    // the compiler keeps so many tiles in flight that registers spill.  The
-    // other wave of the SIMD fills the matrix unit during the multiply-adds.
     auto read = [&](int t, i32x8_t& bop, int& sx) {
       const i32x4_t lo = *(const i32x4_t*)(slot + t * 2048 + (g ^ swz) * 16);
       const i32x4_t hi = *(const i32x4_t*)(slot + t * 2048 + ((4 + g) ^ swz) * 16);
       bop = i32x8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
       sx = sc[t * 64];
     };
+    // The multiply-adds of a product come kLag products later: its result is
+    // there by then, and they run in the shadow of the products in between.
+    // The order is pinned: left alone, the compiler puts them right behind
+    // their product and waits, or keeps so much in flight that registers spill.
+    constexpr int kLag = 2, kRing = kLag + 1, kAll = FS * TT;
     i32x8_t bop[2];
     int sx[2];
+    f32x4_t p[kRing];
     read(0, bop[0], sx[0]);
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      if (t + 1 < TT) read(t + 1, bop[(t + 1) & 1], sx[(t + 1) & 1]);
-      f32x4_t p[FS];
+    for (int i = 0; i < kAll + kLag; ++i) {
+      const int t = i / FS, f = i % FS;
+      if (i < kAll) {
+        if (f == 0 && t + 1 < TT) read(t + 1, bop[(t + 1) & 1], sx[(t + 1) & 1]);
+        p[i % kRing] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[f], bop[t & 1], f32x4_t{}, 0, 0, 0, 127, 0,
+                                                                       sx[t & 1]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (i >= kLag) {
+        const int j = i - kLag;
 #pragma unroll
-      for (int f = 0; f < FS; ++f)
-        p[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[f], bop[t & 1], f32x4_t{}, 0, 0, 0, 127, 0,
-                                                               sx[t & 1]);
-#pragma unroll
-      for (int f = 0; f < FS; ++f)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[f][t][i] = fmaf(wf_[f], p[f][i], acc[f][t][i]);
+        for (int e = 0; e < 4; ++e)
+          acc[j % FS][j / FS][e] = fmaf(wf_[j % FS], p[j % kRing][e], acc[j % FS][j / FS][e]);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
