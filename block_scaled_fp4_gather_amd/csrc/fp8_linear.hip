@@ -193,20 +193,18 @@ __global__ void __launch_bounds__(NW * 64)
 }
 
 // ---- many tokens: BM tokens x BN weight rows per workgroup of 8 waves
-// (WT x WF), one K block per step.  Tokens go to LDS by direct copies (a row
-// of 128 codes: the 16-byte chunk c of row r at position c ^ row_swz(r)), the
-// weights, which only two or four waves share, straight to registers in the
-// layout they were prepared in; both one step ahead, and a step of the large
-// tile takes about as long as the copies (1024 matrix-unit cycles for each of
-// a SIMD's two waves).  Every 4 steps the scale dwords of the tokens' next 4
-// K blocks follow.
+// (WT x WF), one K block per step.  Tokens (a row of 128 codes: the 16-byte
+// chunk c of row r at position c ^ row_swz(r)) and weights (in the layout they
+// were prepared in) go to LDS by direct copies, one step ahead in two slots.
+// Every 4 steps the scale dwords of the tokens' next 4 K blocks follow.
 template <int BM, int BN, int WT, int WF>
 struct Fp8Tile {
   static constexpr int FS = BN / 16 / WF, TT = BM / 16 / WT;
-  static constexpr int kSlot = BM * 128;
-  static constexpr int kCopies = kSlot / 1024 / 8;
+  static constexpr int kTokens = BM * 128, kSlot = kTokens + BN * 128;
+  static constexpr int kCopies = kTokens / 1024 / 8, kWCopies = BN / 64;
   static constexpr int kLds = 2 * kSlot + 2 * 4 * BM;
-  static_assert(WT * WF == 8 && FS % 2 == 0 && BM % 64 == 0, "8 waves, whole gate and up pairs, whole copies");
+  static_assert(WT * WF == 8 && FS % 2 == 0 && BM % 64 == 0 && BN % 64 == 0,
+                "8 waves, whole gate and up pairs, whole copies");
 };
 
 template <int BM, int BN, int WT, int WF, bool GATED>
@@ -253,21 +251,20 @@ __global__ void __launch_bounds__(512, 2)
     if (wave * 64 < BM)
       dma4(xscale + (q * mp + tok0 + wave * 64 + lane) * 4, lds_addr(sring + (q & 1) * 4 * BM + wave * 256));
   };
-  const uint8_t* wsrc[FS];
+  // weight copies of this wave: 1 KiB, half a subtile's block, each; subtiles past the last repeat it
+  const uint8_t* wsrc[T::kWCopies];
 #pragma unroll
-  for (int f = 0; f < FS; ++f) wsrc[f] = prepared + (int64_t)min(sub0 + f, ns - 1) * kb * 2048;
-  const float* const wscale = ws + (int64_t)min(sub0 + lane % FS, ns - 1) * kb;
-  auto load_weights = [&](int b, i32x8_t (&a)[FS], float& w) {
+  for (int c = 0; c < T::kWCopies; ++c) {
+    const int kib = c * 8 + wave;
+    wsrc[c] = prepared + (int64_t)min(tn * (BN / 16) + kib / 2, ns - 1) * kb * 2048 + (kib & 1) * 1024;
+  }
+  auto copy_weights = [&](int b, int ring) {
 #pragma unroll
-    for (int f = 0; f < FS; ++f) {
-      const uint8_t* const at = wsrc[f] + (int64_t)b * 2048;
-      const i32x4_t lo = *(const i32x4_t*)(at + (uint32_t)lane * 16);
-      const i32x4_t hi = *(const i32x4_t*)(at + (uint32_t)lane * 16 + 1024);
-      a[f] = i32x8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-    }
-    w = wscale[b];
+    for (int c = 0; c < T::kWCopies; ++c)
+      dma16_at(wsrc[c] + (int64_t)b * 2048, lane * 16,
+               lds_addr(smem + ring * T::kSlot + T::kTokens + (c * 8 + wave) * 1024));
   };
-
+  const float* const wscale = ws + (int64_t)min(sub0 + lane % FS, ns - 1) * kb;
   f32x4_t acc[FS][TT];
 #pragma unroll
   for (int f = 0; f < FS; ++f)
@@ -276,18 +273,25 @@ __global__ void __launch_bounds__(512, 2)
 
   const int swz = row_swz<128>(r);  // the same for every 16th row: rows 16 t + r
   const int brow = (wt * TT * 16 + r) * 128, bs = (wt * TT * 16 + r) * 4;
-  auto step = [&](int b, i32x8_t (&a)[FS], const float w, i32x8_t (&an)[FS], float& wn) {
-    vm_wait<0>();     // this wave's copies and loads for step b are here
+  float w = wscale[0];
+  copy_tokens(0, 0);
+  copy_weights(0, 0);
+  copy_scales(0);
+#pragma unroll 1
+  for (int b = 0; b < kb; ++b) {
+    vm_wait<0>();     // this wave's copies for step b are here
     __syncthreads();  // everyone's are, and everyone is done with step b - 1
     const int next = min(b + 1, kb - 1);  // past the last block it is loaded again, and not used
     copy_tokens(next, (b + 1) & 1);
+    copy_weights(next, (b + 1) & 1);
     if ((b & 3) == 0 && b + 4 < kb) copy_scales((b >> 2) + 1);
-    load_weights(next, an, wn);
-    __builtin_amdgcn_sched_barrier(0);
     float wf_[FS];
 #pragma unroll
     for (int f = 0; f < FS; ++f) wf_[f] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), f));
+    w = wscale[next];
+    __builtin_amdgcn_sched_barrier(0);
     const uint8_t* const slot = smem + (b & 1) * T::kSlot + brow;
+    const uint8_t* const wslot = smem + (b & 1) * T::kSlot + T::kTokens + wf * FS * 2048 + lane * 16;
     const uint8_t* const sc = sring + ((b >> 2) & 1) * 4 * BM + bs + (b & 3);
     auto read = [&](int t, i32x8_t& bop, int& sx) {
       const i32x4_t lo = *(const i32x4_t*)(slot + t * 2048 + (g ^ swz) * 16);
@@ -300,10 +304,15 @@ __global__ void __launch_bounds__(512, 2)
     // The order is pinned: left alone, the compiler puts them right behind
     // their product and waits, or keeps so much in flight that registers spill.
     constexpr int kLag = 2, kRing = kLag + 1, kAll = FS * TT;
-    i32x8_t bop[2];
+    i32x8_t a[FS], bop[2];
     int sx[2];
     f32x4_t p[kRing];
     read(0, bop[0], sx[0]);
+#pragma unroll
+    for (int f = 0; f < FS; ++f) {
+      const i32x4_t lo = *(const i32x4_t*)(wslot + f * 2048), hi = *(const i32x4_t*)(wslot + f * 2048 + 1024);
+      a[f] = i32x8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    }
 #pragma unroll
     for (int i = 0; i < kAll + kLag; ++i) {
       const int t = i / FS, f = i % FS;
@@ -321,18 +330,7 @@ __global__ void __launch_bounds__(512, 2)
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-  };
-  i32x8_t a0[FS], a1[FS];
-  float w0, w1;
-  copy_tokens(0, 0);
-  copy_scales(0);
-  load_weights(0, a0, w0);
-  int b = 0;
-  for (; b + 1 < kb; b += 2) {
-    step(b, a0, w0, a1, w1);
-    step(b + 1, a1, w1, a0, w0);
   }
-  if (b < kb) step(b, a0, w0, a1, w1);
   vm_wait<0>();  // no copy may land after the workgroup's LDS is released
 
 #pragma unroll
