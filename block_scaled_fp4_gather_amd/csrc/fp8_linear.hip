@@ -201,10 +201,11 @@ template <int BM, int BN, int WT, int WF>
 struct Fp8Tile {
   static constexpr int FS = BN / 16 / WF, TT = BM / 16 / WT;
   static constexpr int kTokens = BM * 128, kSlot = kTokens + BN * 128;
-  static constexpr int kCopies = kTokens / 1024 / 8, kWCopies = BN / 64;
+  static constexpr int kCopies = kTokens / 1024 / 8, kWCopies = BN / 64, kAllCopies = kCopies + kWCopies;
   static constexpr int kLds = 2 * kSlot + 2 * 4 * BM;
   static_assert(WT * WF == 8 && FS % 2 == 0 && BM % 64 == 0 && BN % 64 == 0,
                 "8 waves, whole gate and up pairs, whole copies");
+  static_assert(kAllCopies + 1 < FS * TT, "copies between the products");
 };
 
 template <int BM, int BN, int WT, int WF, bool GATED>
@@ -242,14 +243,15 @@ __global__ void __launch_bounds__(512, 2)
     const int row = (c * 8 + wave) * 8 + lane / 8;
     src[c] = (uint32_t)min(row, rows - 1) * (kb * 128u) + ((lane & 7) ^ row_swz<128>(row)) * 16;
   }
-  auto copy_tokens = [&](int b, int ring) {
-#pragma unroll
-    for (int c = 0; c < T::kCopies; ++c)
-      dma16_at(tile + (int64_t)b * 128, src[c], lds_addr(smem + ring * T::kSlot + (c * 8 + wave) * 1024));
-  };
-  auto copy_scales = [&](int q) {  // scale dwords of K blocks 4q..; the scale rows are padded to whole tiles
-    if (wave * 64 < BM)
-      dma4(xscale + (q * mp + tok0 + wave * 64 + lane) * 4, lds_addr(sring + (q & 1) * 4 * BM + wave * 256));
+  // Scale dwords of K blocks 4q .. 4q + 3 (the scale rows are padded to whole
+  // tiles).  In a step this repeats for 4 steps what the first of them did,
+  // and every wave takes part: a branch in the middle of a step costs more.
+  const uint32_t part = (wave % (BM / 64)) * 256;
+  const uint8_t* const scales = xscale + tok0 * 4 + part;
+  const int last_q = (kb - 1) / 4;
+  auto copy_scales = [&](int q) {
+    const int from = min(q, last_q);
+    dma4_at(scales + from * mp * 4, lane * 4, lds_addr(sring) + (q & 1) * 4 * BM + part);
   };
   // weight copies of this wave: 1 KiB, half a subtile's block, each; subtiles past the last repeat it
   const uint8_t* wsrc[T::kWCopies];
@@ -258,11 +260,13 @@ __global__ void __launch_bounds__(512, 2)
     const int kib = c * 8 + wave;
     wsrc[c] = prepared + (int64_t)min(tn * (BN / 16) + kib / 2, ns - 1) * kb * 2048 + (kib & 1) * 1024;
   }
-  auto copy_weights = [&](int b, int ring) {
-#pragma unroll
-    for (int c = 0; c < T::kWCopies; ++c)
-      dma16_at(wsrc[c] + (int64_t)b * 2048, lane * 16,
-               lds_addr(smem + ring * T::kSlot + T::kTokens + (c * 8 + wave) * 1024));
+  const uint32_t lds0 = lds_addr(smem) + wave * 1024;
+  auto copy = [&](int b, int ring, int c) {  // copy c of K block b: tokens, then weights
+    const uint32_t to = lds0 + ring * T::kSlot + c * 8192;
+    if (c < T::kCopies)
+      dma16_at(tile + (int64_t)b * 128, src[c], to);
+    else
+      dma16_at(wsrc[c - T::kCopies] + (int64_t)b * 2048, lane * 16, to);
   };
   const float* const wscale = ws + (int64_t)min(sub0 + lane % FS, ns - 1) * kb;
   f32x4_t acc[FS][TT];
@@ -274,17 +278,14 @@ __global__ void __launch_bounds__(512, 2)
   const int swz = row_swz<128>(r);  // the same for every 16th row: rows 16 t + r
   const int brow = (wt * TT * 16 + r) * 128, bs = (wt * TT * 16 + r) * 4;
   float w = wscale[0];
-  copy_tokens(0, 0);
-  copy_weights(0, 0);
+#pragma unroll
+  for (int c = 0; c < T::kAllCopies; ++c) copy(0, 0, c);
   copy_scales(0);
 #pragma unroll 1
   for (int b = 0; b < kb; ++b) {
     vm_wait<0>();     // this wave's copies for step b are here
     __syncthreads();  // everyone's are, and everyone is done with step b - 1
-    const int next = min(b + 1, kb - 1);  // past the last block it is loaded again, and not used
-    copy_tokens(next, (b + 1) & 1);
-    copy_weights(next, (b + 1) & 1);
-    if ((b & 3) == 0 && b + 4 < kb) copy_scales((b >> 2) + 1);
+    const int next = min(b + 1, kb - 1);  // past the last block it is copied again, and not used
     float wf_[FS];
 #pragma unroll
     for (int f = 0; f < FS; ++f) wf_[f] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), f));
@@ -318,6 +319,9 @@ __global__ void __launch_bounds__(512, 2)
       const int t = i / FS, f = i % FS;
       if (i < kAll) {
         if (f == 0 && t + 1 < TT) read(t + 1, bop[(t + 1) & 1], sx[(t + 1) & 1]);
+        // the next step's copies go between the first products
+        if (i >= 1 && i <= T::kAllCopies) copy(next, (b + 1) & 1, i - 1);
+        if (i == T::kAllCopies + 1) copy_scales((b >> 2) + 1);
         p[i % kRing] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[f], bop[t & 1], f32x4_t{}, 0, 0, 0, 127, 0,
                                                                        sx[t & 1]);
         __builtin_amdgcn_sched_barrier(0);

@@ -44,6 +44,11 @@ __device__ __forceinline__ void dma16_at(const void* base, uint32_t off, uint32_
   asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\tglobal_load_lds_dwordx4 %1, %2\n\ts_mov_b32 m0, %0"
                : "=&s"(tmp) : "v"(off), "s"(base), "s"(lds));
 }
+__device__ __forceinline__ void dma4_at(const void* base, uint32_t off, uint32_t lds) {
+  uint32_t tmp;
+  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\tglobal_load_lds_dword %1, %2\n\ts_mov_b32 m0, %0"
+               : "=&s"(tmp) : "v"(off), "s"(base), "s"(lds));
+}
 // The same for data read once (weights): non-temporal, so that it does not
 // displace reused lines in the caches.
 __device__ __forceinline__ void dma16_nt(const void* g, uint32_t lds) {
