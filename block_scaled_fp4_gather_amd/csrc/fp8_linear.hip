@@ -337,31 +337,46 @@ __global__ void __launch_bounds__(512, 2)
   }
   vm_wait<0>();  // no copy may land after the workgroup's LDS is released
 
+  __syncthreads();
+
+  // Each wave turns its outputs round in its own part of the LDS, so that it
+  // stores whole rows of up to 128 bytes: 16-byte chunk c of token row i at
+  // position c ^ (i % chunks of a row).
+  constexpr int kRow = (GATED ? FS / 2 : FS) * 32, kPer = kRow / 16;
+  static_assert(8 * TT * 16 * kRow <= 2 * T::kSlot, "the waves' parts");
+  uint8_t* const mine = smem + wave * TT * 16 * kRow;
+  auto put = [&](auto kind) {
 #pragma unroll
-  for (int t = 0; t < TT; ++t) {
-    const int64_t m = tok0 + (wt * TT + t) * 16 + r;
-    if (m >= M) continue;
-    auto epilogue = [&](auto kind) {
+    for (int t = 0; t < TT; ++t)
 #pragma unroll
       for (int f = 0; f < FS; f += GATED ? 2 : 1) {
-        const int n = (GATED ? (sub0 + f) / 2 : sub0 + f) * 16 + 4 * g;
-        if (n >= s.N) continue;  // N % 8 == 0: the lane's four outputs are all in or all out
         f32x4_t v = acc[f][t];
         if constexpr (decltype(kind)::value >= 0)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             v[i] = act_of<decltype(kind)::value>(s.act, v[i], GATED ? acc[f + (GATED ? 1 : 0)][t][i] : 0.0f);
-        *(uint2*)(out + m * s.N + n) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+        const int c = (GATED ? f / 2 : f) * 2 + g / 2;
+        *(uint2*)(mine + (16 * t + r) * kRow + (c ^ (r % kPer)) * 16 + g % 2 * 8) =
+            make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
       }
-    };
-    if constexpr (GATED) {
-      if (s.act.kind == kActGeluTanh) epilogue(std::integral_constant<int, kActGeluTanh>{});
-      else if (s.act.kind == kActSwigluOai) epilogue(std::integral_constant<int, kActSwigluOai>{});
-      else epilogue(std::integral_constant<int, kActSilu>{});
-    } else {
-      if (s.has_act) epilogue(std::integral_constant<int, kActRelu2>{});
-      else epilogue(std::integral_constant<int, -1>{});
-    }
+  };
+  if constexpr (GATED) {
+    if (s.act.kind == kActGeluTanh) put(std::integral_constant<int, kActGeluTanh>{});
+    else if (s.act.kind == kActSwigluOai) put(std::integral_constant<int, kActSwigluOai>{});
+    else put(std::integral_constant<int, kActSilu>{});
+  } else {
+    if (s.has_act) put(std::integral_constant<int, kActRelu2>{});
+    else put(std::integral_constant<int, -1>{});
+  }
+  wave_sync();
+  const int n = (GATED ? sub0 / 2 : sub0) * 16 + lane % kPer * 8;
+  const int64_t m0 = tok0 + wt * TT * 16;
+#pragma unroll
+  for (int i = 0; i < TT * 16 * kPer / 64; ++i) {
+    const int row = i * (64 / kPer) + lane / kPer;
+    const uint4 v = *(const uint4*)(mine + row * kRow + (lane % kPer ^ row % kPer) * 16);
+    // N % 8 == 0: a chunk's eight outputs are all in or all out
+    if (m0 + row < M && n < s.N) *(uint4*)(out + (m0 + row) * s.N + n) = v;
   }
 }
 

@@ -439,14 +439,6 @@ __device__ __forceinline__ void wave_best(double& v, int& e) {
   }
 }
 
-// Orders a wave's LDS accesses for the compiler; the hardware runs them in
-// order.
-__device__ __forceinline__ void wave_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 // The same value, unknown to the compiler: what it derived from v before (a
 // mask register per comparison) is not kept for later uses.
 __device__ __forceinline__ int renew(int v) {
