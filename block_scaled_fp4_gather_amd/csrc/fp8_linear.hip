@@ -74,45 +74,62 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// ---- activation quantisation: 16 consecutive lanes per 128 values
+// ---- activation quantisation
 
-__global__ void __launch_bounds__(256)
-    fp8_quantize_rows(const uint16_t* __restrict__ x, int64_t items, int K, int kb, uint8_t* __restrict__ codes,
-                      uint8_t* __restrict__ scales, int64_t rows) {
-  const int64_t stride = (int64_t)gridDim.x * blockDim.x;
-  // items is a multiple of 16 and so is the stride: a block's lanes stay together
-  for (int64_t it = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; it < items; it += stride) {
-    const int per = kb * 16;
-    const int64_t row = it / per;
-    const int c = (int)(it - row * per);
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    if (c * 8 < K) raw = *(const uint4*)(x + row * K + c * 8);
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-    float v[8];
-    uint32_t amax = 0;
+// Largest of 16 consecutive lanes, in all of them (rotations within a row).
+__device__ __forceinline__ uint32_t row_max_u32(uint32_t v) {
+#define MOE_STEP(CTRL) v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true))
+  MOE_STEP(0x121);  // row_ror:1
+  MOE_STEP(0x122);
+  MOE_STEP(0x124);
+  MOE_STEP(0x128);
+#undef MOE_STEP
+  return v;
+}
+
+// 8 values of a 128-value block, whose other values 15 neighbouring lanes
+// hold: codes and the block's scale byte.  v_cvt_pk_fp8_f32 rounds to
+// nearest-even; no value exceeds 448.
+__device__ __forceinline__ uint2 quantise8(const uint4& raw, uint32_t& byte) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  float v[8];
+  uint32_t amax = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      amax = max(amax, (w[i] << 16) & 0x7FFFFFFFu);
-      amax = max(amax, w[i] & 0x7FFF0000u);
-    }
-#pragma unroll
-    for (int d = 1; d < 16; d <<= 1) amax = max(amax, (uint32_t)__shfl_xor((int)amax, d));
-    const uint32_t sb = block_scale_byte(amax);
-    uint32_t lo = 0x7F7F7F7Fu, hi = 0x7F7F7F7Fu;
-    if (sb != 255u) {
-      const float inv = mx_inv_scale(sb);
-      lo = hi = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        lo |= e4m3_code(v[i] * inv) << (8 * i);
-        hi |= e4m3_code(v[4 + i] * inv) << (8 * i);
-      }
-    }
-    *(uint2*)(codes + it * 8) = make_uint2(lo, hi);
-    if ((c & 15) == 0) scales[((c >> 6) * rows + row) * 4 + ((c >> 4) & 3)] = (uint8_t)sb;
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    amax = max(amax, (w[i] << 16) & 0x7FFFFFFFu);
+    amax = max(amax, w[i] & 0x7FFF0000u);
   }
+  byte = block_scale_byte(row_max_u32(amax));
+  if (byte == 255u) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+  const float inv = mx_inv_scale(byte);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] *= inv;
+  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], lo, true);
+  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], 0, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], hi, true);
+  return make_uint2((uint32_t)lo, (uint32_t)hi);
+}
+
+// One wave per row and 4 K blocks (a scale dword).
+__global__ void __launch_bounds__(256)
+    fp8_quantize_rows(const uint16_t* __restrict__ x, int M, int K, int kb, uint8_t* __restrict__ codes,
+                      uint8_t* __restrict__ scales, int64_t scale_rows) {
+  const int lane = threadIdx.x & 63;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int q = blockIdx.y;
+  if (row >= M) return;
+  const int c = (q * 64 + lane) * 8;
+  uint4 raw = make_uint4(0, 0, 0, 0);
+  if (c < K) raw = *(const uint4*)(x + row * K + c);
+  uint32_t byte;
+  const uint2 code = quantise8(raw, byte);
+  if (c < kb * 128) *(uint2*)(codes + row * kb * 128 + c) = code;
+  const uint32_t dword = __builtin_amdgcn_readlane(byte, 0) | __builtin_amdgcn_readlane(byte, 16) << 8 |
+                         __builtin_amdgcn_readlane(byte, 32) << 16 | __builtin_amdgcn_readlane(byte, 48) << 24;
+  if (lane == 0) *(uint32_t*)(scales + (q * scale_rows + row) * 4) = dword;
 }
 
 // ---- products: each wave takes every NW-th K block of FS subtiles x 16 TT
@@ -422,10 +439,8 @@ hipError_t launch_fp8_linear(const Fp8Shape& s, const uint8_t* prepared, const u
                              uint8_t* ws, hipStream_t st) {
   uint8_t* const codes = ws;
   uint8_t* const xscale = ws + s.code_bytes(M);
-  const int64_t items = (int64_t)M * s.kblocks() * 16;
-  const int64_t blocks = (items + 255) / 256;
-  hipLaunchKernelGGL(fp8_quantize_rows, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, st, x, items,
-                     s.K, s.kblocks(), codes, xscale, s.scale_rows(M));
+  hipLaunchKernelGGL(fp8_quantize_rows, dim3((unsigned)((M + 3) / 4), (unsigned)((s.kblocks() + 3) / 4)), dim3(256), 0,
+                     st, x, M, s.K, s.kblocks(), codes, xscale, s.scale_rows(M));
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (M <= 16) return launch_rows<2, 1, 8>(s, prepared, codes, xscale, M, out, st);
