@@ -132,57 +132,133 @@ __global__ void __launch_bounds__(256)
   if (lane == 0) *(uint32_t*)(scales + (q * scale_rows + row) * 4) = dword;
 }
 
-// ---- products: each wave takes every NW-th K block of FS subtiles x 16 TT
-// tokens; the waves' sums are joined in LDS in wave order.
+// ---- few tokens: FS subtiles x 16 TT tokens per workgroup, whose NW waves
+// share K in runs of consecutive blocks and join their sums in LDS in wave
+// order.  What bounds it is the time from a load to its use, so each wave
+// loads U blocks' operands while it multiplies the U before.
+//
+// FUSED: x is quantised by each workgroup itself into LDS (up to kFusedUnits
+// blocks of 128 values), while the first weights are on their way: for the
+// fewest tokens that takes less than a launch of its own.
 
-template <int FS, int TT, int NW, bool GATED>
+template <int NW>
+constexpr int kFusedUnits = 4 * 4 * NW;  // 4 passes of the workgroup's 16-lane groups
+
+template <int FS, int TT, int NW, int U, bool GATED, bool FUSED>
 __global__ void __launch_bounds__(NW * 64)
-    fp8_rows_kernel(Fp8Shape s, const uint8_t* __restrict__ prepared, const uint8_t* __restrict__ codes,
-                    const uint8_t* __restrict__ xscale, int M, uint16_t* __restrict__ out) {
+    fp8_few_kernel(Fp8Shape s, const uint8_t* __restrict__ prepared, const uint8_t* __restrict__ codes,
+                   const uint8_t* __restrict__ xscale, const uint16_t* __restrict__ x, int M,
+                   uint16_t* __restrict__ out) {
+  static_assert(!GATED || FS % 2 == 0, "whole gate and up pairs");
+  static_assert(!FUSED || TT == 1, "few tokens");
   __shared__ f32x4_t part[NW][FS * TT][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ uint8_t qcodes[FUSED ? kFusedUnits<NW> * 128 : 16], qscale[FUSED ? kFusedUnits<NW> : 16];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kb = s.kblocks(), ns = s.subtiles();
   const int64_t mp = s.scale_rows(M);
   const int sub0 = blockIdx.x * FS;
   const int64_t tok0 = (int64_t)blockIdx.y * (16 * TT);
   const int r = lane & 15, g = lane >> 4;
   const float* const ws = (const float*)(prepared + s.codes_bytes());
+  const int per = (kb + NW - 1) / NW, b0 = wave * per, b1 = min(kb, b0 + per);
+
+  struct Operands {
+    i32x8_t a[U][FS], b[U][TT];
+    int sx[U][TT];
+    float w[U][FS];
+  };
+  const uint8_t* xrow[TT];
+  const uint8_t* srow[TT];
+#pragma unroll
+  for (int t = 0; t < TT; ++t) {
+    const int64_t m = min(tok0 + 16 * t + r, (int64_t)M - 1);  // rows past M repeat the last one and are not stored
+    xrow[t] = codes + m * kb * 128 + g * 16;
+    srow[t] = xscale + m * 4;
+  }
+  auto load = [&](int b, Operands& o) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int bu = min(b + u, kb - 1);  // blocks past the run are loaded and not used
+#pragma unroll
+      for (int f = 0; f < FS; ++f) {
+        const int64_t sub = min(sub0 + f, ns - 1);
+        const uint8_t* const at = prepared + (sub * kb + bu) * 2048;
+        const i32x4_t lo = *(const i32x4_t*)(at + lane * 16), hi = *(const i32x4_t*)(at + lane * 16 + 1024);
+        o.a[u][f] = i32x8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        o.w[u][f] = ws[sub * kb + bu];
+      }
+      if constexpr (!FUSED)
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          const i32x4_t lo = *(const i32x4_t*)(xrow[t] + bu * 128), hi = *(const i32x4_t*)(xrow[t] + bu * 128 + 64);
+          o.b[u][t] = i32x8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+          o.sx[u][t] = srow[t][(bu >> 2) * mp * 4 + (bu & 3)];
+        }
+    }
+  };
   f32x4_t acc[FS][TT];
 #pragma unroll
   for (int f = 0; f < FS; ++f)
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[f][t] = f32x4_t{};
-  const uint8_t* xrow[TT];
-  const uint8_t* srows[TT];
+  auto multiply = [&](int b, Operands& o) {
 #pragma unroll
-  for (int t = 0; t < TT; ++t) {
-    const int64_t m = min(tok0 + 16 * t + r, (int64_t)M - 1);  // rows past M repeat the last one and are not stored
-    xrow[t] = codes + m * kb * 128 + g * 16;
-    srows[t] = xscale + m * 4;
-  }
-  for (int b = wave; b < kb; b += NW) {
-    i32x8_t bop[TT];
-    int sx[TT];
+    for (int u = 0; u < U; ++u) {
+      if (b + u >= b1) break;
+      if constexpr (FUSED) {
+        const int unit = min(r, M - 1) * kb + b + u;
+        const i32x4_t lo = *(const i32x4_t*)(qcodes + unit * 128 + g * 16);
+        const i32x4_t hi = *(const i32x4_t*)(qcodes + unit * 128 + g * 16 + 64);
+        o.b[u][0] = i32x8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        o.sx[u][0] = qscale[unit];
+      }
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      const i32x4_t lo = *(const i32x4_t*)(xrow[t] + b * 128), hi = *(const i32x4_t*)(xrow[t] + b * 128 + 64);
-      bop[t] = i32x8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-      sx[t] = srows[t][(b >> 2) * mp * 4 + (b & 3)];
+      for (int f = 0; f < FS; ++f)
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          const f32x4_t p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(o.a[u][f], o.b[u][t], f32x4_t{}, 0, 0, 0,
+                                                                             127, 0, o.sx[u][t]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[f][t][i] = fmaf(o.w[u][f], p[i], acc[f][t][i]);
+        }
     }
+  };
+
+  Operands o0, o1;
+  if constexpr (FUSED) {
+    const int units = M * kb;
+    uint4 raw[4];
 #pragma unroll
-    for (int f = 0; f < FS; ++f) {
-      const int sub = min(sub0 + f, ns - 1);
-      const uint8_t* a = prepared + ((int64_t)sub * kb + b) * 2048 + lane * 16;
-      const i32x4_t lo = *(const i32x4_t*)a, hi = *(const i32x4_t*)(a + 1024);
-      const i32x8_t aop = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-      const float w = ws[(int64_t)sub * kb + b];
+    for (int i = 0; i < 4; ++i) {
+      const int unit = (i * NW * 64 + (int)threadIdx.x) / 16, row = unit / kb;
+      const int c = (unit - row * kb) * 128 + (lane & 15) * 8;
+      raw[i] = make_uint4(0, 0, 0, 0);
+      if (unit < units && c < s.K) raw[i] = *(const uint4*)(x + (int64_t)row * s.K + c);
+    }
+    __builtin_amdgcn_sched_barrier(0);  // x first: it is needed first
+    load(b0, o0);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        const f32x4_t p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(aop, bop[t], f32x4_t{}, 0, 0, 0, 127, 0, sx[t]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[f][t][i] = fmaf(w, p[i], acc[f][t][i]);
+    for (int i = 0; i < 4; ++i) {
+      const int unit = (i * NW * 64 + (int)threadIdx.x) / 16;
+      uint32_t byte;
+      const uint2 code = quantise8(raw[i], byte);
+      if (unit < units) {
+        *(uint2*)(qcodes + unit * 128 + (lane & 15) * 8) = code;
+        if ((lane & 15) == 0) qscale[unit] = (uint8_t)byte;
       }
     }
+    __syncthreads();
+  } else {
+    load(b0, o0);
+  }
+  for (int b = b0; b < b1; b += 2 * U) {
+    load(b + U, o1);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(b, o0);
+    load(b + 2 * U, o0);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(b + U, o1);
   }
 #pragma unroll
   for (int f = 0; f < FS; ++f)
@@ -412,16 +488,19 @@ hipError_t launch_tile(const Fp8Shape& s, const uint8_t* prepared, const uint8_t
   return hipGetLastError();
 }
 
-template <int FS, int TT, int NW>
-hipError_t launch_rows(const Fp8Shape& s, const uint8_t* prepared, const uint8_t* codes, const uint8_t* xscale, int M,
-                       uint16_t* out, hipStream_t st) {
-  const dim3 grid((unsigned)((s.subtiles() + FS - 1) / FS), (unsigned)((M + 16 * TT - 1) / (16 * TT)));
+template <int FS, int TT, int NW, int U, bool FUSED>
+hipError_t launch_few(const Fp8Shape& s, const uint8_t* prepared, const uint8_t* codes, const uint8_t* xscale,
+                      const uint16_t* x, int M, uint16_t* out, hipStream_t st) {
+  // a gated map takes its subtiles in pairs
+  constexpr int GFS = FS % 2 ? 2 * FS : FS;
+  const int fs = s.gated ? GFS : FS;
+  const dim3 grid((unsigned)((s.subtiles() + fs - 1) / fs), (unsigned)((M + 16 * TT - 1) / (16 * TT)));
   if (s.gated)
-    hipLaunchKernelGGL((fp8_rows_kernel<FS, TT, NW, true>), grid, dim3(NW * 64), 0, st, s, prepared, codes, xscale, M,
-                       out);
+    hipLaunchKernelGGL((fp8_few_kernel<GFS, TT, NW, U, true, FUSED>), grid, dim3(NW * 64), 0, st, s, prepared, codes,
+                       xscale, x, M, out);
   else
-    hipLaunchKernelGGL((fp8_rows_kernel<FS, TT, NW, false>), grid, dim3(NW * 64), 0, st, s, prepared, codes, xscale,
-                       M, out);
+    hipLaunchKernelGGL((fp8_few_kernel<FS, TT, NW, U, false, FUSED>), grid, dim3(NW * 64), 0, st, s, prepared, codes,
+                       xscale, x, M, out);
   return hipGetLastError();
 }
 
@@ -439,12 +518,21 @@ hipError_t launch_fp8_linear(const Fp8Shape& s, const uint8_t* prepared, const u
                              uint8_t* ws, hipStream_t st) {
   uint8_t* const codes = ws;
   uint8_t* const xscale = ws + s.code_bytes(M);
+  const bool deep = s.kblocks() > 16;  // enough blocks for 16 waves
+  if (M <= 4 && M * s.kblocks() <= (deep ? kFusedUnits<16> : kFusedUnits<4>)) {
+    if (deep) return launch_few<1, 1, 16, 2, true>(s, prepared, codes, xscale, x, M, out, st);
+    return launch_few<1, 1, 4, 2, true>(s, prepared, codes, xscale, x, M, out, st);
+  }
   hipLaunchKernelGGL(fp8_quantize_rows, dim3((unsigned)((M + 3) / 4), (unsigned)((s.kblocks() + 3) / 4)), dim3(256), 0,
                      st, x, M, s.K, s.kblocks(), codes, xscale, s.scale_rows(M));
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (M <= 16) return launch_rows<2, 1, 8>(s, prepared, codes, xscale, M, out, st);
-  if (M <= 128) return launch_rows<4, 4, 4>(s, prepared, codes, xscale, M, out, st);
+  if (M <= 16) {
+    if (deep) return launch_few<1, 1, 16, 2, false>(s, prepared, codes, xscale, x, M, out, st);
+    return launch_few<1, 1, 4, 2, false>(s, prepared, codes, xscale, x, M, out, st);
+  }
+  if (M <= 32) return launch_few<2, 2, 8, 1, false>(s, prepared, codes, xscale, x, M, out, st);
+  if (M <= 128) return launch_few<2, 4, 8, 1, false>(s, prepared, codes, xscale, x, M, out, st);
   const int64_t big = (int64_t)((M + 255) / 256) * ((s.subtiles() + 15) / 16);
   if (big >= 192) return launch_tile<256, 256, 2, 4>(s, prepared, codes, xscale, M, out, st);
   return launch_tile<128, 128, 2, 4>(s, prepared, codes, xscale, M, out, st);
