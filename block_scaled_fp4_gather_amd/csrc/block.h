@@ -55,8 +55,9 @@ hipError_t launch_route(const RouterShape& s, const uint8_t* prepared, const uin
 // accumulators gets the gate and the up of the same output.
 //   codes  [subtile][K block of 128][half][lane][16 B]: lane l holds row
 //          l % 16, K values 128 b + 64 half + 16 (l / 16) .. + 15
-//   scales f32 [subtile][K block]: the scale of the subtile's 128-row block
-//          (128 is a multiple of 16, so a subtile has one)
+//   scales f32 [K block][scale_cols]: the scale of each subtile's 128-row
+//          block (128 is a multiple of 16, so a subtile has one); rows are
+//          long enough to read 64 from any subtile
 // Rows past N and K values past K are zero.
 struct Fp8Shape {
   int K, N;
@@ -68,17 +69,16 @@ struct Fp8Shape {
   MOE_HD int subtiles() const { return halves() * ((N + 15) / 16); }
   MOE_HD int kblocks() const { return (K + 127) / 128; }
   MOE_HD int64_t codes_bytes() const { return (int64_t)subtiles() * kblocks() * 2048; }
-  MOE_HD int64_t prepared_bytes() const { return align256(codes_bytes() + 4ll * subtiles() * kblocks()); }
+  MOE_HD int64_t prepared_bytes() const { return align256(codes_bytes() + 4ll * scale_cols() * kblocks()); }
+  MOE_HD int scale_cols() const { return (subtiles() + 63) / 64 * 64 + 64; }
   // quantised activations: codes [M][128 kblocks], then one scale byte per
   // row and K block, as dwords of 4 K blocks: [kblocks / 4][scale_rows]
   MOE_HD int64_t scale_rows(int64_t M) const { return (M + 255) / 256 * 256; }
   MOE_HD int64_t code_bytes(int64_t M) const { return align256(M * kblocks() * 128); }
-  MOE_HD int64_t workspace(int64_t max_tokens) const {
-    const int64_t M = max_tokens < 1 ? 1 : max_tokens;
-    return code_bytes(M) + (kblocks() + 3) / 4 * 4 * scale_rows(M);
-  }
 };
 
+// Workspace for calls of up to max_tokens tokens.
+int64_t fp8_workspace(const Fp8Shape& s, int64_t max_tokens);
 hipError_t launch_fp8_prepare(const Fp8Shape& s, const uint8_t* codes, const float* scales, uint8_t* prepared,
                               hipStream_t st);
 hipError_t launch_fp8_linear(const Fp8Shape& s, const uint8_t* prepared, const uint16_t* x, int M, uint16_t* out,

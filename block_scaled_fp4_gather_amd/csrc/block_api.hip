@@ -141,7 +141,7 @@ moe_fp4_status moe_fp4_fp8_workspace_bytes(const moe_fp4_fp8_desc* desc, int32_t
   const moe_fp4_status st = fp8_shape(desc, &s);
   if (st != MOE_FP4_OK) return st;
   if (!bytes || M < 0 || M > desc->max_tokens) return MOE_FP4_EINVAL;
-  *bytes = (size_t)s.workspace(desc->max_tokens);
+  *bytes = (size_t)moe::fp8_workspace(s, desc->max_tokens);
   return MOE_FP4_OK;
 }
 
@@ -156,7 +156,7 @@ moe_fp4_status moe_fp4_fp8_linear(const moe_fp4_fp8_desc* desc, const void* prep
   if (!aligned(prepared, 256) || !aligned(x, 16) || !aligned(out, 16) || !aligned(workspace, 256))
     return MOE_FP4_EINVAL;
   if (overlap(x, 2ll * M * s.K, out, 2ll * M * s.N)) return MOE_FP4_EINVAL;
-  if ((int64_t)workspace_bytes < s.workspace(desc->max_tokens)) return MOE_FP4_EWORKSPACE;
+  if ((int64_t)workspace_bytes < moe::fp8_workspace(s, desc->max_tokens)) return MOE_FP4_EWORKSPACE;
   return from_hip(moe::launch_fp8_linear(s, (const uint8_t*)prepared, x, M, out, (uint8_t*)workspace,
                                          (hipStream_t)stream));
 }

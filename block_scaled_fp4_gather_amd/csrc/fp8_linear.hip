@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(256)
     }
     ((uint64_t*)prepared)[2 * it] = v[0];
     ((uint64_t*)prepared)[2 * it + 1] = v[1];
-    if (lane == 0 && half == 0) ps[sb] = scales[((int64_t)part * nb + row / 128) * kb + b];
+    if (lane == 0 && half == 0) ps[(int64_t)b * s.scale_cols() + sub] = scales[((int64_t)part * nb + row / 128) * kb + b];
   }
 }
 
@@ -134,8 +134,8 @@ __global__ void __launch_bounds__(256)
 
 // ---- few tokens: FS subtiles x 16 TT tokens per workgroup, whose NW waves
 // share K in runs of consecutive blocks and join their sums in LDS in wave
-// order.  What bounds it is the time from a load to its use, so each wave
-// loads U blocks' operands while it multiplies the U before.
+// order.  What bounds it is the time from a load to its use, so each wave has
+// the operands of U blocks in flight, if it can its whole run.
 //
 // FUSED: x is quantised by each workgroup itself into LDS (up to kFusedUnits
 // blocks of 128 values), while the first weights are on their way: for the
@@ -144,12 +144,15 @@ __global__ void __launch_bounds__(256)
 template <int NW>
 constexpr int kFusedUnits = 4 * 4 * NW;  // 4 passes of the workgroup's 16-lane groups
 
-template <int FS, int TT, int NW, int U, bool GATED, bool FUSED>
+// HALVES (a gated map): instead of a pair of subtiles a workgroup takes 8 gate
+// rows and the 8 up rows of the same outputs as one operand of 16 rows, so
+// that twice as many workgroups share the weights.
+template <int FS, int TT, int NW, int U, bool GATED, bool HALVES, bool FUSED>
 __global__ void __launch_bounds__(NW * 64)
     fp8_few_kernel(Fp8Shape s, const uint8_t* __restrict__ prepared, const uint8_t* __restrict__ codes,
                    const uint8_t* __restrict__ xscale, const uint16_t* __restrict__ x, int M,
                    uint16_t* __restrict__ out) {
-  static_assert(!GATED || FS % 2 == 0, "whole gate and up pairs");
+  static_assert(!GATED || (HALVES ? FS == 1 : FS % 2 == 0), "whole gate and up pairs");
   static_assert(!FUSED || TT == 1, "few tokens");
   __shared__ f32x4_t part[NW][FS * TT][64];
   __shared__ uint8_t qcodes[FUSED ? kFusedUnits<NW> * 128 : 16], qscale[FUSED ? kFusedUnits<NW> : 16];
@@ -159,6 +162,9 @@ __global__ void __launch_bounds__(NW * 64)
   const int sub0 = blockIdx.x * FS;
   const int64_t tok0 = (int64_t)blockIdx.y * (16 * TT);
   const int r = lane & 15, g = lane >> 4;
+  // HALVES: the half blockIdx.x % 2 of both subtiles of pair blockIdx.x / 2
+  const int hsub = (blockIdx.x & ~1u) + (r >> 3);
+  const int hlane = 16 * g + (blockIdx.x & 1) * 8 + (r & 7);
   const float* const ws = (const float*)(prepared + s.codes_bytes());
   const int per = (kb + NW - 1) / NW, b0 = wave * per, b1 = min(kb, b0 + per);
 
@@ -178,14 +184,20 @@ __global__ void __launch_bounds__(NW * 64)
   auto load = [&](int b, Operands& o) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int bu = min(b + u, kb - 1);  // blocks past the run are loaded and not used
+      // Blocks past the run are loaded and multiplied too, with a scale of 0:
+      // a branch would let the compiler move the loads behind it.  (A NaN in
+      // one is a NaN in the same outputs of the wave whose block it is.)
+      const int bu = min(b + u, kb - 1);
+      const bool in = b + u < b1;
 #pragma unroll
       for (int f = 0; f < FS; ++f) {
-        const int64_t sub = min(sub0 + f, ns - 1);
-        const uint8_t* const at = prepared + (sub * kb + bu) * 2048;
-        const i32x4_t lo = *(const i32x4_t*)(at + lane * 16), hi = *(const i32x4_t*)(at + lane * 16 + 1024);
+        const int64_t sub = HALVES ? hsub : min(sub0 + f, ns - 1);
+        const uint8_t* const at = prepared + (sub * kb + bu) * 2048 + (HALVES ? hlane : lane) * 16;
+        const i32x4_t lo = *(const i32x4_t*)at, hi = *(const i32x4_t*)(at + 1024);
         o.a[u][f] = i32x8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-        o.w[u][f] = ws[sub * kb + bu];
+        // the accumulators' rows are 4 g ..: HALVES, the gate's for g < 2
+        const float w = ws[(int64_t)bu * s.scale_cols() + (HALVES ? (int)(blockIdx.x & ~1u) + (g >> 1) : (int)sub)];
+        o.w[u][f] = in ? w : 0.0f;
       }
       if constexpr (!FUSED)
 #pragma unroll
@@ -204,9 +216,8 @@ __global__ void __launch_bounds__(NW * 64)
   auto multiply = [&](int b, Operands& o) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (b + u >= b1) break;
       if constexpr (FUSED) {
-        const int unit = min(r, M - 1) * kb + b + u;
+        const int unit = min(r, M - 1) * kb + min(b + u, kb - 1);
         const i32x4_t lo = *(const i32x4_t*)(qcodes + unit * 128 + g * 16);
         const i32x4_t hi = *(const i32x4_t*)(qcodes + unit * 128 + g * 16 + 64);
         o.b[u][0] = i32x8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
@@ -224,7 +235,7 @@ __global__ void __launch_bounds__(NW * 64)
     }
   };
 
-  Operands o0, o1;
+  Operands o;
   if constexpr (FUSED) {
     const int units = M * kb;
     uint4 raw[4];
@@ -236,7 +247,7 @@ __global__ void __launch_bounds__(NW * 64)
       if (unit < units && c < s.K) raw[i] = *(const uint4*)(x + (int64_t)row * s.K + c);
     }
     __builtin_amdgcn_sched_barrier(0);  // x first: it is needed first
-    load(b0, o0);
+    load(b0, o);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -250,15 +261,15 @@ __global__ void __launch_bounds__(NW * 64)
     }
     __syncthreads();
   } else {
-    load(b0, o0);
+    load(b0, o);
+    __builtin_amdgcn_sched_barrier(0);
   }
-  for (int b = b0; b < b1; b += 2 * U) {
-    load(b + U, o1);
+  multiply(b0, o);
+#pragma unroll 1
+  for (int b = b0 + U; b < b1; b += U) {
+    load(b, o);
     __builtin_amdgcn_sched_barrier(0);
-    multiply(b, o0);
-    load(b + 2 * U, o0);
-    __builtin_amdgcn_sched_barrier(0);
-    multiply(b + U, o1);
+    multiply(b, o);
   }
 #pragma unroll
   for (int f = 0; f < FS; ++f)
@@ -266,18 +277,19 @@ __global__ void __launch_bounds__(NW * 64)
     for (int t = 0; t < TT; ++t) part[wave][f * TT + t][lane] = acc[f][t];
   __syncthreads();
   // output tiles of 16 features x 16 tokens, dealt to the waves
-  constexpr int kTiles = (GATED ? FS / 2 : FS) * TT;
+  constexpr int kTiles = (GATED && !HALVES ? FS / 2 : FS) * TT;
   for (int o = wave; o < kTiles; o += NW) {
     const int f = o / TT, t = o % TT;
     f32x4_t v{}, u{};
 #pragma unroll
     for (int i = 0; i < NW; ++i) {
-      v += part[i][(GATED ? 2 * f : f) * TT + t][lane];
-      if (GATED) u += part[i][(2 * f + 1) * TT + t][lane];
+      v += part[i][(GATED && !HALVES ? 2 * f : f) * TT + t][lane];
+      if (HALVES) u += part[i][t][lane ^ 32];
+      if (GATED && !HALVES) u += part[i][(2 * f + 1) * TT + t][lane];
     }
-    const int n = (GATED ? sub0 / 2 + f : sub0 + f) * 16 + 4 * g;
+    const int n = HALVES ? blockIdx.x * 8 + 4 * g : (GATED ? sub0 / 2 + f : sub0 + f) * 16 + 4 * g;
     const int64_t m = tok0 + 16 * t + r;
-    if (n >= s.N || m >= M) continue;  // N % 8 == 0: the lane's four outputs are all in or all out
+    if ((HALVES && g >= 2) || n >= s.N || m >= M) continue;  // N % 8 == 0: the lane's four outputs are all in or all out
     if (s.has_act)
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = gated_act(s.act, v[i], u[i]);
@@ -288,27 +300,37 @@ __global__ void __launch_bounds__(NW * 64)
 // ---- many tokens: BM tokens x BN weight rows per workgroup of 8 waves
 // (WT x WF), one K block per step.  Tokens (a row of 128 codes: the 16-byte
 // chunk c of row r at position c ^ row_swz(r)) and weights (in the layout they
-// were prepared in) go to LDS by direct copies, one step ahead in two slots.
-// Every 4 steps the scale dwords of the tokens' next 4 K blocks follow.
-template <int BM, int BN, int WT, int WF>
+// were prepared in) go to LDS by direct copies, SLOTS - 1 steps ahead in a ring
+// of SLOTS, with the scales of the weights and, 4 K blocks to a dword, of the
+// tokens.
+//
+// SPLIT: too few tiles to fill the chip: grid.y slices of K, whose sums go to
+// `part` (f32 [slice][token][prepared row]) for fp8_join_kernel.
+template <int BM, int BN, int WT, int WF, int SLOTS>
 struct Fp8Tile {
   static constexpr int FS = BN / 16 / WF, TT = BM / 16 / WT;
   static constexpr int kTokens = BM * 128, kSlot = kTokens + BN * 128;
   static constexpr int kCopies = kTokens / 1024 / 8, kWCopies = BN / 64, kAllCopies = kCopies + kWCopies;
-  static constexpr int kLds = 2 * kSlot + 2 * 4 * BM;
+  static constexpr int kStep = kAllCopies + 2;  // copies of a wave in a step: tokens, weights, both scales
+  static constexpr int kAhead = SLOTS - 1;
+  // the ring, then the tokens' scales (two groups of 4 K blocks), then the weights' (64 floats a slot)
+  static constexpr int kLds = SLOTS * kSlot + 2 * 4 * BM + SLOTS * 256;
   static_assert(WT * WF == 8 && FS % 2 == 0 && BM % 64 == 0 && BN % 64 == 0,
                 "8 waves, whole gate and up pairs, whole copies");
-  static_assert(kAllCopies + 1 < FS * TT, "copies between the products");
+  static_assert(kStep < FS * TT, "copies between the products");
+  static_assert(kAhead <= 3, "two groups of token scales");
 };
 
-template <int BM, int BN, int WT, int WF, bool GATED>
+template <int BM, int BN, int WT, int WF, int SLOTS, bool GATED, bool SPLIT>
 __global__ void __launch_bounds__(512, 2)
     fp8_tile_kernel(Fp8Shape s, const uint8_t* __restrict__ prepared, const uint8_t* __restrict__ codes,
-                    const uint8_t* __restrict__ xscale, int M, int tiles_m, int tiles_n, uint16_t* __restrict__ out) {
-  using T = Fp8Tile<BM, BN, WT, WF>;
+                    const uint8_t* __restrict__ xscale, int M, int tiles_m, int tiles_n, int slice,
+                    uint16_t* __restrict__ out, float* __restrict__ part) {
+  using T = Fp8Tile<BM, BN, WT, WF, SLOTS>;
   constexpr int FS = T::FS, TT = T::TT;
   extern __shared__ __align__(16) uint8_t smem[];
-  uint8_t* const sring = smem + 2 * T::kSlot;
+  uint8_t* const sring = smem + SLOTS * T::kSlot;  // token scales
+  uint8_t* const wring = sring + 2 * 4 * BM;       // weight scales
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   // Workgroups are dealt to the 8 XCDs in turn: give each XCD a contiguous
@@ -322,10 +344,10 @@ __global__ void __launch_bounds__(512, 2)
   const int tn = in_band / bm, tm = 4 * band + in_band % bm;
 
   const int kb = s.kblocks(), ns = s.subtiles();
+  const int first = SPLIT ? blockIdx.y * slice : 0, end = SPLIT ? min(kb, first + slice) : kb;  // slice % 4 == 0
   const int64_t mp = s.scale_rows(M), tok0 = (int64_t)tm * BM;
   const int wf = wave % WF, wt = wave / WF;
   const int sub0 = tn * (BN / 16) + wf * FS;
-  const float* const ws = (const float*)(prepared + s.codes_bytes());
 
   // token copies of this wave: rows of the tile past the last token repeat it
   const uint8_t* const tile = codes + tok0 * kb * 128;
@@ -336,16 +358,14 @@ __global__ void __launch_bounds__(512, 2)
     const int row = (c * 8 + wave) * 8 + lane / 8;
     src[c] = (uint32_t)min(row, rows - 1) * (kb * 128u) + ((lane & 7) ^ row_swz<128>(row)) * 16;
   }
-  // Scale dwords of K blocks 4q .. 4q + 3 (the scale rows are padded to whole
-  // tiles).  In a step this repeats for 4 steps what the first of them did,
-  // and every wave takes part: a branch in the middle of a step costs more.
-  const uint32_t part = (wave % (BM / 64)) * 256;
-  const uint8_t* const scales = xscale + tok0 * 4 + part;
-  const int last_q = (kb - 1) / 4;
-  auto copy_scales = [&](int q) {
-    const int from = min(q, last_q);
-    dma4_at(scales + from * mp * 4, lane * 4, lds_addr(sring) + (q & 1) * 4 * BM + part);
-  };
+  // Scales: every wave copies them (the same bytes), so that all have the same
+  // number of copies and no branch is in the middle of a step.  The tokens'
+  // rows are padded to whole tiles; a group of 4 K blocks is copied again in
+  // each of its steps.
+  const uint32_t quarter = (wave % (BM / 64)) * 256;
+  const uint8_t* const scales = xscale + tok0 * 4 + quarter;
+  const float* const wscales = (const float*)(prepared + s.codes_bytes()) + tn * (BN / 16);
+  const uint32_t lds_s = lds_addr(sring) + quarter, lds_w = lds_addr(wring);
   // weight copies of this wave: 1 KiB, half a subtile's block, each; subtiles past the last repeat it
   const uint8_t* wsrc[T::kWCopies];
 #pragma unroll
@@ -354,14 +374,20 @@ __global__ void __launch_bounds__(512, 2)
     wsrc[c] = prepared + (int64_t)min(tn * (BN / 16) + kib / 2, ns - 1) * kb * 2048 + (kib & 1) * 1024;
   }
   const uint32_t lds0 = lds_addr(smem) + wave * 1024;
-  auto copy = [&](int b, int ring, int c) {  // copy c of K block b: tokens, then weights
+  // Copy c of step `at`: tokens, weights, their scales.  Past the last block it
+  // is copied again, and not used.
+  auto copy = [&](int at, int c) {
+    const int b = min(at, end - 1), ring = (at - first) % SLOTS;
     const uint32_t to = lds0 + ring * T::kSlot + c * 8192;
     if (c < T::kCopies)
       dma16_at(tile + (int64_t)b * 128, src[c], to);
-    else
+    else if (c < T::kAllCopies)
       dma16_at(wsrc[c - T::kCopies] + (int64_t)b * 2048, lane * 16, to);
+    else if (c == T::kAllCopies)
+      dma4_at(scales + (int64_t)(b >> 2) * mp * 4, lane * 4, lds_s + ((at >> 2) & 1) * 4 * BM);
+    else
+      dma4_at(wscales + (int64_t)b * s.scale_cols(), lane * 4, lds_w + ring * 256);
   };
-  const float* const wscale = ws + (int64_t)min(sub0 + lane % FS, ns - 1) * kb;
   f32x4_t acc[FS][TT];
 #pragma unroll
   for (int f = 0; f < FS; ++f)
@@ -370,23 +396,20 @@ __global__ void __launch_bounds__(512, 2)
 
   const int swz = row_swz<128>(r);  // the same for every 16th row: rows 16 t + r
   const int brow = (wt * TT * 16 + r) * 128, bs = (wt * TT * 16 + r) * 4;
-  float w = wscale[0];
 #pragma unroll
-  for (int c = 0; c < T::kAllCopies; ++c) copy(0, 0, c);
-  copy_scales(0);
+  for (int i = 0; i < T::kAhead; ++i)
+#pragma unroll
+    for (int c = 0; c < T::kStep; ++c) copy(first + i, c);
 #pragma unroll 1
-  for (int b = 0; b < kb; ++b) {
-    vm_wait<0>();     // this wave's copies for step b are here
-    __syncthreads();  // everyone's are, and everyone is done with step b - 1
-    const int next = min(b + 1, kb - 1);  // past the last block it is copied again, and not used
-    float wf_[FS];
-#pragma unroll
-    for (int f = 0; f < FS; ++f) wf_[f] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), f));
-    w = wscale[next];
-    __builtin_amdgcn_sched_barrier(0);
-    const uint8_t* const slot = smem + (b & 1) * T::kSlot + brow;
-    const uint8_t* const wslot = smem + (b & 1) * T::kSlot + T::kTokens + wf * FS * 2048 + lane * 16;
+  for (int b = first; b < end; ++b) {
+    vm_wait<(T::kAhead - 1) * T::kStep>();  // this wave's copies for step b are here, later ones may not be
+    __syncthreads();                        // everyone's are, and everyone is done with step b - 1
+    const int ring = (b - first) % SLOTS;
+    const uint8_t* const slot = smem + ring * T::kSlot + brow;
+    const uint8_t* const wslot = smem + ring * T::kSlot + T::kTokens + wf * FS * 2048 + lane * 16;
     const uint8_t* const sc = sring + ((b >> 2) & 1) * 4 * BM + bs + (b & 3);
+    typedef float scales_t __attribute__((ext_vector_type(FS)));
+    const scales_t w = *(const scales_t*)(wring + ring * 256 + wf * FS * 4);
     auto read = [&](int t, i32x8_t& bop, int& sx) {
       const i32x4_t lo = *(const i32x4_t*)(slot + t * 2048 + (g ^ swz) * 16);
       const i32x4_t hi = *(const i32x4_t*)(slot + t * 2048 + ((4 + g) ^ swz) * 16);
@@ -412,9 +435,8 @@ __global__ void __launch_bounds__(512, 2)
       const int t = i / FS, f = i % FS;
       if (i < kAll) {
         if (f == 0 && t + 1 < TT) read(t + 1, bop[(t + 1) & 1], sx[(t + 1) & 1]);
-        // the next step's copies go between the first products
-        if (i >= 1 && i <= T::kAllCopies) copy(next, (b + 1) & 1, i - 1);
-        if (i == T::kAllCopies + 1) copy_scales((b >> 2) + 1);
+        // a later step's copies go between the first products
+        if (i >= 1 && i <= T::kStep) copy(b + T::kAhead, i - 1);
         p[i % kRing] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[f], bop[t & 1], f32x4_t{}, 0, 0, 0, 127, 0,
                                                                        sx[t & 1]);
         __builtin_amdgcn_sched_barrier(0);
@@ -423,20 +445,31 @@ __global__ void __launch_bounds__(512, 2)
         const int j = i - kLag;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          acc[j % FS][j / FS][e] = fmaf(wf_[j % FS], p[j % kRing][e], acc[j % FS][j / FS][e]);
+          acc[j % FS][j / FS][e] = fmaf(w[j % FS], p[j % kRing][e], acc[j % FS][j / FS][e]);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
   }
   vm_wait<0>();  // no copy may land after the workgroup's LDS is released
 
+  if constexpr (SPLIT) {
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      const int64_t m = tok0 + (wt * TT + t) * 16 + r;
+#pragma unroll
+      for (int f = 0; f < FS; ++f)
+        if (m < M && sub0 + f < ns)
+          *(f32x4_t*)(part + ((blockIdx.y * (int64_t)M + m) * ns + sub0 + f) * 16 + 4 * g) = acc[f][t];
+    }
+    return;
+  }
   __syncthreads();
 
   // Each wave turns its outputs round in its own part of the LDS, so that it
   // stores whole rows of up to 128 bytes: 16-byte chunk c of token row i at
   // position c ^ (i % chunks of a row).
   constexpr int kRow = (GATED ? FS / 2 : FS) * 32, kPer = kRow / 16;
-  static_assert(8 * TT * 16 * kRow <= 2 * T::kSlot, "the waves' parts");
+  static_assert(8 * TT * 16 * kRow <= SLOTS * T::kSlot, "the waves' parts");
   uint8_t* const mine = smem + wave * TT * 16 * kRow;
   auto put = [&](auto kind) {
 #pragma unroll
@@ -473,38 +506,92 @@ __global__ void __launch_bounds__(512, 2)
   }
 }
 
-template <int BM, int BN, int WT, int WF>
+// Joins the slices in order and applies the activation: a thread per four
+// outputs.
+template <bool GATED>
+__global__ void __launch_bounds__(256)
+    fp8_join_kernel(Fp8Shape s, const float* __restrict__ part, int slices, int M, uint16_t* __restrict__ out) {
+  const int quads = s.N / 4;
+  const int64_t m = blockIdx.y;
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= quads) return;
+  const int64_t row = 16 * (int64_t)s.subtiles();
+  const int at = GATED ? (c / 4) * 32 + c % 4 * 4 : c * 4;  // prepared row of the four outputs' gate
+  f32x4_t v{}, u{};
+#pragma unroll 4
+  for (int i = 0; i < slices; ++i) {
+    const float* const p = part + (i * (int64_t)M + m) * row + at;
+    v += *(const f32x4_t*)p;
+    if (GATED) u += *(const f32x4_t*)(p + 16);
+  }
+  if (s.has_act)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = gated_act(s.act, v[i], u[i]);
+  *(uint2*)(out + m * s.N + c * 4) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+}
+
+template <int BM, int BN, int WT, int WF, int SLOTS, bool SPLIT>
 hipError_t launch_tile(const Fp8Shape& s, const uint8_t* prepared, const uint8_t* codes, const uint8_t* xscale, int M,
-                       uint16_t* out, hipStream_t st) {
-  using T = Fp8Tile<BM, BN, WT, WF>;
+                       int slices, int slice, uint16_t* out, float* part, hipStream_t st) {
+  using T = Fp8Tile<BM, BN, WT, WF, SLOTS>;
   const int tm = (M + BM - 1) / BM, tn = (s.subtiles() + BN / 16 - 1) / (BN / 16);
-  const dim3 grid(grid8((int64_t)tm * tn));
+  const dim3 grid(grid8((int64_t)tm * tn), (unsigned)slices);
   if (s.gated)
-    hipLaunchKernelGGL((fp8_tile_kernel<BM, BN, WT, WF, true>), grid, dim3(512), T::kLds, st, s, prepared, codes,
-                       xscale, M, tm, tn, out);
+    hipLaunchKernelGGL((fp8_tile_kernel<BM, BN, WT, WF, SLOTS, true, SPLIT>), grid, dim3(512), T::kLds, st, s, prepared, codes,
+                       xscale, M, tm, tn, slice, out, part);
   else
-    hipLaunchKernelGGL((fp8_tile_kernel<BM, BN, WT, WF, false>), grid, dim3(512), T::kLds, st, s, prepared, codes,
-                       xscale, M, tm, tn, out);
+    hipLaunchKernelGGL((fp8_tile_kernel<BM, BN, WT, WF, SLOTS, false, SPLIT>), grid, dim3(512), T::kLds, st, s, prepared,
+                       codes, xscale, M, tm, tn, slice, out, part);
   return hipGetLastError();
 }
 
 template <int FS, int TT, int NW, int U, bool FUSED>
 hipError_t launch_few(const Fp8Shape& s, const uint8_t* prepared, const uint8_t* codes, const uint8_t* xscale,
                       const uint16_t* x, int M, uint16_t* out, hipStream_t st) {
-  // a gated map takes its subtiles in pairs
-  constexpr int GFS = FS % 2 ? 2 * FS : FS;
-  const int fs = s.gated ? GFS : FS;
-  const dim3 grid((unsigned)((s.subtiles() + fs - 1) / fs), (unsigned)((M + 16 * TT - 1) / (16 * TT)));
+  // a gated map takes pairs of subtiles, or with FS = 1 half of a pair: as many workgroups either way
+  constexpr bool kHalves = FS == 1;
+  const dim3 grid((unsigned)((s.subtiles() + FS - 1) / FS), (unsigned)((M + 16 * TT - 1) / (16 * TT)));
   if (s.gated)
-    hipLaunchKernelGGL((fp8_few_kernel<GFS, TT, NW, U, true, FUSED>), grid, dim3(NW * 64), 0, st, s, prepared, codes,
+    hipLaunchKernelGGL((fp8_few_kernel<FS, TT, NW, U, true, kHalves, FUSED>), grid, dim3(NW * 64), 0, st, s, prepared, codes,
                        xscale, x, M, out);
   else
-    hipLaunchKernelGGL((fp8_few_kernel<FS, TT, NW, U, false, FUSED>), grid, dim3(NW * 64), 0, st, s, prepared, codes,
+    hipLaunchKernelGGL((fp8_few_kernel<FS, TT, NW, U, false, false, FUSED>), grid, dim3(NW * 64), 0, st, s, prepared, codes,
                        xscale, x, M, out);
   return hipGetLastError();
 }
 
+// Slices of K for M tokens on 128 x 128 tiles: as many as fill the CUs, at
+// least 4 K blocks each.
+struct Fp8Slices {
+  int count, blocks;
+};
+
+Fp8Slices fp8_slices(const Fp8Shape& s, int64_t M) {
+  const int64_t tiles = ((M + 127) / 128) * ((s.subtiles() + 7) / 8);
+  const int kb = s.kblocks();
+  int64_t count = tiles > 128 ? 1 : 256 / tiles;
+  if (count > 8) count = 8;
+  const int quads = (kb + 3) / 4;
+  if (count > quads) count = quads;
+  const int blocks = (int)((quads + count - 1) / count) * 4;
+  return Fp8Slices{(kb + blocks - 1) / blocks, blocks};
+}
+
 }  // namespace
+
+int64_t fp8_workspace(const Fp8Shape& s, int64_t max_tokens) {
+  // codes and scales, then the slices' sums; these grow with M but for steps
+  // where the number of slices falls, so they are largest at a full last tile
+  // or at the last M
+  const int64_t last = max_tokens < 1 ? 1 : max_tokens;
+  auto sums = [&](int64_t M) {
+    const int count = fp8_slices(s, M).count;
+    return count == 1 ? 0 : count * M * s.subtiles() * 64;
+  };
+  int64_t most = sums(last);
+  for (int64_t M = 128; M < last && M <= 128 * 128; M += 128) most = sums(M) > most ? sums(M) : most;
+  return s.code_bytes(last) + (s.kblocks() + 3) / 4 * 4 * s.scale_rows(last) + align256(most);
+}
 
 hipError_t launch_fp8_prepare(const Fp8Shape& s, const uint8_t* codes, const float* scales, uint8_t* prepared,
                               hipStream_t st) {
@@ -518,24 +605,34 @@ hipError_t launch_fp8_linear(const Fp8Shape& s, const uint8_t* prepared, const u
                              uint8_t* ws, hipStream_t st) {
   uint8_t* const codes = ws;
   uint8_t* const xscale = ws + s.code_bytes(M);
-  const bool deep = s.kblocks() > 16;  // enough blocks for 16 waves
-  if (M <= 4 && M * s.kblocks() <= (deep ? kFusedUnits<16> : kFusedUnits<4>)) {
-    if (deep) return launch_few<1, 1, 16, 2, true>(s, prepared, codes, xscale, x, M, out, st);
-    return launch_few<1, 1, 4, 2, true>(s, prepared, codes, xscale, x, M, out, st);
-  }
+  const int kb = s.kblocks();
+#define MOE_FEW(...) launch_few<__VA_ARGS__>(s, prepared, codes, xscale, x, M, out, st)
+  if (M <= 4 && M * kb <= (kb > 16 ? kFusedUnits<16> : kFusedUnits<4>))
+    return kb > 32 && M * kb <= kFusedUnits<8> ? MOE_FEW(1, 1, 8, 4, true)
+           : kb > 32 ? MOE_FEW(1, 1, 16, 4, true) : kb > 16 ? MOE_FEW(1, 1, 16, 2, true)
+           : kb > 4 ? MOE_FEW(1, 1, 4, 4, true) : MOE_FEW(1, 1, 4, 1, true);
   hipLaunchKernelGGL(fp8_quantize_rows, dim3((unsigned)((M + 3) / 4), (unsigned)((s.kblocks() + 3) / 4)), dim3(256), 0,
                      st, x, M, s.K, s.kblocks(), codes, xscale, s.scale_rows(M));
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (M <= 16) {
-    if (deep) return launch_few<1, 1, 16, 2, false>(s, prepared, codes, xscale, x, M, out, st);
-    return launch_few<1, 1, 4, 2, false>(s, prepared, codes, xscale, x, M, out, st);
-  }
-  if (M <= 32) return launch_few<2, 2, 8, 1, false>(s, prepared, codes, xscale, x, M, out, st);
-  if (M <= 128) return launch_few<2, 4, 8, 1, false>(s, prepared, codes, xscale, x, M, out, st);
+  if (M <= 16)
+    return kb > 16 ? MOE_FEW(1, 1, 16, 2, false) : kb > 4 ? MOE_FEW(1, 1, 4, 4, false) : MOE_FEW(1, 1, 4, 1, false);
+  if (M <= 32) return MOE_FEW(2, 2, 8, 2, false);
+  if (M <= 128) return MOE_FEW(2, 4, 8, 1, false);
+#undef MOE_FEW
   const int64_t big = (int64_t)((M + 255) / 256) * ((s.subtiles() + 15) / 16);
-  if (big >= 192) return launch_tile<256, 256, 2, 4>(s, prepared, codes, xscale, M, out, st);
-  return launch_tile<128, 128, 2, 4>(s, prepared, codes, xscale, M, out, st);
+  if (big >= 192) return launch_tile<256, 256, 2, 4, 2, false>(s, prepared, codes, xscale, M, 1, kb, out, nullptr, st);
+  const Fp8Slices p = fp8_slices(s, M);
+  if (p.count == 1) return launch_tile<128, 128, 2, 4, 4, false>(s, prepared, codes, xscale, M, 1, kb, out, nullptr, st);
+  float* const part = (float*)(xscale + (kb + 3) / 4 * 4 * s.scale_rows(M));
+  e = launch_tile<128, 128, 2, 4, 4, true>(s, prepared, codes, xscale, M, p.count, p.blocks, out, part, st);
+  if (e != hipSuccess) return e;
+  const dim3 grid((unsigned)((s.N / 4 + 255) / 256), (unsigned)M);
+  if (s.gated)
+    hipLaunchKernelGGL(fp8_join_kernel<true>, grid, dim3(256), 0, st, s, part, p.count, M, out);
+  else
+    hipLaunchKernelGGL(fp8_join_kernel<false>, grid, dim3(256), 0, st, s, part, p.count, M, out);
+  return hipGetLastError();
 }
 
 }  // namespace moe
