@@ -71,10 +71,13 @@ struct Fp8Shape {
   MOE_HD int64_t codes_bytes() const { return (int64_t)subtiles() * kblocks() * 2048; }
   MOE_HD int64_t prepared_bytes() const { return align256(codes_bytes() + 4ll * scale_cols() * kblocks()); }
   MOE_HD int scale_cols() const { return (subtiles() + 63) / 64 * 64 + 64; }
-  // quantised activations: codes [M][128 kblocks], then one scale byte per
-  // row and K block, as dwords of 4 K blocks: [kblocks / 4][scale_rows]
+  // Quantised activations: codes as the weights', [16 tokens][K block][half]
+  // [lane][16 B], zeros past the last token; then one scale byte per token and
+  // K block, as dwords of 4 K blocks: [kblocks / 4][scale_rows].  (Rows of K
+  // bytes would put the rows that a tile takes of a K block on few of the L2's
+  // channels where K is a multiple of a large power of two.)
   MOE_HD int64_t scale_rows(int64_t M) const { return (M + 255) / 256 * 256; }
-  MOE_HD int64_t code_bytes(int64_t M) const { return align256(M * kblocks() * 128); }
+  MOE_HD int64_t code_bytes(int64_t M) const { return (M + 15) / 16 * kblocks() * 2048; }
 };
 
 // Workspace for calls of up to max_tokens tokens.

@@ -113,23 +113,42 @@ __device__ __forceinline__ uint2 quantise8(const uint4& raw, uint32_t& byte) {
   return make_uint2((uint32_t)lo, (uint32_t)hi);
 }
 
-// One wave per row and 4 K blocks (a scale dword).
+// A workgroup per 16 tokens and 4 K blocks (a scale dword): each wave takes 4
+// tokens, 1 KiB of each at a time, and the codes are put in operand order in
+// LDS.
 __global__ void __launch_bounds__(256)
     fp8_quantize_rows(const uint16_t* __restrict__ x, int M, int K, int kb, uint8_t* __restrict__ codes,
                       uint8_t* __restrict__ scales, int64_t scale_rows) {
-  const int lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  __shared__ uint4 turned[512];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t group = blockIdx.x;
   const int q = blockIdx.y;
-  if (row >= M) return;
   const int c = (q * 64 + lane) * 8;
-  uint4 raw = make_uint4(0, 0, 0, 0);
-  if (c < K) raw = *(const uint4*)(x + row * K + c);
-  uint32_t byte;
-  const uint2 code = quantise8(raw, byte);
-  if (c < kb * 128) *(uint2*)(codes + row * kb * 128 + c) = code;
-  const uint32_t dword = __builtin_amdgcn_readlane(byte, 0) | __builtin_amdgcn_readlane(byte, 16) << 8 |
-                         __builtin_amdgcn_readlane(byte, 32) << 16 | __builtin_amdgcn_readlane(byte, 48) << 24;
-  if (lane == 0) *(uint32_t*)(scales + (q * scale_rows + row) * 4) = dword;
+  uint4 raw[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = group * 16 + wave * 4 + i;
+    raw[i] = make_uint4(0, 0, 0, 0);
+    if (c < K && row < M) raw[i] = *(const uint4*)(x + row * K + c);
+  }
+  // this lane's 8 codes: block lane / 16 of the four, half, group and place of its 16-byte chunk
+  const int chunk = (lane / 8) * 64 + (lane % 8) / 2 * 16;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = wave * 4 + i;
+    uint32_t byte;
+    const uint2 code = quantise8(raw[i], byte);
+    ((uint2*)turned)[(chunk + r) * 2 + lane % 2] = code;
+    const uint32_t dword = __builtin_amdgcn_readlane(byte, 0) | __builtin_amdgcn_readlane(byte, 16) << 8 |
+                           __builtin_amdgcn_readlane(byte, 32) << 16 | __builtin_amdgcn_readlane(byte, 48) << 24;
+    if (lane == 0 && group * 16 + r < M) *(uint32_t*)(scales + (q * scale_rows + group * 16 + r) * 4) = dword;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int at = i * 256 + threadIdx.x;  // 16-byte chunk of the four blocks
+    if (q * 4 + at / 128 < kb) ((uint4*)(codes + (group * kb + q * 4) * 2048))[at] = turned[at];
+  }
 }
 
 // ---- few tokens: FS subtiles x 16 TT tokens per workgroup, whose NW waves
@@ -173,13 +192,13 @@ __global__ void __launch_bounds__(NW * 64)
     int sx[U][TT];
     float w[U][FS];
   };
-  const uint8_t* xrow[TT];
+  const uint8_t* xgroup[TT];
   const uint8_t* srow[TT];
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
-    const int64_t m = min(tok0 + 16 * t + r, (int64_t)M - 1);  // rows past M repeat the last one and are not stored
-    xrow[t] = codes + m * kb * 128 + g * 16;
-    srow[t] = xscale + m * 4;
+    const int64_t last = (M - 1) / 16, group = min(tok0 / 16 + t, last);  // past the last group it is repeated
+    xgroup[t] = codes + group * kb * 2048 + lane * 16;
+    srow[t] = xscale + (group * 16 + r) * 4;
   }
   auto load = [&](int b, Operands& o) {
 #pragma unroll
@@ -202,7 +221,8 @@ __global__ void __launch_bounds__(NW * 64)
       if constexpr (!FUSED)
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-          const i32x4_t lo = *(const i32x4_t*)(xrow[t] + bu * 128), hi = *(const i32x4_t*)(xrow[t] + bu * 128 + 64);
+          const uint8_t* const at = xgroup[t] + bu * 2048;
+          const i32x4_t lo = *(const i32x4_t*)at, hi = *(const i32x4_t*)(at + 1024);
           o.b[u][t] = i32x8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
           o.sx[u][t] = srow[t][(bu >> 2) * mp * 4 + (bu & 3)];
         }
@@ -298,11 +318,9 @@ __global__ void __launch_bounds__(NW * 64)
 }
 
 // ---- many tokens: BM tokens x BN weight rows per workgroup of 8 waves
-// (WT x WF), one K block per step.  Tokens (a row of 128 codes: the 16-byte
-// chunk c of row r at position c ^ row_swz(r)) and weights (in the layout they
-// were prepared in) go to LDS by direct copies, SLOTS - 1 steps ahead in a ring
-// of SLOTS, with the scales of the weights and, 4 K blocks to a dword, of the
-// tokens.
+// (WT x WF), one K block per step.  Tokens and weights, both in operand order,
+// go to LDS by direct copies, SLOTS - 1 steps ahead in a ring of SLOTS, with
+// the scales of the weights and, 4 K blocks to a dword, of the tokens.
 //
 // SPLIT: too few tiles to fill the chip: grid.y slices of K, whose sums go to
 // `part` (f32 [slice][token][prepared row]) for fp8_join_kernel.
@@ -349,14 +367,14 @@ __global__ void __launch_bounds__(512, 2)
   const int wf = wave % WF, wt = wave / WF;
   const int sub0 = tn * (BN / 16) + wf * FS;
 
-  // token copies of this wave: rows of the tile past the last token repeat it
-  const uint8_t* const tile = codes + tok0 * kb * 128;
-  const int rows = (int)min((int64_t)M - tok0, (int64_t)BM);
-  uint32_t src[T::kCopies];  // at most 255 rows of 2^20 bytes
+  // copies of this wave: 1 KiB, half a K block of 16 tokens or of a subtile, each; past the last it is repeated
+  const uint8_t* src[T::kAllCopies];
 #pragma unroll
-  for (int c = 0; c < T::kCopies; ++c) {
-    const int row = (c * 8 + wave) * 8 + lane / 8;
-    src[c] = (uint32_t)min(row, rows - 1) * (kb * 128u) + ((lane & 7) ^ row_swz<128>(row)) * 16;
+  for (int c = 0; c < T::kAllCopies; ++c) {
+    const int kib = (c < T::kCopies ? c : c - T::kCopies) * 8 + wave;
+    const int64_t last = (M - 1) / 16;
+    src[c] = c < T::kCopies ? codes + min(tok0 / 16 + kib / 2, last) * kb * 2048 + (kib & 1) * 1024
+                            : prepared + (int64_t)min(tn * (BN / 16) + kib / 2, ns - 1) * kb * 2048 + (kib & 1) * 1024;
   }
   // Scales: every wave copies them (the same bytes), so that all have the same
   // number of copies and no branch is in the middle of a step.  The tokens'
@@ -366,23 +384,14 @@ __global__ void __launch_bounds__(512, 2)
   const uint8_t* const scales = xscale + tok0 * 4 + quarter;
   const float* const wscales = (const float*)(prepared + s.codes_bytes()) + tn * (BN / 16);
   const uint32_t lds_s = lds_addr(sring) + quarter, lds_w = lds_addr(wring);
-  // weight copies of this wave: 1 KiB, half a subtile's block, each; subtiles past the last repeat it
-  const uint8_t* wsrc[T::kWCopies];
-#pragma unroll
-  for (int c = 0; c < T::kWCopies; ++c) {
-    const int kib = c * 8 + wave;
-    wsrc[c] = prepared + (int64_t)min(tn * (BN / 16) + kib / 2, ns - 1) * kb * 2048 + (kib & 1) * 1024;
-  }
   const uint32_t lds0 = lds_addr(smem) + wave * 1024;
   // Copy c of step `at`: tokens, weights, their scales.  Past the last block it
   // is copied again, and not used.
   auto copy = [&](int at, int c) {
     const int b = min(at, end - 1), ring = (at - first) % SLOTS;
     const uint32_t to = lds0 + ring * T::kSlot + c * 8192;
-    if (c < T::kCopies)
-      dma16_at(tile + (int64_t)b * 128, src[c], to);
-    else if (c < T::kAllCopies)
-      dma16_at(wsrc[c - T::kCopies] + (int64_t)b * 2048, lane * 16, to);
+    if (c < T::kAllCopies)
+      dma16_at(src[c] + (int64_t)b * 2048, lane * 16, to);
     else if (c == T::kAllCopies)
       dma4_at(scales + (int64_t)(b >> 2) * mp * 4, lane * 4, lds_s + ((at >> 2) & 1) * 4 * BM);
     else
@@ -394,8 +403,7 @@ __global__ void __launch_bounds__(512, 2)
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[f][t] = f32x4_t{};
 
-  const int swz = row_swz<128>(r);  // the same for every 16th row: rows 16 t + r
-  const int brow = (wt * TT * 16 + r) * 128, bs = (wt * TT * 16 + r) * 4;
+  const int brow = wt * TT * 2048 + lane * 16, bs = (wt * TT * 16 + r) * 4;
 #pragma unroll
   for (int i = 0; i < T::kAhead; ++i)
 #pragma unroll
@@ -411,8 +419,7 @@ __global__ void __launch_bounds__(512, 2)
     typedef float scales_t __attribute__((ext_vector_type(FS)));
     const scales_t w = *(const scales_t*)(wring + ring * 256 + wf * FS * 4);
     auto read = [&](int t, i32x8_t& bop, int& sx) {
-      const i32x4_t lo = *(const i32x4_t*)(slot + t * 2048 + (g ^ swz) * 16);
-      const i32x4_t hi = *(const i32x4_t*)(slot + t * 2048 + ((4 + g) ^ swz) * 16);
+      const i32x4_t lo = *(const i32x4_t*)(slot + t * 2048), hi = *(const i32x4_t*)(slot + t * 2048 + 1024);
       bop = i32x8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
       sx = sc[t * 64];
     };
@@ -611,7 +618,7 @@ hipError_t launch_fp8_linear(const Fp8Shape& s, const uint8_t* prepared, const u
     return kb > 32 && M * kb <= kFusedUnits<8> ? MOE_FEW(1, 1, 8, 4, true)
            : kb > 32 ? MOE_FEW(1, 1, 16, 4, true) : kb > 16 ? MOE_FEW(1, 1, 16, 2, true)
            : kb > 4 ? MOE_FEW(1, 1, 4, 4, true) : MOE_FEW(1, 1, 4, 1, true);
-  hipLaunchKernelGGL(fp8_quantize_rows, dim3((unsigned)((M + 3) / 4), (unsigned)((s.kblocks() + 3) / 4)), dim3(256), 0,
+  hipLaunchKernelGGL(fp8_quantize_rows, dim3((unsigned)((M + 15) / 16), (unsigned)((s.kblocks() + 3) / 4)), dim3(256), 0,
                      st, x, M, s.K, s.kblocks(), codes, xscale, s.scale_rows(M));
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
