@@ -329,7 +329,7 @@ struct Fp8Tile {
   static constexpr int FS = BN / 16 / WF, TT = BM / 16 / WT;
   static constexpr int kTokens = BM * 128, kSlot = kTokens + BN * 128;
   static constexpr int kCopies = kTokens / 1024 / 8, kWCopies = BN / 64, kAllCopies = kCopies + kWCopies;
-  static constexpr int kStep = kAllCopies + 2;  // copies of a wave in a step: tokens, weights, both scales
+  static constexpr int kStep = kAllCopies + 1;  // copies of a wave in a step: tokens, weights, scales
   static constexpr int kAhead = SLOTS - 1;
   // the ring, then the tokens' scales (two groups of 4 K blocks), then the weights' (64 floats a slot)
   static constexpr int kLds = SLOTS * kSlot + 2 * 4 * BM + SLOTS * 256;
@@ -376,14 +376,15 @@ __global__ void __launch_bounds__(512, 2)
     src[c] = c < T::kCopies ? codes + min(tok0 / 16 + kib / 2, last) * kb * 2048 + (kib & 1) * 1024
                             : prepared + (int64_t)min(tn * (BN / 16) + kib / 2, ns - 1) * kb * 2048 + (kib & 1) * 1024;
   }
-  // Scales: every wave copies them (the same bytes), so that all have the same
-  // number of copies and no branch is in the middle of a step.  The tokens'
-  // rows are padded to whole tiles; a group of 4 K blocks is copied again in
-  // each of its steps.
-  const uint32_t quarter = (wave % (BM / 64)) * 256;
-  const uint8_t* const scales = xscale + tok0 * 4 + quarter;
-  const float* const wscales = (const float*)(prepared + s.codes_bytes()) + tn * (BN / 16);
-  const uint32_t lds_s = lds_addr(sring) + quarter, lds_w = lds_addr(wring);
+  // Scales: one copy per wave and step, so that all waves have the same number
+  // of copies and no branch is in the middle of a step: the first BM / 64
+  // waves the tokens' (rows padded to whole tiles; a group of 4 K blocks is
+  // copied again in each of its steps), the others the weights'.
+  const bool of_tokens = wave < BM / 64;
+  const uint8_t* const scales =
+      of_tokens ? xscale + (tok0 + wave * 64) * 4 : prepared + s.codes_bytes() + tn * (BN / 16) * 4;
+  const int64_t scale_stride = of_tokens ? mp * 4 : (int64_t)s.scale_cols() * 4;
+  const uint32_t lds_scale = of_tokens ? lds_addr(sring) + wave * 256 : lds_addr(wring);
   const uint32_t lds0 = lds_addr(smem) + wave * 1024;
   // Copy c of step `at`: tokens, weights, their scales.  Past the last block it
   // is copied again, and not used.
@@ -392,10 +393,9 @@ __global__ void __launch_bounds__(512, 2)
     const uint32_t to = lds0 + ring * T::kSlot + c * 8192;
     if (c < T::kAllCopies)
       dma16_at(src[c] + (int64_t)b * 2048, lane * 16, to);
-    else if (c == T::kAllCopies)
-      dma4_at(scales + (int64_t)(b >> 2) * mp * 4, lane * 4, lds_s + ((at >> 2) & 1) * 4 * BM);
     else
-      dma4_at(wscales + (int64_t)b * s.scale_cols(), lane * 4, lds_w + ring * 256);
+      dma4_at(scales + (of_tokens ? b >> 2 : b) * scale_stride, lane * 4,
+              lds_scale + (of_tokens ? ((at >> 2) & 1) * 4 * BM : ring * 256));
   };
   f32x4_t acc[FS][TT];
 #pragma unroll
