@@ -321,9 +321,6 @@ __global__ void __launch_bounds__(NW * 64)
 // (WT x WF), one K block per step.  Tokens and weights, both in operand order,
 // go to LDS by direct copies, SLOTS - 1 steps ahead in a ring of SLOTS, with
 // the scales of the weights and, 4 K blocks to a dword, of the tokens.
-//
-// SPLIT: too few tiles to fill the chip: grid.y slices of K, whose sums go to
-// `part` (f32 [slice][token][prepared row]) for fp8_join_kernel.
 template <int BM, int BN, int WT, int WF, int SLOTS>
 struct Fp8Tile {
   static constexpr int FS = BN / 16 / WF, TT = BM / 16 / WT;
@@ -339,11 +336,11 @@ struct Fp8Tile {
   static_assert(kAhead <= 3, "two groups of token scales");
 };
 
-template <int BM, int BN, int WT, int WF, int SLOTS, bool GATED, bool SPLIT>
+template <int BM, int BN, int WT, int WF, int SLOTS, bool GATED>
 __global__ void __launch_bounds__(512, 2)
     fp8_tile_kernel(Fp8Shape s, const uint8_t* __restrict__ prepared, const uint8_t* __restrict__ codes,
-                    const uint8_t* __restrict__ xscale, int M, int tiles_m, int tiles_n, int slice,
-                    uint16_t* __restrict__ out, float* __restrict__ part) {
+                    const uint8_t* __restrict__ xscale, int M, int tiles_m, int tiles_n,
+                    uint16_t* __restrict__ out) {
   using T = Fp8Tile<BM, BN, WT, WF, SLOTS>;
   constexpr int FS = T::FS, TT = T::TT;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -362,7 +359,6 @@ __global__ void __launch_bounds__(512, 2)
   const int tn = in_band / bm, tm = 4 * band + in_band % bm;
 
   const int kb = s.kblocks(), ns = s.subtiles();
-  const int first = SPLIT ? blockIdx.y * slice : 0, end = SPLIT ? min(kb, first + slice) : kb;  // slice % 4 == 0
   const int64_t mp = s.scale_rows(M), tok0 = (int64_t)tm * BM;
   const int wf = wave % WF, wt = wave / WF;
   const int sub0 = tn * (BN / 16) + wf * FS;
@@ -389,7 +385,7 @@ __global__ void __launch_bounds__(512, 2)
   // Copy c of step `at`: tokens, weights, their scales.  Past the last block it
   // is copied again, and not used.
   auto copy = [&](int at, int c) {
-    const int b = min(at, end - 1), ring = (at - first) % SLOTS;
+    const int b = min(at, kb - 1), ring = at % SLOTS;
     const uint32_t to = lds0 + ring * T::kSlot + c * 8192;
     if (c < T::kAllCopies)
       dma16_at(src[c] + (int64_t)b * 2048, lane * 16, to);
@@ -407,12 +403,12 @@ __global__ void __launch_bounds__(512, 2)
 #pragma unroll
   for (int i = 0; i < T::kAhead; ++i)
 #pragma unroll
-    for (int c = 0; c < T::kStep; ++c) copy(first + i, c);
+    for (int c = 0; c < T::kStep; ++c) copy(i, c);
 #pragma unroll 1
-  for (int b = first; b < end; ++b) {
+  for (int b = 0; b < kb; ++b) {
     vm_wait<(T::kAhead - 1) * T::kStep>();  // this wave's copies for step b are here, later ones may not be
     __syncthreads();                        // everyone's are, and everyone is done with step b - 1
-    const int ring = (b - first) % SLOTS;
+    const int ring = b % SLOTS;
     const uint8_t* const slot = smem + ring * T::kSlot + brow;
     const uint8_t* const wslot = smem + ring * T::kSlot + T::kTokens + wf * FS * 2048 + lane * 16;
     const uint8_t* const sc = sring + ((b >> 2) & 1) * 4 * BM + bs + (b & 3);
@@ -459,17 +455,6 @@ __global__ void __launch_bounds__(512, 2)
   }
   vm_wait<0>();  // no copy may land after the workgroup's LDS is released
 
-  if constexpr (SPLIT) {
-#pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      const int64_t m = tok0 + (wt * TT + t) * 16 + r;
-#pragma unroll
-      for (int f = 0; f < FS; ++f)
-        if (m < M && sub0 + f < ns)
-          *(f32x4_t*)(part + ((blockIdx.y * (int64_t)M + m) * ns + sub0 + f) * 16 + 4 * g) = acc[f][t];
-    }
-    return;
-  }
   __syncthreads();
 
   // Each wave turns its outputs round in its own part of the LDS, so that it
@@ -513,42 +498,18 @@ __global__ void __launch_bounds__(512, 2)
   }
 }
 
-// Joins the slices in order and applies the activation: a thread per four
-// outputs.
-template <bool GATED>
-__global__ void __launch_bounds__(256)
-    fp8_join_kernel(Fp8Shape s, const float* __restrict__ part, int slices, int M, uint16_t* __restrict__ out) {
-  const int quads = s.N / 4;
-  const int64_t m = blockIdx.y;
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= quads) return;
-  const int64_t row = 16 * (int64_t)s.subtiles();
-  const int at = GATED ? (c / 4) * 32 + c % 4 * 4 : c * 4;  // prepared row of the four outputs' gate
-  f32x4_t v{}, u{};
-#pragma unroll 4
-  for (int i = 0; i < slices; ++i) {
-    const float* const p = part + (i * (int64_t)M + m) * row + at;
-    v += *(const f32x4_t*)p;
-    if (GATED) u += *(const f32x4_t*)(p + 16);
-  }
-  if (s.has_act)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = gated_act(s.act, v[i], u[i]);
-  *(uint2*)(out + m * s.N + c * 4) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-}
-
-template <int BM, int BN, int WT, int WF, int SLOTS, bool SPLIT>
+template <int BM, int BN, int WT, int WF, int SLOTS>
 hipError_t launch_tile(const Fp8Shape& s, const uint8_t* prepared, const uint8_t* codes, const uint8_t* xscale, int M,
-                       int slices, int slice, uint16_t* out, float* part, hipStream_t st) {
+                       uint16_t* out, hipStream_t st) {
   using T = Fp8Tile<BM, BN, WT, WF, SLOTS>;
   const int tm = (M + BM - 1) / BM, tn = (s.subtiles() + BN / 16 - 1) / (BN / 16);
-  const dim3 grid(grid8((int64_t)tm * tn), (unsigned)slices);
+  const dim3 grid(grid8((int64_t)tm * tn));
   if (s.gated)
-    hipLaunchKernelGGL((fp8_tile_kernel<BM, BN, WT, WF, SLOTS, true, SPLIT>), grid, dim3(512), T::kLds, st, s, prepared, codes,
-                       xscale, M, tm, tn, slice, out, part);
+    hipLaunchKernelGGL((fp8_tile_kernel<BM, BN, WT, WF, SLOTS, true>), grid, dim3(512), T::kLds, st, s, prepared, codes,
+                       xscale, M, tm, tn, out);
   else
-    hipLaunchKernelGGL((fp8_tile_kernel<BM, BN, WT, WF, SLOTS, false, SPLIT>), grid, dim3(512), T::kLds, st, s, prepared,
-                       codes, xscale, M, tm, tn, slice, out, part);
+    hipLaunchKernelGGL((fp8_tile_kernel<BM, BN, WT, WF, SLOTS, false>), grid, dim3(512), T::kLds, st, s, prepared, codes,
+                       xscale, M, tm, tn, out);
   return hipGetLastError();
 }
 
@@ -567,37 +528,11 @@ hipError_t launch_few(const Fp8Shape& s, const uint8_t* prepared, const uint8_t*
   return hipGetLastError();
 }
 
-// Slices of K for M tokens on 128 x 128 tiles: as many as fill the CUs, at
-// least 4 K blocks each.
-struct Fp8Slices {
-  int count, blocks;
-};
-
-Fp8Slices fp8_slices(const Fp8Shape& s, int64_t M) {
-  const int64_t tiles = ((M + 127) / 128) * ((s.subtiles() + 7) / 8);
-  const int kb = s.kblocks();
-  int64_t count = tiles > 128 ? 1 : 256 / tiles;
-  if (count > 8) count = 8;
-  const int quads = (kb + 3) / 4;
-  if (count > quads) count = quads;
-  const int blocks = (int)((quads + count - 1) / count) * 4;
-  return Fp8Slices{(kb + blocks - 1) / blocks, blocks};
-}
-
 }  // namespace
 
 int64_t fp8_workspace(const Fp8Shape& s, int64_t max_tokens) {
-  // codes and scales, then the slices' sums; these grow with M but for steps
-  // where the number of slices falls, so they are largest at a full last tile
-  // or at the last M
   const int64_t last = max_tokens < 1 ? 1 : max_tokens;
-  auto sums = [&](int64_t M) {
-    const int count = fp8_slices(s, M).count;
-    return count == 1 ? 0 : count * M * s.subtiles() * 64;
-  };
-  int64_t most = sums(last);
-  for (int64_t M = 128; M < last && M <= 128 * 128; M += 128) most = sums(M) > most ? sums(M) : most;
-  return s.code_bytes(last) + (s.kblocks() + 3) / 4 * 4 * s.scale_rows(last) + align256(most);
+  return s.code_bytes(last) + (s.kblocks() + 3) / 4 * 4 * s.scale_rows(last);
 }
 
 hipError_t launch_fp8_prepare(const Fp8Shape& s, const uint8_t* codes, const float* scales, uint8_t* prepared,
@@ -625,21 +560,18 @@ hipError_t launch_fp8_linear(const Fp8Shape& s, const uint8_t* prepared, const u
   if (M <= 16)
     return kb > 16 ? MOE_FEW(1, 1, 16, 2, false) : kb > 4 ? MOE_FEW(1, 1, 4, 4, false) : MOE_FEW(1, 1, 4, 1, false);
   if (M <= 32) return MOE_FEW(2, 2, 8, 2, false);
-  if (M <= 128) return MOE_FEW(2, 4, 8, 1, false);
+  // Up to two workgroups of 64 tokens x 64 rows per CU the tiles are no match:
+  // K4096 N4096, M = 256: 14.5 against 20.9 us, M = 512: 23.1 against 25.5;
+  // K1024 N1024, M = 512: 7.7 against 14.3.  Past it they are: K2048 N7168,
+  // M = 320: 15.9 against 21.0.  With 32 rows each while that leaves one per
+  // CU: K4096 N4096, M = 128: 11.7 against 14.4, M = 256: 16.3 against 14.5.
+  const int64_t groups = (M + 63) / 64;
+  if (groups * ((s.subtiles() + 1) / 2) <= 256) return MOE_FEW(2, 4, 8, 1, false);
+  if (groups * ((s.subtiles() + 3) / 4) <= 512) return MOE_FEW(4, 4, 8, 1, false);
 #undef MOE_FEW
   const int64_t big = (int64_t)((M + 255) / 256) * ((s.subtiles() + 15) / 16);
-  if (big >= 192) return launch_tile<256, 256, 2, 4, 2, false>(s, prepared, codes, xscale, M, 1, kb, out, nullptr, st);
-  const Fp8Slices p = fp8_slices(s, M);
-  if (p.count == 1) return launch_tile<128, 128, 2, 4, 4, false>(s, prepared, codes, xscale, M, 1, kb, out, nullptr, st);
-  float* const part = (float*)(xscale + (kb + 3) / 4 * 4 * s.scale_rows(M));
-  e = launch_tile<128, 128, 2, 4, 4, true>(s, prepared, codes, xscale, M, p.count, p.blocks, out, part, st);
-  if (e != hipSuccess) return e;
-  const dim3 grid((unsigned)((s.N / 4 + 255) / 256), (unsigned)M);
-  if (s.gated)
-    hipLaunchKernelGGL(fp8_join_kernel<true>, grid, dim3(256), 0, st, s, part, p.count, M, out);
-  else
-    hipLaunchKernelGGL(fp8_join_kernel<false>, grid, dim3(256), 0, st, s, part, p.count, M, out);
-  return hipGetLastError();
+  if (big >= 192) return launch_tile<256, 256, 2, 4, 2>(s, prepared, codes, xscale, M, out, st);
+  return launch_tile<128, 128, 2, 4, 4>(s, prepared, codes, xscale, M, out, st);
 }
 
 }  // namespace moe

@@ -191,6 +191,7 @@ FP8 = [
     (17, 256, 128, "none"), (31, 392, 200, "silu"), (40, 2048, 96, "none"), (64, 128, 512, "relu2"),
     (65, 640, 264, "none"), (100, 1536, 328, "gelu_tanh"), (129, 264, 520, "swigluoai"), (256, 512, 512, "none"),
     (300, 1024, 776, "silu"), (520, 384, 256, "none"), (1030, 256, 1288, "none"), (700, 200, 648, "swigluoai"),
+    (1500, 264, 1544, "swigluoai"), (2050, 392, 1032, "none"), (1200, 1160, 2056, "silu"),  # for the small ones
     (3100, 136, 4120, "none"), (2900, 648, 2056, "silu"), (3000, 1160, 4096, "relu2"),  # enough for the large tiles
 ]
 
