@@ -21,7 +21,8 @@ MOE_HD constexpr int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 //         a wave holds expert 16 s + l % 16, K values 32 b + 8 (l / 16) .. + 7
 //         in bf16, the A operand of v_mfma_f32_16x16x32_bf16.  fp32 weights
 //         are three bf16 planes whose sum is the weight exactly
-//         (24 = 3 x 8 significant bits).
+//         (24 = 3 x 8 significant bits).  K blocks past H are zero, up to a
+//         multiple of kPadBlocks.
 //   norms f32[E]: the experts' 2-norms, rounded up.
 struct RouterShape {
   int E, H, k, groups, top_groups;
@@ -31,7 +32,9 @@ struct RouterShape {
   float scale;
 
   MOE_HD int subtiles() const { return (E + 15) / 16; }
-  MOE_HD int kblocks() const { return (H + 31) / 32; }
+  static constexpr int kPadBlocks = 8;
+  MOE_HD int blocks() const { return (H + 31) / 32; }
+  MOE_HD int kblocks() const { return (blocks() + kPadBlocks - 1) / kPadBlocks * kPadBlocks; }
   MOE_HD int64_t plane_bytes() const { return (int64_t)subtiles() * kblocks() * 1024; }
   MOE_HD int64_t norms_offset() const { return planes * plane_bytes(); }
   MOE_HD int64_t prepared_bytes() const { return align256(norms_offset() + 4ll * E); }

@@ -559,7 +559,7 @@ hipError_t launch_fp8_linear(const Fp8Shape& s, const uint8_t* prepared, const u
   if (e != hipSuccess) return e;
   if (M <= 16)
     return kb > 16 ? MOE_FEW(1, 1, 16, 2, false) : kb > 4 ? MOE_FEW(1, 1, 4, 4, false) : MOE_FEW(1, 1, 4, 1, false);
-  if (M <= 32) return MOE_FEW(2, 2, 8, 2, false);
+  if (M <= 32) return MOE_FEW(2, 2, 8, 1, false);
   // Up to two workgroups of 64 tokens x 64 rows per CU the tiles are no match:
   // K4096 N4096, M = 256: 14.5 against 20.9 us, M = 512: 23.1 against 25.5;
   // K1024 N1024, M = 512: 7.7 against 14.3.  Past it they are: K2048 N7168,

@@ -12,6 +12,8 @@
 // still fill the chip) and route_select (one wave per token).
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "block.h"
 #include "decode.h"
 #include "gemm_util.h"
@@ -103,11 +105,12 @@ struct LogitPlan {
 
 // K blocks (of 32) of a step of the tiled kernel
 constexpr int gemm_step(int planes) { return planes == 1 ? 2 : 1; }
+static_assert(RouterShape::kPadBlocks % kChain == 0, "the tiled kernel takes whole chains");
 
 LogitPlan logit_plan(const RouterShape& s, int64_t M) {
   LogitPlan p{};
-  const int kb = s.kblocks();
   p.gemm = M > 256;
+  const int kb = p.gemm ? s.kblocks() : s.blocks();
   int64_t splits;
   if (!p.gemm) {
     p.tt = M <= 16 ? 1 : M <= 32 ? 2 : 4;
@@ -119,7 +122,7 @@ LogitPlan logit_plan(const RouterShape& s, int64_t M) {
     splits = (p.be == 256 ? 256 : 512) / tiles;
     splits = splits < 1 ? 1 : splits > 8 ? 8 : splits;
   }
-  const int unit = p.gemm ? gemm_step(s.planes) : 4;
+  const int unit = p.gemm ? kChain / s.planes : 4;  // whole chains; a block for each wave
   const int64_t units = (kb + unit - 1) / unit;
   if (splits > units) splits = units;
   p.per = (int)((units + splits - 1) / splits) * unit;
@@ -134,15 +137,13 @@ int64_t partial_floats(const RouterShape& s, int64_t M) {
   return p.splits * M * (16 * (int64_t)s.subtiles() + 1);
 }
 
-// Squares of 2^32 x: those of |x| from 2^-95 to 2^31 neither vanish nor
-// overflow.
-__device__ __forceinline__ float add_squares(bf16x8_t v, float sq) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float f = (float)v[j] * 0x1p32f;
-    sq = fmaf(f, f, sq);
-  }
-  return sq;
+// x's squared norms come from the matrix cores too: a token tile times itself
+// has them on its diagonal, which lane l holds in accumulator l % 4 if l / 16
+// is l % 16 / 4.  (On the VALU a tile takes 48 instructions for one.)
+__device__ __forceinline__ bool on_diagonal(int lane) { return (lane >> 4) == ((lane & 15) >> 2); }
+__device__ __forceinline__ float diagonal(f32x4_t v, int lane) {
+  const float a = lane & 1 ? v[1] : v[0], b = lane & 1 ? v[3] : v[2];
+  return lane & 2 ? b : a;
 }
 
 // Few tokens: the weights are read once (per 64 tokens), straight into
@@ -152,23 +153,21 @@ __global__ void __launch_bounds__(256)
     route_few_kernel(RouterShape s, const uint8_t* __restrict__ prepared, const uint16_t* __restrict__ x, int M,
                      int per, float* __restrict__ part, float* __restrict__ xx) {
   __shared__ f32x4_t sums[4][TT][64];
-  __shared__ float squares[4][TT][16];
+  __shared__ f32x4_t squares[4][TT][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r = lane & 15, g = lane >> 4;
-  const int kb = s.kblocks(), Ep = 16 * s.subtiles();
+  const int kb = s.blocks(), Ep = 16 * s.subtiles();
   const int sub = blockIdx.x;
   const int64_t split = blockIdx.y, tok0 = (int64_t)blockIdx.z * (16 * TT);
   const int b0 = (int)split * per + wave, b1 = min(kb, (int)(split + 1) * per);
   const bool norms = sub == 0;
   const int64_t plane = s.plane_bytes();
-  const uint8_t* const w0 = prepared + (int64_t)sub * kb * 1024 + lane * 16;
-  f32x4_t acc[TT], chain[TT];
-  float sq[TT];
+  const uint8_t* const w0 = prepared + (int64_t)sub * s.kblocks() * 1024 + lane * 16;
+  f32x4_t acc[TT], chain[TT], sq[TT];
   const uint16_t* xr[TT];
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
-    acc[t] = chain[t] = f32x4_t{};
-    sq[t] = 0.0f;
+    acc[t] = chain[t] = sq[t] = f32x4_t{};
     xr[t] = x + min(tok0 + 16 * t + r, (int64_t)M - 1) * s.H + g * 8;
   }
   // the slice's blocks of this wave, kAhead at a time: all loads first
@@ -198,7 +197,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
         const bf16x8_t bop = __builtin_bit_cast(bf16x8_t, xv[i][t]);
-        if (norms) sq[t] = add_squares(bop, sq[t]);
+        if (norms) sq[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bop, bop, sq[t], 0, 0, 0);
 #pragma unroll
         for (int q = 0; q < NP; ++q)
           chain[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, wv[i][q]), bop, chain[t], 0,
@@ -217,12 +216,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
     sums[wave][t][lane] = acc[t] + chain[t];
-    if (norms) {
-      float v = sq[t];
-      v += __shfl_xor(v, 16);
-      v += __shfl_xor(v, 32);
-      if (g == 0) squares[wave][t][r] = v;
-    }
+    if (norms) squares[wave][t][lane] = sq[t];
   }
   __syncthreads();
   for (int t = wave; t < TT; t += 4) {
@@ -230,23 +224,25 @@ __global__ void __launch_bounds__(256)
     if (m < M) {
       const f32x4_t v = (sums[0][t][lane] + sums[1][t][lane]) + (sums[2][t][lane] + sums[3][t][lane]);
       *(f32x4_t*)(part + (split * M + m) * Ep + sub * 16 + 4 * g) = v;
-      if (norms && g == 0)
-        xx[split * M + m] = squares[0][t][r] + squares[1][t][r] + squares[2][t][r] + squares[3][t][r];
+      if (norms && on_diagonal(lane))
+        xx[split * M + m] = diagonal(
+            (squares[0][t][lane] + squares[1][t][lane]) + (squares[2][t][lane] + squares[3][t][lane]), lane);
     }
   }
 }
 
 // Many tokens: BM tokens x BE experts per workgroup, so that x is read once
 // for up to BE experts; x and the weights go to LDS by direct copies, two
-// steps ahead in a ring of three slots, one barrier per step.  WM x WE waves.
+// steps ahead in a ring of three slots, one barrier per step.  8 waves, each
+// 16 FE experts x 16 TT tokens.
 //
 // An x slot holds BM rows of 32 S values; the 16-byte chunk c of row r is at
 // position c ^ row_swz(r).
-template <int BM, int BE, int NP>
+template <int BM, int BE, int FE, int NP>
 struct RouteGemm {
   static constexpr int S = gemm_step(NP);           // K blocks of 32 per step
   static constexpr int kWaves = 8;
-  static constexpr int WE = BE / 64, WM = kWaves / WE;  // waves over experts and tokens: 64 experts each
+  static constexpr int WE = BE / 16 / FE, WM = kWaves / WE;  // waves over experts and tokens
   static constexpr int TT = BM / 16 / WM;           // token tiles of a wave
   static constexpr int kRow = 64 * S;               // bytes of an x row in a slot
   static constexpr int kX = BM * kRow, kW = NP * S * (BE / 16) * 1024;
@@ -255,100 +251,132 @@ struct RouteGemm {
   static constexpr int kCopies = kXCopies + kWCopies;
   static constexpr int kLds = 3 * kSlot;
   static_assert(kX % (1024 * kWaves) == 0 && kW % (1024 * kWaves) == 0 && TT >= 1, "whole copies per wave");
+  static_assert(WE * FE * 16 == BE && WM * TT * 16 == BM && TT <= WE, "whole tiles; a wave's norms are of one tile");
 };
 
-template <int BM, int BE, int NP>
+template <int BM, int BE, int FE, int NP>
 __global__ void __launch_bounds__(512)
     route_gemm_kernel(RouterShape s, const uint8_t* __restrict__ prepared, const uint16_t* __restrict__ x, int M,
                       int per, float* __restrict__ part, float* __restrict__ xx) {
-  using G = RouteGemm<BM, BE, NP>;
+  using G = RouteGemm<BM, BE, FE, NP>;
   constexpr int S = G::S, TT = G::TT, kChunks = G::kRow / 16;
   extern __shared__ __align__(16) uint8_t smem[];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int we = wave % G::WE, wm = wave / G::WE;
   const int kb = s.kblocks(), ns = s.subtiles(), Ep = 16 * ns;
   const int64_t split = blockIdx.z, tok0 = (int64_t)blockIdx.x * BM;
   const int b0 = (int)split * per, b1 = min(kb, b0 + per);
-  const int nsteps = (b1 - b0 + S - 1) / S;
+  const int nsteps = (b1 - b0) / S;  // whole chains
+  const int xlast = (s.H - 1) / (32 * S) * S;
   const int sub0 = blockIdx.y * (BE / 16);
-  const int64_t plane = s.plane_bytes();
 
-  // copy c of a step (the same number for every wave; past the last step and
-  // past the data they repeat what is there and are not used)
-  auto copy = [&](int step, int c) {
-    const int b = b0 + min(step, nsteps - 1) * S;
-    uint8_t* const slot = smem + (step % 3) * G::kSlot;
-    if (c < G::kXCopies) {
-      const int kib = c * G::kWaves + wave;  // 1 KiB: 64 / kChunks rows
-      const int row = kib * (64 / kChunks) + lane / kChunks;
-      const int chunk = (lane % kChunks) ^ row_swz<G::kRow>(row);
-      const int64_t m = min(tok0 + row, (int64_t)M - 1);
-      const int k = min(b * 32 + chunk * 8, s.H - 8);
-      dma16(x + m * s.H + k, lds_addr(slot + kib * 1024));
-    } else {
-      const int kib = (c - G::kXCopies) * G::kWaves + wave;  // [plane][subtile][block of the step]
-      const int j = kib % S, sub = kib / S % (BE / 16), q = kib / S / (BE / 16);
-      const int64_t at = ((int64_t)min(sub0 + sub, ns - 1) * kb + min(b + j, kb - 1)) * 1024;
-      dma16(prepared + q * plane + at + lane * 16, lds_addr(slot + G::kX + kib * 1024));
-    }
-  };
-  auto copies = [&](int step) {
+  // Copies of this wave, 1 KiB each: rows of x (past the last token it is
+  // repeated), then [plane][subtile][block of the step] of the weights.
+  const uint8_t* const xb = (const uint8_t*)(x + tok0 * s.H);
+  uint32_t xoff[G::kXCopies];
+  int xchunk[G::kXCopies];
 #pragma unroll
-    for (int c = 0; c < G::kCopies; ++c) copy(step, c);
-  };
-
-  f32x4_t acc[4][TT], chain[4][TT];
-  float sq[TT];
-#pragma unroll
-  for (int t = 0; t < TT; ++t) {
-    sq[t] = 0.0f;
-#pragma unroll
-    for (int f = 0; f < 4; ++f) acc[f][t] = chain[f][t] = f32x4_t{};
+  for (int c = 0; c < G::kXCopies; ++c) {
+    const int row = (c * G::kWaves + wave) * (64 / kChunks) + lane / kChunks;
+    xchunk[c] = ((lane % kChunks) ^ row_swz<G::kRow>(row)) * 16;
+    xoff[c] = (uint32_t)min((int64_t)row, M - 1 - tok0) * (uint32_t)(2 * s.H);
   }
-  const bool norms = blockIdx.y == 0;
-  copies(0);
-  copies(1);
-  constexpr int kFlush = kChain / (S * NP) > 0 ? kChain / (S * NP) : 1;  // steps of a chain
-#pragma unroll 1
-  for (int step = 0; step < nsteps; ++step) {
+  const uint8_t* wsrc[G::kWCopies];
+  int wblock[G::kWCopies];
+#pragma unroll
+  for (int c = 0; c < G::kWCopies; ++c) {
+    const int kib = c * G::kWaves + wave;
+    const int sub = kib / S % (BE / 16), q = kib / S / (BE / 16);
+    wblock[c] = kib % S;
+    wsrc[c] = prepared + q * s.plane_bytes() + (int64_t)min(sub0 + sub, ns - 1) * kb * 1024;
+  }
+  const uint32_t lds0 = lds_addr(smem) + wave * 1024;
+  // Copy c of a step (the same number for every wave).  Past the last step it
+  // repeats that and is not used; past the end of x's rows it repeats their
+  // last values, for which the weights are zero.  (They count in the norm,
+  // which then gives a bound on the high side.)
+  auto copy = [&](int step, int ring, int c) {
+    const int b = b0 + min(step, nsteps - 1) * S, bx = min(b, xlast);
+    const uint32_t to = lds0 + ring * G::kSlot + c * 8192;
+    if (c < G::kXCopies)
+      dma16_at(xb + (int64_t)bx * 64, xoff[c] + (uint32_t)min(xchunk[c], 2 * (s.H - 8) - bx * 64), to);
+    else
+      dma16_at(wsrc[c - G::kXCopies] + (int64_t)(b + wblock[c - G::kXCopies]) * 1024, lane * 16, to);
+  };
+
+  f32x4_t acc[FE][TT], chain[FE][TT];
+#pragma unroll
+  for (int f = 0; f < FE; ++f)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) acc[f][t] = chain[f][t] = f32x4_t{};
+  f32x4_t sq{};
+  // the waves of a row of tiles share its tokens' norms: this one's tile
+  const int tn = min(we, TT - 1);
+  const bool norms = blockIdx.y == 0 && we < TT;
+  int xat[S], nat[S];  // rows 16 apart have the same swizzle
+#pragma unroll
+  for (int j = 0; j < S; ++j) {
+    xat[j] = (wm * TT * 16 + r) * G::kRow + ((4 * j + g) ^ row_swz<G::kRow>(r)) * 16;
+    nat[j] = xat[j] + tn * 16 * G::kRow;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int c = 0; c < G::kCopies; ++c) copy(i, i, c);
+  constexpr int kFlush = kChain / (S * NP);  // steps of a chain
+  static_assert(kFlush >= 1, "chain length");
+  int ring = 0;
+  auto run = [&](int step, auto starts) {  // starts: the step that begins a chain
     vm_wait<G::kCopies>();  // this wave's copies of the step have landed, those of the next may not have
     __syncthreads();        // everyone's have, and everyone is done with the step before
-    copies(step + 2);
-    const uint8_t* const slot = smem + (step % 3) * G::kSlot;
-    const int b = b0 + step * S;
+    const uint8_t* const slot = smem + ring * G::kSlot;
+    const uint8_t* const wslot = slot + G::kX + we * FE * S * 1024 + lane * 16;
+    const int last = ring == 0 ? 2 : ring - 1;  // slot of the step before
+    ring = ring == 2 ? 0 : ring + 1;
+    // operands of an instruction group are read a group ahead
+    bf16x8_t xv[2][TT], nv[2], wv[2][FE];
+    auto read_x = [&](int j) {
 #pragma unroll
-    for (int j = 0; j < S; ++j) {
-      bf16x8_t bop[TT];
-      const bool in = b + j < b1 && (b + j) * 32 + g * 8 < s.H;
+      for (int t = 0; t < TT; ++t) xv[j & 1][t] = *(const bf16x8_t*)(slot + xat[j] + t * 16 * G::kRow);
+      nv[j & 1] = *(const bf16x8_t*)(slot + nat[j]);
+    };
+    auto read_w = [&](int i) {
+      const int j = i / NP, q = i % NP;
 #pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        const int row = (wm * TT + t) * 16 + r;
-        uint4 v = *(const uint4*)(slot + row * G::kRow + ((4 * j + g) ^ row_swz<G::kRow>(row)) * 16);
-        if (!in) v = make_uint4(0, 0, 0, 0);
-        bop[t] = __builtin_bit_cast(bf16x8_t, v);
-        if (norms && t % G::WE == we) sq[t] = add_squares(bop[t], sq[t]);
-      }
+      for (int f = 0; f < FE; ++f) wv[i & 1][f] = *(const bf16x8_t*)(wslot + ((q * (BE / 16) + f) * S + j) * 1024);
+    };
+    read_x(0);
+    read_w(0);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int q = 0; q < NP; ++q)
+    for (int c = 0; c < G::kCopies; ++c) copy(step + 2, last, c);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int f = 0; f < 4; ++f) {
-          const int kib = (q * (BE / 16) + we * 4 + f) * S + j;
-          const bf16x8_t a = __builtin_bit_cast(bf16x8_t, *(const uint4*)(slot + G::kX + kib * 1024 + lane * 16));
+    for (int i = 0; i < S * NP; ++i) {
+      const int j = i / NP;
+      if (i % NP == 0 && j + 1 < S) read_x(j + 1);
+      if (i + 1 < S * NP) read_w(i + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      if (i % NP == 0) sq = __builtin_amdgcn_mfma_f32_16x16x32_bf16(nv[j & 1], nv[j & 1], sq, 0, 0, 0);
 #pragma unroll
-          for (int t = 0; t < TT; ++t)
-            chain[f][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, bop[t], chain[f][t], 0, 0, 0);
-        }
-    }
-    if (step % kFlush == kFlush - 1) {
-#pragma unroll
-      for (int f = 0; f < 4; ++f)
+      for (int f = 0; f < FE; ++f)
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-          acc[f][t] += chain[f][t];
-          chain[f][t] = f32x4_t{};
+          if (decltype(starts)::value && i == 0) {
+            acc[f][t] += chain[f][t];
+            chain[f][t] = f32x4_t{};
+          }
+          chain[f][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[i & 1][f], xv[j & 1][t], chain[f][t], 0, 0, 0);
+          __builtin_amdgcn_sched_barrier(0);
         }
     }
+  };
+#pragma unroll 1
+  for (int step = 0; step < nsteps; step += kFlush) {
+    run(step, std::true_type{});
+#pragma unroll
+    for (int u = 1; u < kFlush; ++u) run(step + u, std::false_type{});
   }
   vm_wait<0>();  // no copy may land after the workgroup's LDS is released
 #pragma unroll
@@ -356,17 +384,13 @@ __global__ void __launch_bounds__(512)
     const int64_t m = tok0 + (wm * TT + t) * 16 + r;
     if (m < M)
 #pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        const int sub = sub0 + we * 4 + f;
+      for (int f = 0; f < FE; ++f) {
+        const int sub = sub0 + we * FE + f;
         if (sub < ns) *(f32x4_t*)(part + (split * M + m) * Ep + sub * 16 + 4 * g) = acc[f][t] + chain[f][t];
       }
-    if (norms && t % G::WE == we) {
-      float v = sq[t];
-      v += __shfl_xor(v, 16);
-      v += __shfl_xor(v, 32);
-      if (m < M && g == 0) xx[split * M + m] = v;
-    }
   }
+  const int64_t m = tok0 + (wm * TT + tn) * 16 + r;
+  if (norms && m < M && on_diagonal(lane)) xx[split * M + m] = diagonal(sq, lane);
 }
 
 // ---- selection: one wave per token, lane l holds experts NI l .. NI l + NI - 1
@@ -845,7 +869,7 @@ __global__ void __launch_bounds__(256)
   const float* p0 = part + m * Ep + lane * NI;  // a lane's experts are all below Ep (a multiple of 16) or none is
 #pragma unroll 8
   for (int q = 0; q < splits; ++q) {
-    x2 += xx[(int64_t)q * M + m];  // of 2^32 x
+    x2 += xx[(int64_t)q * M + m];
     if (lane * NI < Ep) zv += *(const vec_t*)(p0 + (int64_t)q * M * Ep);
   }
   float z[NI];
@@ -861,7 +885,18 @@ __global__ void __launch_bounds__(256)
   }
   wave_sync();
   // ||x|| ||w|| times the coefficient of the plan, which counts the roundings
-  const float bound = sqrtf(x2) * (1.001f * 0x1p-32f) * __uint_as_float(wave_max_u32(wn)) * coef;
+  float xnorm = sqrtf(x2);
+  if (x2 < 0x1p-60f) {  // squares may have vanished: sqrt(H) times the largest value instead, and 0 for a row of zeros
+    uint32_t most = 0;
+    for (int c = lane * 2; c < s.H; c += 128) {
+      const uint32_t v = *(const uint32_t*)(x + m * s.H + c);
+      most = max(most, max(v << 16 & 0x7FFFFFFFu, v & 0x7FFF0000u));
+    }
+    xnorm = __uint_as_float(wave_max_u32(most)) * sqrtf((float)s.H);
+  }
+  // at the end what products below the smallest normal number lose
+  float bound = xnorm * 1.001f * __uint_as_float(wave_max_u32(wn)) * coef;
+  if (xnorm != 0.0f) bound += (float)s.H * 0x1p-125f;
   const int kept = select_experts<NI, GROUPS>(s, L, prepared, x + m * s.H, z, bound, bias, lane);
   lane = renew(lane);
 
@@ -939,13 +974,13 @@ hipError_t launch_route(const RouterShape& s, const uint8_t* prepared, const uin
   if (p.gemm) {
     const dim3 grid((unsigned)((M + p.bm - 1) / p.bm), (unsigned)((s.E + p.be - 1) / p.be), (unsigned)p.splits);
     if (s.planes == 3)
-      hipLaunchKernelGGL((route_gemm_kernel<128, 128, 3>), grid, dim3(512), (RouteGemm<128, 128, 3>::kLds), st, s,
+      hipLaunchKernelGGL((route_gemm_kernel<128, 128, 4, 3>), grid, dim3(512), (RouteGemm<128, 128, 4, 3>::kLds), st, s,
                          prepared, x, M, p.per, part, xx);
     else if (p.be == 256)
-      hipLaunchKernelGGL((route_gemm_kernel<128, 256, 1>), grid, dim3(512), (RouteGemm<128, 256, 1>::kLds), st, s,
+      hipLaunchKernelGGL((route_gemm_kernel<128, 256, 4, 1>), grid, dim3(512), (RouteGemm<128, 256, 4, 1>::kLds), st, s,
                          prepared, x, M, p.per, part, xx);
     else
-      hipLaunchKernelGGL((route_gemm_kernel<64, 128, 1>), grid, dim3(512), (RouteGemm<64, 128, 1>::kLds), st, s,
+      hipLaunchKernelGGL((route_gemm_kernel<64, 128, 2, 1>), grid, dim3(512), (RouteGemm<64, 128, 2, 1>::kLds), st, s,
                          prepared, x, M, p.per, part, xx);
   } else {
     const dim3 grid((unsigned)s.subtiles(), (unsigned)p.splits, (unsigned)((M + 16 * p.tt - 1) / (16 * p.tt)));
