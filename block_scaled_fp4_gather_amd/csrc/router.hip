@@ -395,10 +395,33 @@ __global__ void __launch_bounds__(512)
 
 // ---- selection: one wave per token, lane l holds experts NI l .. NI l + NI - 1
 
+// What every lane has alike, told to the compiler: branches on it need no
+// masks.
+__device__ __forceinline__ float uniform(float v) {
+  return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v)));
+}
+
+// v of the lane that CTRL's move names, 0 bits where there is none
+template <int CTRL>
+__device__ __forceinline__ double moved(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xF, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xF, 0xF, false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// Sum over the wave, in lane order moves as below.
 __device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
-  return v;
+  v += moved<0x111>(v);
+  v += moved<0x112>(v);
+  v += moved<0x114>(v);
+  v += moved<0x118>(v);
+  v += moved<0x142>(v);
+  v += moved<0x143>(v);
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, 63);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
 __device__ __forceinline__ double wave_max(double v) {
@@ -470,41 +493,56 @@ __device__ __forceinline__ int renew(int v) {
   return v;
 }
 
-// Logit of expert e in 64 bits: products of bf16 values are exact.  Four
-// chunks of 8 values per lane are loaded before they are used.
-__device__ __forceinline__ double exact_logit(const RouterShape& s, const uint8_t* __restrict__ prepared,
-                                              const uint16_t* __restrict__ xr, int e, int lane) {
+// Logits of experts e[0] and e[1] in 64 bits: products of bf16 values are
+// exact.  A lane takes every 64th chunk of 8 values, plane by plane; the
+// operands of kAhead of them are loaded before they are used.
+__device__ __forceinline__ void exact_logits(const RouterShape& s, const uint8_t* __restrict__ prepared,
+                                             const uint16_t* __restrict__ xr, const int (&e)[2], int lane,
+                                             double (&sum)[2]) {
   constexpr int kAhead = 4;
-  const int chunks = s.H / 8;
-  const uint8_t* const row = prepared + (int64_t)(e >> 4) * s.kblocks() * 1024 + (e & 15) * 16;
-  double sum = 0.0;
-#pragma unroll 1
-  for (int q = 0; q < s.planes; ++q) {
-#pragma unroll 1
-    for (int c0 = lane; c0 < chunks; c0 += 64 * kAhead) {
-      uint4 xv[kAhead], wv[kAhead];
+  const int chunks = s.H / 8, per = (chunks + 63) / 64;
+  const uint8_t* row[2];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int c = c0 + 64 * i;
-        xv[i] = wv[i] = make_uint4(0, 0, 0, 0);
-        if (c < chunks) {
-          xv[i] = *(const uint4*)(xr + c * 8);
-          wv[i] = *(const uint4*)(row + q * s.plane_bytes() + c * 256);  // 16 rows of 16 bytes per chunk
-        }
+  for (int p = 0; p < 2; ++p) {
+    row[p] = prepared + (int64_t)(e[p] >> 4) * s.kblocks() * 1024 + (e[p] & 15) * 16;
+    sum[p] = 0.0;
+  }
+  int q = 0, at = 0;
+#pragma unroll 1
+  for (int left = per * s.planes; left > 0; left -= kAhead) {
+    uint4 xv[kAhead], wv[kAhead][2];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int c = at * 64 + lane;
+      xv[i] = wv[i][0] = wv[i][1] = make_uint4(0, 0, 0, 0);
+      if (i < left && c < chunks) {
+        xv[i] = *(const uint4*)(xr + c * 8);
+#pragma unroll
+        for (int p = 0; p < 2; ++p)  // 16 rows of 16 bytes per chunk
+          wv[i][p] = *(const uint4*)(row[p] + q * s.plane_bytes() + c * 256);
       }
+      if (++at == per) {
+        at = 0;
+        ++q;
+      }
+    }
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const uint32_t xw[4] = {xv[i].x, xv[i].y, xv[i].z, xv[i].w};
-        const uint32_t ww[4] = {wv[i].x, wv[i].y, wv[i].z, wv[i].w};
+    for (int i = 0; i < kAhead; ++i) {
+      const uint32_t xw[4] = {xv[i].x, xv[i].y, xv[i].z, xv[i].w};
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const uint32_t ww[4] = {wv[i][p].x, wv[i][p].y, wv[i][p].z, wv[i][p].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          sum = fma((double)__uint_as_float(xw[j] << 16), (double)__uint_as_float(ww[j] << 16), sum);
-          sum = fma((double)__uint_as_float(xw[j] & 0xFFFF0000u), (double)__uint_as_float(ww[j] & 0xFFFF0000u), sum);
+          sum[p] = fma((double)__uint_as_float(xw[j] << 16), (double)__uint_as_float(ww[j] << 16), sum[p]);
+          sum[p] = fma((double)__uint_as_float(xw[j] & 0xFFFF0000u), (double)__uint_as_float(ww[j] & 0xFFFF0000u),
+                       sum[p]);
         }
       }
     }
   }
-  return wave_sum(sum);
+  sum[0] = wave_sum(sum[0]);
+  sum[1] = wave_sum(sum[1]);
 }
 
 constexpr double kNone = -__builtin_inf();
@@ -518,25 +556,42 @@ struct SelectLds {
   uint16_t e[64 * NI];   // list: experts, best first
   uint16_t run[64 * NI]; // list: first place of the run of unsure neighbours a place belongs to
   int taken[64];
-  // where the results go: kept here while the experts are chosen, which needs
-  // all the scalar registers
+  // where the token's row and the results are: kept here while the experts are
+  // chosen, which needs all the scalar registers
+  const uint16_t* x;
+  const uint8_t* prepared;
+  int H, planes;
   int* ids;
   float *w, *logits;
 };
 
-// Recomputes the logits of the experts in `want` (bit i: this lane's i-th).
+// Recomputes the logits of the experts in `want` (bit i: this lane's i-th),
+// two at a time.
 template <int NI>
-__device__ __forceinline__ void refine(const RouterShape& s, SelectLds<NI>& L, const uint8_t* __restrict__ prepared,
-                                       const uint16_t* __restrict__ xr, uint32_t want, int lane) {
+__device__ __forceinline__ void refine(int E, SelectLds<NI>& L, uint32_t want, int lane) {
+  RouterShape shape{};
+  shape.E = E;
+  shape.H = __builtin_amdgcn_readfirstlane(L.H);
+  shape.planes = __builtin_amdgcn_readfirstlane(L.planes);
 #pragma unroll 1
-  for (int i = 0; i < NI; ++i) {
-    uint64_t todo = __ballot(want >> i & 1u);
-    while (todo) {
-      const int l = __ffsll((unsigned long long)todo) - 1;
-      todo &= todo - 1;
-      const double v = exact_logit(s, prepared, xr, l * NI + i, lane);
-      if (lane == l) L.z[l * NI + i] = v;
+  while (true) {
+    int e[2] = {-1, -1};
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const uint64_t any = __ballot(want != 0u);
+      if (any == 0) break;
+      const int l = __ffsll((unsigned long long)any) - 1;
+      const int i = __ffs(__builtin_amdgcn_readlane((int)want, l)) - 1;
+      e[p] = l * NI + i;
+      if (lane == l) want &= want - 1u;
     }
+    if (e[0] < 0) break;
+    const bool two = e[1] >= 0;
+    if (!two) e[1] = e[0];
+    double v[2];
+    exact_logits(shape, L.prepared, L.x, e, lane, v);
+    if (lane < 2) L.z[lane == 0 ? e[0] : e[1]] = lane == 0 ? v[0] : v[1];
+    if (!two) break;
   }
   wave_sync();
 }
@@ -566,12 +621,11 @@ __device__ __forceinline__ double group_top2(const SelectLds<NI>& L, int q, int 
 // that holds the k-th; the order of runs is certain, and within a run it is
 // that of the recomputed scores.
 template <int NI, bool GROUPS>
-__device__ __forceinline__ int select_experts(const RouterShape& s, SelectLds<NI>& L,
-                                              const uint8_t* __restrict__ prepared, const uint16_t* __restrict__ xr,
-                                              const float (&z)[NI], float bound, const float* __restrict__ bias,
-                                              int lane) {
+__device__ __forceinline__ int select_experts(const RouterShape& s, SelectLds<NI>& L, const float (&z)[NI], float bound, const float* __restrict__ bias,
+                                              int size, int per_group, int lane) {
   const int E = s.E;
   const bool scored = bias != nullptr || GROUPS;
+  bound = uniform(bound);
   float t[NI];
   float err = bound, zmax = 0.0f;
   if (scored) {
@@ -592,7 +646,7 @@ __device__ __forceinline__ int select_experts(const RouterShape& s, SelectLds<NI
       }
 #pragma unroll
       for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
-      const float top = 1.0f / sum;  // the largest score
+      const float top = uniform(1.0f / sum);  // the largest score
 #pragma unroll
       for (int i = 0; i < NI; ++i) t[i] *= top;
       err = (2.0f * bound + 0x1p-20f) * top;  // exp(z - zmax) / sum, each part within `bound` of itself
@@ -629,11 +683,10 @@ __device__ __forceinline__ int select_experts(const RouterShape& s, SelectLds<NI
   // the groups' largest; the unsure runs') and decides anew.
   uint32_t want = all ? open : 0u;
   bool have_groups = all, have_runs = all;
-  const int size = GROUPS ? E / s.groups : E;
   const int lanes_per_group = GROUPS && size % NI == 0 && ((size / NI) & (size / NI - 1)) == 0 ? size / NI : 0;
-  int group[NI];
+  int group[NI];  // n / size = n * (2^20 / size, rounded up) / 2^20 for n < 512: n (size - 1) < 2^20
 #pragma unroll
-  for (int i = 0; i < NI; ++i) group[i] = GROUPS ? renew((lane * NI + i) / size & 63) : 0;
+  for (int i = 0; i < NI; ++i) group[i] = GROUPS ? renew(__umul24(lane * NI + i, per_group) >> 20 & 63) : 0;
   int n = 0;
 
 #pragma unroll 1
@@ -645,7 +698,7 @@ __device__ __forceinline__ int select_experts(const RouterShape& s, SelectLds<NI
       group[i] = renew(group[i]);
       zk[i] = (uint32_t)renew((int)zk[i]);
     }
-    if (bound != 0.0f) refine<NI>(s, L, prepared, xr, want, lane);  // logits of a zero row are exact
+    if (bound != 0.0f) refine<NI>(E, L, want, lane);  // logits of a zero row are exact
     want = 0u;
     double total = 1.0;
     if (all) {
@@ -848,14 +901,15 @@ __device__ __forceinline__ int select_experts(const RouterShape& s, SelectLds<NI
 template <int NI, bool GROUPS>
 __global__ void __launch_bounds__(256)
     route_select_kernel(RouterShape s, const uint8_t* __restrict__ prepared, const uint16_t* __restrict__ x, int M,
-                        int splits, float coef, const float* __restrict__ part, const float* __restrict__ xx,
+                        int splits, float coef, int size, int per_group, const float* __restrict__ part, const float* __restrict__ xx,
                         const float* __restrict__ bias, int* __restrict__ ids, float* __restrict__ wout,
                         float* __restrict__ logits) {
   __shared__ SelectLds<NI> lds[4];
   int lane = threadIdx.x & 63;
-  const int64_t m = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t m = (int64_t)blockIdx.x * 4 + wave;
   if (m >= M) return;  // waves do not wait for each other
-  SelectLds<NI>& L = lds[threadIdx.x >> 6];
+  SelectLds<NI>& L = lds[wave];
   const int E = s.E, Ep = 16 * s.subtiles(), k = s.k;
   const float* const norms = (const float*)(prepared + s.norms_offset());
 
@@ -879,6 +933,10 @@ __global__ void __launch_bounds__(256)
     L.z[lane * NI + i] = (double)z[i];
   }
   if (lane == 0) {
+    L.x = x + m * s.H;
+    L.prepared = prepared;
+    L.H = s.H;
+    L.planes = s.planes;
     L.ids = ids + m * k;
     L.w = wout + m * k;
     L.logits = logits ? logits + m * E : nullptr;
@@ -897,7 +955,7 @@ __global__ void __launch_bounds__(256)
   // at the end what products below the smallest normal number lose
   float bound = xnorm * 1.001f * __uint_as_float(wave_max_u32(wn)) * coef;
   if (xnorm != 0.0f) bound += (float)s.H * 0x1p-125f;
-  const int kept = select_experts<NI, GROUPS>(s, L, prepared, x + m * s.H, z, bound, bias, lane);
+  const int kept = select_experts<NI, GROUPS>(s, L, z, bound, bias, size, per_group, lane);
   lane = renew(lane);
 
   // weights: the taken experts' probabilities, from their logits
@@ -1008,9 +1066,10 @@ hipError_t launch_route(const RouterShape& s, const uint8_t* prepared, const uin
   // the magnitudes of its chain of kChain instructions, with one rounding.
   // The chains, the waves' sums and the slices are added in fp32.
   const float coef = (float)((4.0 * kChain + 8.0 + (p.per * s.planes / (kChain / 2) + 4.0) + p.splits) * 0x1p-24);
+  const int size = s.E / s.groups, per_group = ((1 << 20) + size - 1) / size;
 #define MOE_SELECT_G(NI, G)                                                                                         \
-  hipLaunchKernelGGL((route_select_kernel<NI, G>), sgrid, dim3(256), 0, st, s, prepared, x, M, p.splits, coef, part, \
-                     xx, bias, ids, w, logits)
+  hipLaunchKernelGGL((route_select_kernel<NI, G>), sgrid, dim3(256), 0, st, s, prepared, x, M, p.splits, coef, size, \
+                     per_group, part, xx, bias, ids, w, logits)
 #define MOE_SELECT(NI)      \
   if (s.groups > 1)         \
     MOE_SELECT_G(NI, true); \
