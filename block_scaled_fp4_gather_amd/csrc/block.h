@@ -24,6 +24,7 @@ MOE_HD constexpr int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 //         (24 = 3 x 8 significant bits).  K blocks past H are zero, up to a
 //         multiple of kPadBlocks.
 //   norms f32[E]: the experts' 2-norms, rounded up.
+//   rows  [E][H]: the weights as they came.
 struct RouterShape {
   int E, H, k, groups, top_groups;
   int planes;    // 1 (bf16 weights) or 3 (fp32)
@@ -37,7 +38,8 @@ struct RouterShape {
   MOE_HD int kblocks() const { return (blocks() + kPadBlocks - 1) / kPadBlocks * kPadBlocks; }
   MOE_HD int64_t plane_bytes() const { return (int64_t)subtiles() * kblocks() * 1024; }
   MOE_HD int64_t norms_offset() const { return planes * plane_bytes(); }
-  MOE_HD int64_t prepared_bytes() const { return align256(norms_offset() + 4ll * E); }
+  MOE_HD int64_t rows_offset() const { return align256(norms_offset() + 4ll * E); }
+  MOE_HD int64_t prepared_bytes() const { return align256(rows_offset() + (planes == 1 ? 2ll : 4ll) * E * H); }
 };
 
 constexpr int kRouterMaxExperts = 512;

@@ -67,13 +67,18 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// Norms, rounded up: the fp32 sum is off by less than 2^-13 of itself for
-// H <= 65536 (256 lanes, trees).
+// Rows as they are, and norms, rounded up: the fp32 sum is off by less than
+// 2^-13 of itself for H <= 65536 (256 lanes, trees).
 template <bool F32>
 __global__ void __launch_bounds__(256)
-    router_norms_kernel(RouterShape s, const void* __restrict__ weight, float* __restrict__ norms) {
+    router_rows_kernel(RouterShape s, const void* __restrict__ weight, uint8_t* __restrict__ prepared) {
   __shared__ float sums[4];
   const int e = blockIdx.x;
+  float* const norms = (float*)(prepared + s.norms_offset());
+  constexpr int kSize = F32 ? 4 : 2;
+  const uint4* const from = (const uint4*)((const uint8_t*)weight + (int64_t)e * s.H * kSize);  // H % 8 == 0
+  uint4* const to = (uint4*)(prepared + s.rows_offset() + (int64_t)e * s.H * kSize);
+  for (int i = threadIdx.x; i < s.H * kSize / 16; i += 256) to[i] = from[i];
   float ss = 0.0f;
   for (int h = threadIdx.x; h < s.H; h += 256) {
     const float v = F32 ? ((const float*)weight)[(int64_t)e * s.H + h]
@@ -493,52 +498,55 @@ __device__ __forceinline__ int renew(int v) {
   return v;
 }
 
-// Logits of experts e[0] and e[1] in 64 bits: products of bf16 values are
-// exact.  A lane takes every 64th chunk of 8 values, plane by plane; the
-// operands of kAhead of them are loaded before they are used.
-__device__ __forceinline__ void exact_logits(const RouterShape& s, const uint8_t* __restrict__ prepared,
-                                             const uint16_t* __restrict__ xr, const int (&e)[2], int lane,
-                                             double (&sum)[2]) {
-  constexpr int kAhead = 4;
-  const int chunks = s.H / 8, per = (chunks + 63) / 64;
-  const uint8_t* row[2];
+// Logits of experts e[0] and e[1] in 64 bits, in which products of a bf16 and
+// an fp32 value are exact, from the weights' rows.  A lane takes every 64th
+// chunk of 8 values; the operands of kAhead of them are loaded before they are
+// used.  (From the operand layout, where 16 bytes of an expert are followed by
+// 240 of others', M = 37 with fp32 weights
+// took 21 us for 18.)
+template <bool F32>
+__device__ __forceinline__ void exact_logits(int H, const uint8_t* __restrict__ rows, const uint16_t* __restrict__ xr,
+                                             const int (&e)[2], int lane, double (&sum)[2]) {
+  constexpr int kAhead = F32 ? 2 : 3, kW = F32 ? 2 : 1;  // kW: 16-byte pieces of a chunk of weights
+  const int chunks = H / 8;
+  const uint4* row[2];
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
-    row[p] = prepared + (int64_t)(e[p] >> 4) * s.kblocks() * 1024 + (e[p] & 15) * 16;
+    row[p] = (const uint4*)rows + (int64_t)e[p] * (chunks * kW);
     sum[p] = 0.0;
   }
-  int q = 0, at = 0;
 #pragma unroll 1
-  for (int left = per * s.planes; left > 0; left -= kAhead) {
-    uint4 xv[kAhead], wv[kAhead][2];
+  for (int c0 = lane; c0 < chunks; c0 += 64 * kAhead) {
+    uint4 xv[kAhead], wv[kAhead][2][kW];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int c = at * 64 + lane;
-      xv[i] = wv[i][0] = wv[i][1] = make_uint4(0, 0, 0, 0);
-      if (i < left && c < chunks) {
+      const int c = c0 + 64 * i;
+      xv[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int h = 0; h < kW; ++h) wv[i][p][h] = make_uint4(0, 0, 0, 0);
+      if (c < chunks) {
         xv[i] = *(const uint4*)(xr + c * 8);
 #pragma unroll
-        for (int p = 0; p < 2; ++p)  // 16 rows of 16 bytes per chunk
-          wv[i][p] = *(const uint4*)(row[p] + q * s.plane_bytes() + c * 256);
-      }
-      if (++at == per) {
-        at = 0;
-        ++q;
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int h = 0; h < kW; ++h) wv[i][p][h] = row[p][c * kW + h];
       }
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const uint32_t xw[4] = {xv[i].x, xv[i].y, xv[i].z, xv[i].w};
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const uint32_t ww[4] = {wv[i][p].x, wv[i][p].y, wv[i][p].z, wv[i][p].w};
+      for (int p = 0; p < 2; ++p)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          sum[p] = fma((double)__uint_as_float(xw[j] << 16), (double)__uint_as_float(ww[j] << 16), sum[p]);
-          sum[p] = fma((double)__uint_as_float(xw[j] & 0xFFFF0000u), (double)__uint_as_float(ww[j] & 0xFFFF0000u),
-                       sum[p]);
+        for (int j = 0; j < 8; ++j) {
+          const uint4 v = wv[i][p][F32 ? j / 4 : 0];
+          const uint32_t ww[4] = {v.x, v.y, v.z, v.w};
+          const uint32_t w = F32 ? ww[j % 4] : j % 2 ? ww[j / 2] & 0xFFFF0000u : ww[j / 2] << 16;
+          const uint32_t xb = j % 2 ? xw[j / 2] & 0xFFFF0000u : xw[j / 2] << 16;
+          sum[p] = fma((double)__uint_as_float(xb), (double)__uint_as_float(w), sum[p]);
         }
-      }
     }
   }
   sum[0] = wave_sum(sum[0]);
@@ -559,39 +567,48 @@ struct SelectLds {
   // where the token's row and the results are: kept here while the experts are
   // chosen, which needs all the scalar registers
   const uint16_t* x;
-  const uint8_t* prepared;
-  int H, planes;
+  const uint8_t* rows;  // of the weights
+  int H;
   int* ids;
   float *w, *logits;
 };
 
-// Recomputes the logits of the experts in `want` (bit i: this lane's i-th),
-// two at a time.
-template <int NI>
-__device__ __forceinline__ void refine(int E, SelectLds<NI>& L, uint32_t want, int lane) {
-  RouterShape shape{};
-  shape.E = E;
-  shape.H = __builtin_amdgcn_readfirstlane(L.H);
-  shape.planes = __builtin_amdgcn_readfirstlane(L.planes);
+// Recomputes logits, two at a time: those of the first n places of the list
+// that are in runs of more than one, or with n = 0 those of the experts in
+// `want` (bit i: this lane's i-th).
+template <int NI, bool F32>
+__device__ __forceinline__ void refine(SelectLds<NI>& L, uint32_t want, int n, int lane) {
+  const int H = __builtin_amdgcn_readfirstlane(L.H);
 #pragma unroll 1
-  while (true) {
-    int e[2] = {-1, -1};
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const uint64_t any = __ballot(want != 0u);
-      if (any == 0) break;
-      const int l = __ffsll((unsigned long long)any) - 1;
-      const int i = __ffs(__builtin_amdgcn_readlane((int)want, l)) - 1;
-      e[p] = l * NI + i;
-      if (lane == l) want &= want - 1u;
+  for (int i = 0; i < (n != 0 ? (n + 63) / 64 : NI); ++i) {
+    int expert = lane * NI + i;
+    bool in = want >> (i & 31) & 1u;
+    if (n != 0) {
+      const int j = i * 64 + lane;
+      in = false;
+      if (j < n) {
+        const int r = L.run[j];
+        expert = L.e[j];
+        in = r != j || (j + 1 < n && L.run[j + 1] == r);
+      }
     }
-    if (e[0] < 0) break;
-    const bool two = e[1] >= 0;
-    if (!two) e[1] = e[0];
-    double v[2];
-    exact_logits(shape, L.prepared, L.x, e, lane, v);
-    if (lane < 2) L.z[lane == 0 ? e[0] : e[1]] = lane == 0 ? v[0] : v[1];
-    if (!two) break;
+    uint64_t todo = __ballot(in);
+#pragma unroll 1
+    while (todo) {
+      int e[2];
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        if (p == 1 && todo == 0) {
+          e[1] = e[0];
+        } else {
+          e[p] = __builtin_amdgcn_readlane(expert, __ffsll((unsigned long long)todo) - 1);
+          todo &= todo - 1;
+        }
+      }
+      double v[2];
+      exact_logits<F32>(H, L.rows, L.x, e, lane, v);
+      if (lane < 2) L.z[lane == 0 ? e[0] : e[1]] = lane == 0 ? v[0] : v[1];
+    }
   }
   wave_sync();
 }
@@ -620,7 +637,7 @@ __device__ __forceinline__ double group_top2(const SelectLds<NI>& L, int q, int 
 // cut into runs of neighbours nearer than twice the bound, as far as the run
 // that holds the k-th; the order of runs is certain, and within a run it is
 // that of the recomputed scores.
-template <int NI, bool GROUPS>
+template <int NI, bool GROUPS, bool F32>
 __device__ __forceinline__ int select_experts(const RouterShape& s, SelectLds<NI>& L, const float (&z)[NI], float bound, const float* __restrict__ bias,
                                               int size, int per_group, int lane) {
   const int E = s.E;
@@ -688,6 +705,7 @@ __device__ __forceinline__ int select_experts(const RouterShape& s, SelectLds<NI
 #pragma unroll
   for (int i = 0; i < NI; ++i) group[i] = GROUPS ? renew(__umul24(lane * NI + i, per_group) >> 20 & 63) : 0;
   int n = 0;
+  bool listed = false, runs = false;  // the list stands; it has unsure neighbours
 
 #pragma unroll 1
   while (true) {
@@ -698,7 +716,7 @@ __device__ __forceinline__ int select_experts(const RouterShape& s, SelectLds<NI
       group[i] = renew(group[i]);
       zk[i] = (uint32_t)renew((int)zk[i]);
     }
-    if (bound != 0.0f) refine<NI>(E, L, want, lane);  // logits of a zero row are exact
+    if (bound != 0.0f) refine<NI, F32>(L, want, listed ? n : 0, lane);  // logits of a zero row are exact
     want = 0u;
     double total = 1.0;
     if (all) {
@@ -724,7 +742,7 @@ __device__ __forceinline__ int select_experts(const RouterShape& s, SelectLds<NI
     };
 
     uint64_t in_groups = ~0ull;
-    if constexpr (GROUPS) {
+    if (GROUPS && !listed) {
       float score = -__builtin_inff();  // lane q: that of group q
       uint32_t near = 0;                // could be among the two largest of their groups
       if (lanes_per_group > 0) {        // groups of whole lanes, a power of two of them: all groups at once
@@ -815,66 +833,64 @@ __device__ __forceinline__ int select_experts(const RouterShape& s, SelectLds<NI
     // the list: key of expert e in the groups taken; within them, without a
     // bias, the order is that of the logits
     lane = renew(lane);
-    uint32_t left[NI], may = 0;
+    if (!listed) {
+      uint32_t left[NI], may = 0;
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      if (!GROUPS || (in_groups >> group[i] & 1ull)) may |= 1u << i;
-      left[i] = may >> i & 1u ? key[i] : 0u;
-      if (!bias && left[i] != 0u) left[i] = zk[i];
-    }
-    n = 0;
-    bool runs = all;
-    if (all) {  // one run of all that may be taken, in any order
-#pragma unroll 1
       for (int i = 0; i < NI; ++i) {
-        const int e = lane * NI + i;
-        const bool in = e < E && (may >> i & 1u) && exact_score(e, false) > kNone;
-        const uint64_t who = __ballot(in);
-        if (in) {
-          const int at = n + __popcll(who & ((1ull << lane) - 1ull));
-          L.e[at] = (uint16_t)e;
-          L.run[at] = 0;
-        }
-        n += __popcll(who);
+        if (!GROUPS || (in_groups >> group[i] & 1ull)) may |= 1u << i;
+        left[i] = may >> i & 1u ? key[i] : 0u;
+        if (!bias && left[i] != 0u) left[i] = zk[i];
       }
-    } else {
-      const float apart = 2.0f * (bias ? err : bound);
-      float prev = 0.0f;
-      int start = 0;
+      n = 0;
+      runs = all;
+      if (all) {  // one run of all that may be taken, in any order
 #pragma unroll 1
-      while (true) {
-        lane = renew(lane);
-        int e;
-        const uint32_t best = wave_best_key<NI>(left, e);
-        if (best == 0u) break;
-        const float v = key_value(best);
-        const bool unsure = n > 0 && apart > 0.0f && !(prev - v > apart);
-        if (n >= s.k && !unsure) break;
-        if (!unsure) start = n;
-        runs |= unsure;
-        if (lane == 0) {
-          L.e[n] = (uint16_t)e;
-          L.run[n] = (uint16_t)start;
+        for (int i = 0; i < NI; ++i) {
+          const int e = lane * NI + i;
+          const bool in = e < E && (may >> i & 1u) && exact_score(e, false) > kNone;
+          const uint64_t who = __ballot(in);
+          if (in) {
+            const int at = n + __popcll(who & ((1ull << lane) - 1ull));
+            L.e[at] = (uint16_t)e;
+            L.run[at] = 0;
+          }
+          n += __popcll(who);
         }
+      } else {
+        const float apart = 2.0f * (bias ? err : bound);
+        float prev = 0.0f;
+        int start = 0;
+#pragma unroll 1
+        while (true) {
+          lane = renew(lane);
+          int e;
+          const uint32_t best = wave_best_key<NI>(left, e);
+          if (best == 0u) break;
+          const float v = key_value(best);
+          const bool unsure = n > 0 && apart > 0.0f && !(prev - v > apart);
+          if (n >= s.k && !unsure) break;
+          if (!unsure) start = n;
+          runs |= unsure;
+          if (lane == 0) {
+            L.e[n] = (uint16_t)e;
+            L.run[n] = (uint16_t)start;
+          }
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
-          if (lane * NI + i == e) left[i] = 0u;
-        prev = v;
-        ++n;
+          for (int i = 0; i < NI; ++i)
+            if (lane * NI + i == e) left[i] = 0u;
+          prev = v;
+          ++n;
+        }
       }
+      wave_sync();
     }
-    wave_sync();
 
     if (!runs) {
       if (lane < n) L.taken[lane] = L.e[lane];
     } else {
       if (!have_runs) {
         have_runs = true;
-#pragma unroll 1
-        for (int j = 0; j < n; ++j) {
-          const int e = L.e[j], r = L.run[j];
-          if (e / NI == lane && (r != j || (j + 1 < n && L.run[j + 1] == r))) want |= 1u << (e % NI);
-        }
+        listed = !whole;
         if (whole) {
           all = true;
           want = open;
@@ -898,7 +914,7 @@ __device__ __forceinline__ int select_experts(const RouterShape& s, SelectLds<NI
   }
 }
 
-template <int NI, bool GROUPS>
+template <int NI, bool GROUPS, bool F32>
 __global__ void __launch_bounds__(256)
     route_select_kernel(RouterShape s, const uint8_t* __restrict__ prepared, const uint16_t* __restrict__ x, int M,
                         int splits, float coef, int size, int per_group, const float* __restrict__ part, const float* __restrict__ xx,
@@ -934,9 +950,8 @@ __global__ void __launch_bounds__(256)
   }
   if (lane == 0) {
     L.x = x + m * s.H;
-    L.prepared = prepared;
+    L.rows = prepared + s.rows_offset();
     L.H = s.H;
-    L.planes = s.planes;
     L.ids = ids + m * k;
     L.w = wout + m * k;
     L.logits = logits ? logits + m * E : nullptr;
@@ -955,7 +970,7 @@ __global__ void __launch_bounds__(256)
   // at the end what products below the smallest normal number lose
   float bound = xnorm * 1.001f * __uint_as_float(wave_max_u32(wn)) * coef;
   if (xnorm != 0.0f) bound += (float)s.H * 0x1p-125f;
-  const int kept = select_experts<NI, GROUPS>(s, L, z, bound, bias, size, per_group, lane);
+  const int kept = select_experts<NI, GROUPS, F32>(s, L, z, bound, bias, size, per_group, lane);
   lane = renew(lane);
 
   // weights: the taken experts' probabilities, from their logits
@@ -1013,13 +1028,12 @@ int64_t router_workspace(const RouterShape& s, int64_t max_tokens) {
 hipError_t launch_router_prepare(const RouterShape& s, const void* weight, uint8_t* prepared, hipStream_t st) {
   const int64_t blocks = ((int64_t)s.subtiles() * s.kblocks() * 64 + 255) / 256;
   const dim3 grid((unsigned)(blocks < 8192 ? blocks : 8192));
-  float* const norms = (float*)(prepared + s.norms_offset());
   if (s.planes == 3) {
     hipLaunchKernelGGL(router_prepare_kernel<true>, grid, dim3(256), 0, st, s, weight, prepared);
-    hipLaunchKernelGGL(router_norms_kernel<true>, dim3(s.E), dim3(256), 0, st, s, weight, norms);
+    hipLaunchKernelGGL(router_rows_kernel<true>, dim3(s.E), dim3(256), 0, st, s, weight, prepared);
   } else {
     hipLaunchKernelGGL(router_prepare_kernel<false>, grid, dim3(256), 0, st, s, weight, prepared);
-    hipLaunchKernelGGL(router_norms_kernel<false>, dim3(s.E), dim3(256), 0, st, s, weight, norms);
+    hipLaunchKernelGGL(router_rows_kernel<false>, dim3(s.E), dim3(256), 0, st, s, weight, prepared);
   }
   return hipGetLastError();
 }
@@ -1067,14 +1081,14 @@ hipError_t launch_route(const RouterShape& s, const uint8_t* prepared, const uin
   // The chains, the waves' sums and the slices are added in fp32.
   const float coef = (float)((4.0 * kChain + 8.0 + (p.per * s.planes / (kChain / 2) + 4.0) + p.splits) * 0x1p-24);
   const int size = s.E / s.groups, per_group = ((1 << 20) + size - 1) / size;
-#define MOE_SELECT_G(NI, G)                                                                                         \
-  hipLaunchKernelGGL((route_select_kernel<NI, G>), sgrid, dim3(256), 0, st, s, prepared, x, M, p.splits, coef, size, \
-                     per_group, part, xx, bias, ids, w, logits)
-#define MOE_SELECT(NI)      \
-  if (s.groups > 1)         \
-    MOE_SELECT_G(NI, true); \
-  else                      \
-    MOE_SELECT_G(NI, false)
+#define MOE_SELECT_G(NI, G, F32)                                                                                  \
+  hipLaunchKernelGGL((route_select_kernel<NI, G, F32>), sgrid, dim3(256), 0, st, s, prepared, x, M, p.splits, coef, \
+                     size, per_group, part, xx, bias, ids, w, logits)
+#define MOE_SELECT(NI)                                                 \
+  if (s.groups > 1 && s.planes == 3) MOE_SELECT_G(NI, true, true);     \
+  else if (s.groups > 1) MOE_SELECT_G(NI, true, false);                \
+  else if (s.planes == 3) MOE_SELECT_G(NI, false, true);               \
+  else MOE_SELECT_G(NI, false, false)
   if (s.E <= 64) {
     MOE_SELECT(1);
   } else if (s.E <= 128) {
