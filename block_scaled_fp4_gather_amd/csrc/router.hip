@@ -406,6 +406,13 @@ __device__ __forceinline__ float uniform(float v) {
   return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v)));
 }
 
+template <class T>
+__device__ __forceinline__ const T* uniform(const T* p) {
+  const uint64_t u = (uint64_t)p;
+  return (const T*)((uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(u >> 32)) << 32 |
+                    (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)u));
+}
+
 // v of the lane that CTRL's move names, 0 bits where there is none
 template <int CTRL>
 __device__ __forceinline__ double moved(double v) {
@@ -491,6 +498,10 @@ __device__ __forceinline__ void wave_best(double& v, int& e) {
   }
 }
 
+// exp(v) within (|v| + 2) 2^-23 of itself, 0 where that is below the normal
+// numbers: two instructions, where scores only need to be compared.
+__device__ __forceinline__ float fast_exp(float v) { return __builtin_amdgcn_exp2f(v * 1.44269504f); }
+
 // The same value, unknown to the compiler: what it derived from v before (a
 // mask register per comparison) is not kept for later uses.
 __device__ __forceinline__ int renew(int v) {
@@ -507,7 +518,7 @@ __device__ __forceinline__ int renew(int v) {
 template <bool F32>
 __device__ __forceinline__ void exact_logits(int H, const uint8_t* __restrict__ rows, const uint16_t* __restrict__ xr,
                                              const int (&e)[2], int lane, double (&sum)[2]) {
-  constexpr int kAhead = F32 ? 2 : 3, kW = F32 ? 2 : 1;  // kW: 16-byte pieces of a chunk of weights
+  constexpr int kAhead = F32 ? 1 : 2, kW = F32 ? 2 : 1;  // kW: 16-byte pieces of a chunk of weights
   const int chunks = H / 8;
   const uint4* row[2];
 #pragma unroll
@@ -538,15 +549,17 @@ __device__ __forceinline__ void exact_logits(int H, const uint8_t* __restrict__ 
     for (int i = 0; i < kAhead; ++i) {
       const uint32_t xw[4] = {xv[i].x, xv[i].y, xv[i].z, xv[i].w};
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
+      for (int j = 0; j < 8; ++j) {
+        const double xd = (double)__uint_as_float(j % 2 ? xw[j / 2] & 0xFFFF0000u : xw[j / 2] << 16);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int p = 0; p < 2; ++p) {
           const uint4 v = wv[i][p][F32 ? j / 4 : 0];
           const uint32_t ww[4] = {v.x, v.y, v.z, v.w};
           const uint32_t w = F32 ? ww[j % 4] : j % 2 ? ww[j / 2] & 0xFFFF0000u : ww[j / 2] << 16;
-          const uint32_t xb = j % 2 ? xw[j / 2] & 0xFFFF0000u : xw[j / 2] << 16;
-          sum[p] = fma((double)__uint_as_float(xb), (double)__uint_as_float(w), sum[p]);
+          sum[p] = fma(xd, (double)__uint_as_float(w), sum[p]);
         }
+        if (j % 2) __builtin_amdgcn_sched_barrier(0);  // few conversions at a time: registers
+      }
     }
   }
   sum[0] = wave_sum(sum[0]);
@@ -606,7 +619,7 @@ __device__ __forceinline__ void refine(SelectLds<NI>& L, uint32_t want, int n, i
         }
       }
       double v[2];
-      exact_logits<F32>(H, L.rows, L.x, e, lane, v);
+      exact_logits<F32>(H, uniform(L.rows), uniform(L.x), e, lane, v);
       if (lane < 2) L.z[lane == 0 ? e[0] : e[1]] = lane == 0 ? v[0] : v[1];
     }
   }
@@ -638,8 +651,9 @@ __device__ __forceinline__ double group_top2(const SelectLds<NI>& L, int q, int 
 // that holds the k-th; the order of runs is certain, and within a run it is
 // that of the recomputed scores.
 template <int NI, bool GROUPS, bool F32>
-__device__ __forceinline__ int select_experts(const RouterShape& s, SelectLds<NI>& L, const float (&z)[NI], float bound, const float* __restrict__ bias,
-                                              int size, int per_group, int lane) {
+__device__ __forceinline__ int select_experts(const RouterShape& s, SelectLds<NI>& L, const float (&z)[NI],
+                                              float bound, const float* __restrict__ bias,
+                                              const float (&biases)[NI], int size, int per_group, int lane) {
   const int E = s.E;
   const bool scored = bias != nullptr || GROUPS;
   bound = uniform(bound);
@@ -648,8 +662,9 @@ __device__ __forceinline__ int select_experts(const RouterShape& s, SelectLds<NI
   if (scored) {
     if (s.sigmoid) {
 #pragma unroll
-      for (int i = 0; i < NI; ++i) t[i] = 1.0f / (1.0f + expf(-z[i]));
-      err = 0.25f * bound + 0x1p-20f;  // scores are at most 1, with a few roundings of 2^-24 each
+      for (int i = 0; i < NI; ++i) t[i] = __builtin_amdgcn_rcpf(1.0f + fast_exp(-z[i]));
+      // a score p <= 1 is within |z| 2^-23 (1 - p) p, at most 2^-25, and a few roundings of 2^-24 of itself
+      err = 0.25f * bound + 0x1p-20f;
     } else {
       uint32_t key = 0;
 #pragma unroll
@@ -658,7 +673,7 @@ __device__ __forceinline__ int select_experts(const RouterShape& s, SelectLds<NI
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        t[i] = expf(z[i] - zmax);
+        t[i] = fast_exp(z[i] - zmax);
         sum += t[i];
       }
 #pragma unroll
@@ -666,13 +681,16 @@ __device__ __forceinline__ int select_experts(const RouterShape& s, SelectLds<NI
       const float top = uniform(1.0f / sum);  // the largest score
 #pragma unroll
       for (int i = 0; i < NI; ++i) t[i] *= top;
-      err = (2.0f * bound + 0x1p-20f) * top;  // exp(z - zmax) / sum, each part within `bound` of itself
+      // exp(z - zmax) / sum, each part within `bound` of itself.  The terms e of
+      // the sum are off by 3 |log e| 2^-24, by log E on the mean, and the sum by
+      // at most 14 roundings.
+      err = (2.0f * bound + 0x1p-18f) * top;
     }
     if (bias) {
       float most = 0.0f;
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const float b = lane * NI + i < E ? bias[lane * NI + i] : 0.0f;
+        const float b = biases[i];
         t[i] += b;
         if (fabsf(b) < __builtin_inff()) most = fmaxf(most, fabsf(b));
       }
@@ -915,11 +933,11 @@ __device__ __forceinline__ int select_experts(const RouterShape& s, SelectLds<NI
 }
 
 template <int NI, bool GROUPS, bool F32>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, NI <= 4 ? 5 : 4)
     route_select_kernel(RouterShape s, const uint8_t* __restrict__ prepared, const uint16_t* __restrict__ x, int M,
-                        int splits, float coef, int size, int per_group, const float* __restrict__ part, const float* __restrict__ xx,
-                        const float* __restrict__ bias, int* __restrict__ ids, float* __restrict__ wout,
-                        float* __restrict__ logits) {
+                        int splits, float coef, int size, int per_group, const float* __restrict__ part,
+                        const float* __restrict__ xx, const float* __restrict__ bias, int* __restrict__ ids,
+                        float* __restrict__ wout, float* __restrict__ logits) {
   __shared__ SelectLds<NI> lds[4];
   int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -929,19 +947,29 @@ __global__ void __launch_bounds__(256)
   const int E = s.E, Ep = 16 * s.subtiles(), k = s.k;
   const float* const norms = (const float*)(prepared + s.norms_offset());
 
+  // all that is needed from memory, in flight together
   typedef float vec_t __attribute__((ext_vector_type(NI)));
-  vec_t zv = {};
-  uint32_t wn = 0;
+  float wnorm[NI], biases[NI];
 #pragma unroll
-  for (int i = 0; i < NI; ++i)
-    if (lane * NI + i < E) wn = max(wn, __float_as_uint(norms[lane * NI + i]));  // norms are not negative
+  for (int i = 0; i < NI; ++i) {
+    wnorm[i] = norms[min(lane * NI + i, E - 1)];
+    biases[i] = 0.0f;
+  }
+  if (bias)
+#pragma unroll
+    for (int i = 0; i < NI; ++i) biases[i] = bias[min(lane * NI + i, E - 1)];
   float x2 = 0.0f;
-  const float* p0 = part + m * Ep + lane * NI;  // a lane's experts are all below Ep (a multiple of 16) or none is
+  vec_t zv = {};
+  // a lane's experts are all below Ep, a multiple of 16, or none is
+  const float* p0 = part + m * Ep + min(lane * NI, Ep - NI);
 #pragma unroll 8
   for (int q = 0; q < splits; ++q) {
     x2 += xx[(int64_t)q * M + m];
-    if (lane * NI < Ep) zv += *(const vec_t*)(p0 + (int64_t)q * M * Ep);
+    zv += *(const vec_t*)(p0 + (int64_t)q * M * Ep);
   }
+  uint32_t wn = 0;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) wn = max(wn, __float_as_uint(wnorm[i]));  // norms are not negative
   float z[NI];
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
@@ -970,7 +998,7 @@ __global__ void __launch_bounds__(256)
   // at the end what products below the smallest normal number lose
   float bound = xnorm * 1.001f * __uint_as_float(wave_max_u32(wn)) * coef;
   if (xnorm != 0.0f) bound += (float)s.H * 0x1p-125f;
-  const int kept = select_experts<NI, GROUPS, F32>(s, L, z, bound, bias, size, per_group, lane);
+  const int kept = select_experts<NI, GROUPS, F32>(s, L, z, bound, bias, biases, size, per_group, lane);
   lane = renew(lane);
 
   // weights: the taken experts' probabilities, from their logits
