@@ -398,7 +398,9 @@ __global__ void __launch_bounds__(512)
   if (norms && m < M && on_diagonal(lane)) xx[split * M + m] = diagonal(sq, lane);
 }
 
-// ---- selection: one wave per token, lane l holds experts NI l .. NI l + NI - 1
+// ---- selection: one wave per token, a workgroup of its own (in workgroups of
+// four, tokens with something to recompute keep the places of those without:
+// M = 16384, E = 256 in groups took 67 us for 59), lane l holds experts NI l .. NI l + NI - 1
 
 // What every lane has alike, told to the compiler: branches on it need no
 // masks.
@@ -933,17 +935,14 @@ __device__ __forceinline__ int select_experts(const RouterShape& s, SelectLds<NI
 }
 
 template <int NI, bool GROUPS, bool F32>
-__global__ void __launch_bounds__(256, NI <= 4 ? 5 : 4)
+__global__ void __launch_bounds__(64, NI <= 4 ? 5 : 4)
     route_select_kernel(RouterShape s, const uint8_t* __restrict__ prepared, const uint16_t* __restrict__ x, int M,
                         int splits, float coef, int size, int per_group, const float* __restrict__ part,
                         const float* __restrict__ xx, const float* __restrict__ bias, int* __restrict__ ids,
                         float* __restrict__ wout, float* __restrict__ logits) {
-  __shared__ SelectLds<NI> lds[4];
-  int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t m = (int64_t)blockIdx.x * 4 + wave;
-  if (m >= M) return;  // waves do not wait for each other
-  SelectLds<NI>& L = lds[wave];
+  __shared__ SelectLds<NI> L;
+  int lane = threadIdx.x;
+  const int64_t m = blockIdx.x;
   const int E = s.E, Ep = 16 * s.subtiles(), k = s.k;
   const float* const norms = (const float*)(prepared + s.norms_offset());
 
@@ -1099,7 +1098,7 @@ hipError_t launch_route(const RouterShape& s, const uint8_t* prepared, const uin
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const dim3 sgrid((unsigned)((M + 3) / 4));
+  const dim3 sgrid((unsigned)M);
   // Error bound of a logit, over ||x|| ||w||, which is at least the sum A of
   // the magnitudes |x w|.  v_mfma_f32_16x16x32_bf16 adds its 32 products in
   // four groups of 8 (measured): within a group they are cut to multiples of
@@ -1110,7 +1109,7 @@ hipError_t launch_route(const RouterShape& s, const uint8_t* prepared, const uin
   const float coef = (float)((4.0 * kChain + 8.0 + (p.per * s.planes / (kChain / 2) + 4.0) + p.splits) * 0x1p-24);
   const int size = s.E / s.groups, per_group = ((1 << 20) + size - 1) / size;
 #define MOE_SELECT_G(NI, G, F32)                                                                                  \
-  hipLaunchKernelGGL((route_select_kernel<NI, G, F32>), sgrid, dim3(256), 0, st, s, prepared, x, M, p.splits, coef, \
+  hipLaunchKernelGGL((route_select_kernel<NI, G, F32>), sgrid, dim3(64), 0, st, s, prepared, x, M, p.splits, coef, \
                      size, per_group, part, xx, bias, ids, w, logits)
 #define MOE_SELECT(NI)                                                 \
   if (s.groups > 1 && s.planes == 3) MOE_SELECT_G(NI, true, true);     \
