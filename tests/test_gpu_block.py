@@ -85,6 +85,8 @@ ROUTES = [
     (1000, 72, 300, 8, "fp32", "sigmoid", True, 1, 1, True, 1.0),
     (2000, 1096, 64, 2, "bf16", "softmax", True, 1, 1, True, 1.0),
     (1025, 40, 512, 5, "bf16", "sigmoid", False, 8, 2, True, 1.0),
+    (600, 416, 444, 6, "bf16", "softmax", True, 4, 4, True, 1.0),
+    (270, 648, 241, 10, "fp32", "softmax", True, 1, 1, True, 1.0),
 ]
 
 
@@ -149,12 +151,38 @@ def test_route_infinite_bias_and_large_values():
     E, H, M, k = 40, 256, 6, 5
     bias = 0.05 * rand(4, E)
     bias[7], bias[30] = math.inf, math.inf
-    router, w = make_router(E, H, k, M, "bf16", bias, scoring="sigmoid")
-    ids, _, _ = check_routes(router, w, hidden(2, M, H), bias)
-    assert bool((ids[:, 0] == 7).all()) and bool((ids[:, 1] == 30).all())
+    for scoring in ("sigmoid", "softmax"):
+        router, w = make_router(E, H, k, M, "bf16", bias, scoring=scoring)
+        ids, _, _ = check_routes(router, w, hidden(2, M, H), bias)
+        assert bool((ids[:, 0] == 7).all()) and bool((ids[:, 1] == 30).all())
     # logits of +-1e4: saturated scores, told apart by the logits
     router, w = make_router(E, H, k, M, "bf16", scoring="sigmoid", renorm=True)
     check_routes(router, w, (hidden(2, M, H).float() * 2.0 ** 14).bfloat16())
+
+
+@pytest.mark.parametrize("scoring,biased,groups,top_groups,weight", [
+    ("softmax", False, 1, 1, "bf16"), ("softmax", True, 1, 1, "fp32"), ("softmax", True, 8, 3, "bf16"),
+    ("sigmoid", True, 8, 3, "fp32"), ("sigmoid", False, 1, 1, "bf16")])
+def test_route_without_a_bound(scoring, biased, groups, top_groups, weight):
+    """Squares of x that overflow leave no bound on the logits' errors, and ones
+    that vanish a loose one: still the exact experts."""
+    E, H, M, k = 104, 520, 7, 6
+    bias = 0.05 * rand(4, E) if biased else None
+    g = torch.Generator().manual_seed(31)
+    x = hidden(30, M, H)
+    w = rand(29, E, H) / math.sqrt(2 * H)
+    x[1] = (x[1].float() * 2.0 ** 64).bfloat16()
+    x[4] = (x[4].float() * 2.0 ** -100).bfloat16()
+    x[5] = 0
+    x[5, 7] = 2.0 ** -130
+    x[6] = torch.where(torch.rand(H, generator=g) < 0.5, x[6].float() * 2.0 ** 62, x[6].float()).bfloat16()
+    # rows of +-2^64 saturate every score: only the logits' order is left, so no bias there
+    rows = list(range(M)) if not biased and groups == 1 else [0, 2, 3, 4, 5]
+    router, w = make_router(E, H, k, M, weight, bias, w=w, scoring=scoring, groups=groups, top_groups=top_groups)
+    ids, wt = router(x.cuda())
+    rid, rw, _ = ref.route(x, w, k, scoring, bias, groups, top_groups, True, 1.0)
+    assert torch.equal(ids.cpu()[rows], rid[rows])
+    assert bool(torch.isfinite(wt).all())
 
 
 def test_route_is_the_same_alone_and_in_a_batch():
