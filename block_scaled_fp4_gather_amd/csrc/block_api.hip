@@ -14,8 +14,7 @@ bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
 
 moe_fp4_status from_hip(hipError_t e) { return e == hipSuccess ? MOE_FP4_OK : MOE_FP4_EHIP; }
 
-// Largest max_tokens of the router and the FP8 map (token tiles go on a
-// grid's second dimension, which holds 65535).
+// Largest max_tokens of the router and the FP8 map.
 constexpr int kMaxTokens = 1 << 20;
 
 // Whether [p, p + n) and [q, q + m) share a byte.
@@ -59,7 +58,8 @@ moe_fp4_status fp8_shape(const moe_fp4_fp8_desc* d, moe::Fp8Shape* s) {
   if (d->act_fn == MOE_FP4_FN_SWIGLUOAI &&
       (!std::isfinite(d->act_alpha) || !std::isfinite(d->act_beta) || !(d->act_limit > 0.0f)))
     return MOE_FP4_EINVAL;
-  if (d->in_features > 1 << 20 || (int64_t)d->in_features * d->out_features > (int64_t)1 << 30 || d->max_tokens > kMaxTokens)
+  if (d->in_features > 1 << 20 || (int64_t)d->in_features * d->out_features > (int64_t)1 << 30 ||
+      d->max_tokens > kMaxTokens)
     return MOE_FP4_EUNSUPPORTED;
   const bool act = d->act_fn != MOE_FP4_FN_NONE;
   *s = moe::Fp8Shape{d->in_features, d->out_features, act && d->act_fn != MOE_FP4_FN_RELU2,
@@ -111,6 +111,19 @@ moe_fp4_status moe_fp4_route(const moe_fp4_router_desc* desc, const void* prepar
   if (!aligned(prepared, 256) || !aligned(x, 16) || !aligned(topk_ids, 4) || !aligned(topk_w, 4) ||
       !aligned(bias, 4) || !aligned(logits, 4) || !aligned(workspace, 256))
     return MOE_FP4_EINVAL;
+  const struct {
+    const void* p;
+    int64_t bytes;
+  } in[] = {{x, 2ll * M * s.H}, {bias, 4ll * s.E}, {prepared, s.prepared_bytes()},
+            {workspace, moe::router_workspace(s, desc->max_tokens)}},
+    out[] = {{topk_ids, 4ll * M * s.k}, {topk_w, 4ll * M * s.k}, {logits, 4ll * M * s.E}};
+  if (overlap(x, in[0].bytes, workspace, in[3].bytes)) return MOE_FP4_EINVAL;
+  for (int o = 0; o < 3; ++o) {
+    for (const auto& i : in)
+      if (overlap(out[o].p, out[o].bytes, i.p, i.bytes)) return MOE_FP4_EINVAL;
+    for (int q = 0; q < o; ++q)
+      if (overlap(out[o].p, out[o].bytes, out[q].p, out[q].bytes)) return MOE_FP4_EINVAL;
+  }
   if ((int64_t)workspace_bytes < moe::router_workspace(s, desc->max_tokens)) return MOE_FP4_EWORKSPACE;
   return from_hip(moe::launch_route(s, (const uint8_t*)prepared, x, M, bias, topk_ids, topk_w, logits,
                                     (uint8_t*)workspace, (hipStream_t)stream));
@@ -155,8 +168,11 @@ moe_fp4_status moe_fp4_fp8_linear(const moe_fp4_fp8_desc* desc, const void* prep
   if (!prepared || !x || !out || !workspace) return MOE_FP4_EINVAL;
   if (!aligned(prepared, 256) || !aligned(x, 16) || !aligned(out, 16) || !aligned(workspace, 256))
     return MOE_FP4_EINVAL;
-  if (overlap(x, 2ll * M * s.K, out, 2ll * M * s.N)) return MOE_FP4_EINVAL;
-  if ((int64_t)workspace_bytes < moe::fp8_workspace(s, desc->max_tokens)) return MOE_FP4_EWORKSPACE;
+  const int64_t need = moe::fp8_workspace(s, desc->max_tokens), out_bytes = 2ll * M * s.N;
+  if (overlap(out, out_bytes, x, 2ll * M * s.K) || overlap(out, out_bytes, prepared, s.prepared_bytes()) ||
+      overlap(out, out_bytes, workspace, need) || overlap(x, 2ll * M * s.K, workspace, need))
+    return MOE_FP4_EINVAL;
+  if ((int64_t)workspace_bytes < need) return MOE_FP4_EWORKSPACE;
   return from_hip(moe::launch_fp8_linear(s, (const uint8_t*)prepared, x, M, out, (uint8_t*)workspace,
                                          (hipStream_t)stream));
 }
@@ -178,7 +194,8 @@ moe_fp4_status moe_fp4_block_norm(const moe_fp4_norm_desc* desc, int32_t M, cons
   if (M == 0) return MOE_FP4_OK;
   // a branch writes a residual; a norm has its weight and its output; there
   // is something to do
-  if (!h || (y != nullptr) != (h_out != nullptr) || (pre_weight != nullptr) != (x_out != nullptr)) return MOE_FP4_EINVAL;
+  if (!h || (y != nullptr) != (h_out != nullptr) || (pre_weight != nullptr) != (x_out != nullptr))
+    return MOE_FP4_EINVAL;
   if (!y && (y2 || post_weight || d.gate != MOE_FP4_GATE_NONE)) return MOE_FP4_EINVAL;
   if (!y && !x_out) return MOE_FP4_EINVAL;
   if ((d.gate != MOE_FP4_GATE_NONE) != (gate != nullptr)) return MOE_FP4_EINVAL;

@@ -973,6 +973,7 @@ __device__ __forceinline__ int select_all(const RouterShape& shape, SelectLds<NI
 #pragma unroll 1
     for (int e = lane; e < E; e += 64) sum += exp(L.z[e] - zmax);
     total = wave_sum(sum);
+    if (total != total) return 0;  // a NaN or +infinity among the logits: no probabilities
   }
   auto scores = [&](bool logits) {  // -infinity for what may not be taken
 #pragma unroll 1

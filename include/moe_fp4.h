@@ -377,7 +377,9 @@ moe_fp4_status moe_fp4_router_workspace_bytes(const moe_fp4_router_desc* desc, i
 
 /* Routes M tokens.  x: bf16 [M][H], 16-byte aligned; bias: fp32 [E] or NULL;
  * topk_ids: int32 [M][k] and topk_w: fp32 [M][k], overwritten; logits: fp32
- * [M][E], overwritten, or NULL.  M may be 0 (nothing is launched). */
+ * [M][E], overwritten, or NULL.  No output may overlap another, the workspace
+ * or anything that is read, nor x the workspace.  M may be 0 (nothing is
+ * launched). */
 moe_fp4_status moe_fp4_route(const moe_fp4_router_desc* desc, const void* prepared, const uint16_t* x, int32_t M,
                              const float* bias, int32_t* topk_ids, float* topk_w, float* logits, void* workspace,
                              size_t workspace_bytes, void* stream);
@@ -417,7 +419,7 @@ moe_fp4_status moe_fp4_fp8_prepare(const moe_fp4_fp8_desc* desc, const uint8_t* 
 moe_fp4_status moe_fp4_fp8_workspace_bytes(const moe_fp4_fp8_desc* desc, int32_t M, size_t* bytes);
 
 /* The map on M tokens.  x: bf16 [M][K], out: bf16 [M][N], overwritten; both
- * 16-byte aligned, not overlapping.  M may be 0 (nothing is launched). */
+ * 16-byte aligned, not overlapping each other or the workspace.  M may be 0 (nothing is launched). */
 moe_fp4_status moe_fp4_fp8_linear(const moe_fp4_fp8_desc* desc, const void* prepared, const uint16_t* x, int32_t M,
                                   uint16_t* out, void* workspace, size_t workspace_bytes, void* stream);
 

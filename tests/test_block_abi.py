@@ -59,15 +59,22 @@ def test_route_rejects_before_launch(L):
     ref = ctypes.byref(d.c())
     need = block.router_workspace_bytes(d, 8)
 
-    def call(M=8, prepared=256, x=512, bias=None, ids=1024, w=2048, logits=None, ws=4096, n=need):
+    P, X, I, W, G, S = (1 << b for b in range(20, 26))  # far enough apart
+
+    def call(M=8, prepared=P, x=X, bias=None, ids=I, w=W, logits=None, ws=S, n=need):
         return L.moe_fp4_route(ref, prepared, x, M, bias, ids, w, logits, ws, n, None)
 
     assert call(M=0) == 0
     assert call(M=9) == EINVAL and call(M=-1) == EINVAL
     for name in ("prepared", "x", "ids", "w", "ws"):
         assert call(**{name: None}) == EINVAL
-    assert call(prepared=128) == EINVAL and call(x=520) == EINVAL and call(ids=1026) == EINVAL
-    assert call(w=2050) == EINVAL and call(bias=6) == EINVAL and call(logits=6) == EINVAL and call(ws=4224) == EINVAL
+    assert call(prepared=P + 128) == EINVAL and call(x=X + 8) == EINVAL and call(ids=I + 2) == EINVAL
+    assert call(w=W + 2) == EINVAL and call(bias=6) == EINVAL and call(logits=G + 2) == EINVAL
+    assert call(ws=S + 128) == EINVAL
+    # outputs on each other or on what is read, and x on the workspace
+    assert call(w=I + 124) == EINVAL and call(logits=W - 2044) == EINVAL and call(logits=I) == EINVAL
+    assert call(ids=X + 4092) == EINVAL and call(w=P) == EINVAL and call(logits=S + need - 4) == EINVAL
+    assert call(bias=I - 252) == EINVAL and call(x=S) == EINVAL
     assert call(n=need - 1) == EWORKSPACE
     assert L.moe_fp4_router_prepare(ref, None, 256, 1 << 30, None) == EINVAL
     assert L.moe_fp4_router_prepare(ref, 8, 256, 1 << 30, None) == EINVAL
@@ -101,6 +108,7 @@ def test_fp8_linear_rejects_before_launch(L):
     assert call(prepared=128) == EINVAL and call(x=(1 << 14) + 8) == EINVAL and call(out=(1 << 16) + 8) == EINVAL
     assert call(ws=(1 << 18) + 128) == EINVAL
     assert call(out=1 << 14) == EINVAL and call(out=(1 << 14) + 2 * 8 * 128 - 16) == EINVAL  # overlaps x
+    assert call(out=1 << 18) == EINVAL and call(x=(1 << 18) + 256) == EINVAL and call(out=512) == EINVAL
     assert call(n=need - 1) == EWORKSPACE
     assert L.moe_fp4_fp8_prepare(ref, 16, None, 256, 1 << 30, None) == EINVAL
     assert L.moe_fp4_fp8_prepare(ref, 16, 16, 256, 16, None) == EWORKSPACE

@@ -165,7 +165,8 @@ def test_route_infinite_bias_and_large_values():
     ("sigmoid", True, 8, 3, "fp32"), ("sigmoid", False, 1, 1, "bf16")])
 def test_route_without_a_bound(scoring, biased, groups, top_groups, weight):
     """Squares of x that overflow leave no bound on the logits' errors, and ones
-    that vanish a loose one: still the exact experts."""
+    that vanish a loose one: still the exact experts.  An infinity in x makes
+    logits infinite: a softmax over them takes nothing."""
     E, H, M, k = 104, 520, 7, 6
     bias = 0.05 * rand(4, E) if biased else None
     g = torch.Generator().manual_seed(31)
@@ -175,6 +176,7 @@ def test_route_without_a_bound(scoring, biased, groups, top_groups, weight):
     x[4] = (x[4].float() * 2.0 ** -100).bfloat16()
     x[5] = 0
     x[5, 7] = 2.0 ** -130
+    x[3, 9] = math.inf
     x[6] = torch.where(torch.rand(H, generator=g) < 0.5, x[6].float() * 2.0 ** 62, x[6].float()).bfloat16()
     # rows of +-2^64 saturate every score: only the logits' order is left, so no bias there
     rows = list(range(M)) if not biased and groups == 1 else [0, 2, 3, 4, 5]
@@ -182,6 +184,8 @@ def test_route_without_a_bound(scoring, biased, groups, top_groups, weight):
     ids, wt = router(x.cuda())
     rid, rw, _ = ref.route(x, w, k, scoring, bias, groups, top_groups, True, 1.0)
     assert torch.equal(ids.cpu()[rows], rid[rows])
+    if scoring == "softmax":
+        assert bool((ids[3] == -1).all())
     assert bool(torch.isfinite(wt).all())
 
 
