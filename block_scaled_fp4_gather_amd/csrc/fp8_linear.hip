@@ -582,10 +582,17 @@ hipError_t launch_fp8_linear(const Fp8Shape& s, const uint8_t* prepared, const u
   if (groups * ((s.subtiles() + 1) / 2) <= 256) return MOE_FEW(2, 4, 8, 1, false);
   if (groups * ((s.subtiles() + 3) / 4) <= 512) return MOE_FEW(4, 4, 8, 1, false);
 #undef MOE_FEW
-  const int64_t big = (int64_t)((M + 255) / 256) * ((s.subtiles() + 15) / 16);
-  // K2048 N7168, M = 1400 (168 large tiles): 34.8 us for 39.4 with small ones;
-  // K4096 N4096, M = 2000 (128): 56.7 for 52.5
-  if (big >= 160) return launch_tile<256, 256, 2, 4, 2>(s, prepared, codes, xscale, M, out, st);
+  // One workgroup fits a CU, so a launch takes as many rounds as it has 256s of
+  // tiles, and a round of 128 x 128, 256 x 128 or 256 x 256 about 10 : 14 : 20 by
+  // the operands that it reads from LDS.  K4096 N4096, by tile: M = 900 30.2,
+  // 38.9, 52.1 us; M = 1400 46.2, 40.4, 53.2; M = 2500 68.9, 73.2, 57.9; M = 4096
+  // 93.9, 82.6, 71.6.
+  auto rounds = [&](int bm, int bn) {
+    return ((M + bm - 1) / bm * (int64_t)((s.subtiles() * 16 + bn - 1) / bn) + 255) / 256;
+  };
+  const int64_t small = 10 * rounds(128, 128), wide = 14 * rounds(256, 128), large = 20 * rounds(256, 256);
+  if (large <= small && large <= wide) return launch_tile<256, 256, 2, 4, 2>(s, prepared, codes, xscale, M, out, st);
+  if (wide <= small) return launch_tile<256, 128, 4, 2, 3>(s, prepared, codes, xscale, M, out, st);
   return launch_tile<128, 128, 2, 4, 4>(s, prepared, codes, xscale, M, out, st);
 }
 
