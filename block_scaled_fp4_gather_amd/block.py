@@ -159,6 +159,14 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _empty_like(t, dtype, stream):
+    """The same of t's shape, in half the host's time where the type is t's too."""
+    if stream is None:
+        return torch.empty_like(t) if t.dtype is dtype else torch.empty_like(t, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t, dtype=dtype)
+
+
 def _launch(index: int, stream, fn, args, tensors) -> None:
     """fn(*args, stream address) with device `index` current, which launches go
     by.  `tensors` are kept until an explicitly given stream is past the call."""
@@ -281,9 +289,9 @@ def block_norm(h, y=None, y2=None, *, gate=None, post_weight=None, pre_weight=No
     new residual (None without y) and the normed hidden states (None without
     pre_weight).  h_out may be h."""
     M, H = h.shape
-    dev, at = h.device, h.get_device()
+    at = h.get_device()
     if stream is not None:
-        stream = _stream(stream, dev)
+        stream = _stream(stream, h.device)
     wt = next((t.dtype for t in (pre_weight, post_weight, gate) if t is not None), torch.bfloat16)
     if h.dtype not in _TORCH_TYPES or wt not in _TORCH_TYPES:
         raise ValueError(f"block_norm takes bf16 and fp32, got {h.dtype} and {wt}")
@@ -300,9 +308,9 @@ def block_norm(h, y=None, y2=None, *, gate=None, post_weight=None, pre_weight=No
             raise ValueError(f"gate {list(shape)}: want [{H}], [{M}, 1] or [{M}, {H}]")
     rows = (M, H)
     if y is not None and h_out is None:
-        h_out = _empty(rows, h.dtype, dev, stream)
+        h_out = _empty_like(h, h.dtype, stream)
     if pre_weight is not None and x_out is None:
-        x_out = _empty(rows, torch.bfloat16, dev, stream)
+        x_out = _empty_like(h, torch.bfloat16, stream)
     bf16 = torch.bfloat16
     _launch(at, stream, moe.lib().moe_fp4_block_norm, (
         _norm_desc(H, _TORCH_TYPES[h.dtype], _TORCH_TYPES[wt], kind, int(gate_sigmoid), eps, residual_scale,
