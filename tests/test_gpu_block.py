@@ -160,6 +160,21 @@ def test_route_infinite_bias_and_large_values():
     check_routes(router, w, (hidden(2, M, H).float() * 2.0 ** 14).bfloat16())
 
 
+@pytest.mark.parametrize("M,E,H,k,weight,groups,top_groups", [
+    (5, 48, 520, 6, "bf16", 1, 1), (40, 300, 1024, 8, "fp32", 1, 1), (400, 128, 264, 4, "bf16", 8, 4)])
+def test_route_bias_that_evens_a_softmax(M, E, H, k, weight, groups, top_groups):
+    """A bias that makes all scores of some tokens alike but for its rounding to
+    fp32, while their probabilities differ: the sum over all experts decides."""
+    x = hidden(91, M, H)
+    w = rand(92, E, H) / math.sqrt(2 * H)
+    w = w.bfloat16() if weight == "bf16" else w
+    p = torch.softmax(x[M // 2].double() @ w.double().t(), 0)
+    bias = (0.1 - p).float()
+    x[0] = x[M // 2]
+    router, w = make_router(E, H, k, M, weight, bias, w=w, groups=groups, top_groups=top_groups)
+    check_routes(router, w, x, bias)
+
+
 @pytest.mark.parametrize("scoring,biased,groups,top_groups,weight", [
     ("softmax", False, 1, 1, "bf16"), ("softmax", True, 1, 1, "fp32"), ("softmax", True, 8, 3, "bf16"),
     ("sigmoid", True, 8, 3, "fp32"), ("sigmoid", False, 1, 1, "bf16")])
