@@ -105,6 +105,7 @@ struct NormArgs {
   void* h_out;         // of the residual's type, or null
   uint16_t* x_out;     // bf16 or null
   int M, H;
+  int64_t row0;  // first row of a launch
   int64_t gate_row;
   bool gate_vector, gate_sigmoid, h_f32, w_f32;
   float eps, residual_scale, branch_scale, weight_offset;

@@ -78,7 +78,7 @@ template <int WPR, int NV, bool HF32, bool WF32, bool VGATE>
 __global__ void __launch_bounds__(WPR < 4 ? 256 : WPR * 64) block_norm_kernel(NormArgs a) {
   __shared__ float sums[2][WPR > 1 ? WPR : 1];
   constexpr int kRows = WPR < 4 ? 4 / WPR : 1;
-  const int64_t row = (int64_t)blockIdx.x * kRows + (kRows > 1 ? threadIdx.x / (64 * WPR) : 0);
+  const int64_t row = a.row0 + (int64_t)blockIdx.x * kRows + (kRows > 1 ? threadIdx.x / (64 * WPR) : 0);
   if (kRows > 1 && row >= a.M) return;  // one wave per row: no barrier follows
   const int t = kRows > 1 ? threadIdx.x % (64 * WPR) : threadIdx.x;
   const int H = a.H;
@@ -174,26 +174,35 @@ __global__ void __launch_bounds__(WPR < 4 ? 256 : WPR * 64) block_norm_kernel(No
 
 template <int WPR, int NV>
 hipError_t launch_nv(const NormArgs& a, hipStream_t st) {
-  constexpr int kRows = WPR < 4 ? 4 / WPR : 1;
-  const dim3 grid((unsigned)(((int64_t)a.M + kRows - 1) / kRows)), block(WPR < 4 ? 256 : WPR * 64);
-#define MOE_NORM(HF, WF, VG) hipLaunchKernelGGL((block_norm_kernel<WPR, NV, HF, WF, VG>), grid, block, 0, st, a)
+  constexpr int kRows = WPR < 4 ? 4 / WPR : 1, kThreads = WPR < 4 ? 256 : WPR * 64;
+  // A launch has fewer than 2^32 threads (one of more left rows undone, with no
+  // error): more rows take several.
+  constexpr int64_t kLaunchRows = (1ll << 31) / kThreads * kRows;
+  NormArgs part = a;
+  for (part.row0 = 0; part.row0 < a.M; part.row0 += kLaunchRows) {
+    const int64_t rows = a.M - part.row0 < kLaunchRows ? a.M - part.row0 : kLaunchRows;
+    const dim3 grid((unsigned)((rows + kRows - 1) / kRows)), block(kThreads);
+#define MOE_NORM(HF, WF, VG) hipLaunchKernelGGL((block_norm_kernel<WPR, NV, HF, WF, VG>), grid, block, 0, st, part)
 #define MOE_NORM_G(HF, WF)   \
   if (a.gate_vector)         \
     MOE_NORM(HF, WF, true);  \
   else                       \
     MOE_NORM(HF, WF, false)
-  if (a.h_f32 && a.w_f32) {
-    MOE_NORM_G(true, true);
-  } else if (a.h_f32) {
-    MOE_NORM_G(true, false);
-  } else if (a.w_f32) {
-    MOE_NORM_G(false, true);
-  } else {
-    MOE_NORM_G(false, false);
+    if (a.h_f32 && a.w_f32) {
+      MOE_NORM_G(true, true);
+    } else if (a.h_f32) {
+      MOE_NORM_G(true, false);
+    } else if (a.w_f32) {
+      MOE_NORM_G(false, true);
+    } else {
+      MOE_NORM_G(false, false);
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
 #undef MOE_NORM_G
 #undef MOE_NORM
-  return hipGetLastError();
+  return hipSuccess;
 }
 
 }  // namespace

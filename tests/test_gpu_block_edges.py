@@ -6,6 +6,7 @@ import torch
 
 from block_scaled_fp4_gather_amd import block
 from gpu_util import say
+from test_gpu_block import rand
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +41,19 @@ def test_fp8_products_are_cut_as_the_header_says(M):
         at = (rows + start) % (2 * len(t))
         y = lin(x[at].cuda()).cpu()
         assert torch.equal(y.double(), want[at])
+
+
+def test_block_norm_of_more_rows_than_a_launch_has_threads():
+    """2^26 rows of 8 values and a few more, 64 threads a row: past the 2^32
+    threads of one launch."""
+    M, H, n = (1 << 26) + 1031, 8, 1031
+    rows = rand(80, n, H).bfloat16().cuda()
+    h = torch.zeros(M, H, dtype=torch.bfloat16, device="cuda")
+    h[:n], h[-n:] = rows, rows
+    h[1 << 25:(1 << 25) + n] = rows
+    w = (1 + 0.1 * rand(81, H)).bfloat16().cuda()
+    want = block.block_norm(rows, pre_weight=w)[1]
+    x = block.block_norm(h, pre_weight=w)[1]
+    for at in (0, 1 << 25, M - n):
+        assert torch.equal(x[at:at + n], want)
+    assert bool((x[n:1 << 25] == 0).all()) and bool((x[(1 << 25) + n:M - n] == 0).all())
