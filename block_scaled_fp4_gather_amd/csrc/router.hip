@@ -68,28 +68,29 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// Rows as they are, and norms, rounded up: the fp32 sum is off by less than
-// 2^-13 of itself for H <= 65536 (256 lanes, trees).
+// Rows as they are, and norms, rounded up.  Squares are summed in 64 bits: in
+// 32 those of weights below 2^-63 vanish, and the bound that the norms stand
+// in would be too small to see that logits are near each other.
 template <bool F32>
 __global__ void __launch_bounds__(256)
     router_rows_kernel(RouterShape s, const void* __restrict__ weight, uint8_t* __restrict__ prepared) {
-  __shared__ float sums[4];
+  __shared__ double sums[4];
   const int e = blockIdx.x;
   float* const norms = (float*)(prepared + s.norms_offset());
   constexpr int kSize = F32 ? 4 : 2;
   const uint4* const from = (const uint4*)((const uint8_t*)weight + (int64_t)e * s.H * kSize);  // H % 8 == 0
   uint4* const to = (uint4*)(prepared + s.rows_offset() + (int64_t)e * s.H * kSize);
   for (int i = threadIdx.x; i < s.H * kSize / 16; i += 256) to[i] = from[i];
-  float ss = 0.0f;
+  double ss = 0.0;
   for (int h = threadIdx.x; h < s.H; h += 256) {
-    const float v = F32 ? ((const float*)weight)[(int64_t)e * s.H + h]
+    const double v = F32 ? ((const float*)weight)[(int64_t)e * s.H + h]
                         : __uint_as_float((uint32_t)((const uint16_t*)weight)[(int64_t)e * s.H + h] << 16);
     ss += v * v;
   }
   for (int d = 32; d >= 1; d >>= 1) ss += __shfl_xor(ss, d);
   if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = ss;
   __syncthreads();
-  if (threadIdx.x == 0) norms[e] = sqrtf(sums[0] + sums[1] + sums[2] + sums[3]) * 1.001f + 1e-30f;
+  if (threadIdx.x == 0) norms[e] = (float)sqrt(sums[0] + sums[1] + sums[2] + sums[3]) * 1.001f + 0x1p-148f;
 }
 
 // ---- logits
@@ -1075,7 +1076,7 @@ __device__ __forceinline__ void finish(const RouterShape& shape, SelectLds<NI>& 
 template <int NI, bool GROUPS, bool F32>
 __global__ void __launch_bounds__(64, NI <= 4 ? 5 : 4)
     route_select_kernel(RouterShape s, const uint8_t* __restrict__ prepared, const uint16_t* __restrict__ x, int M,
-                        int splits, float coef, int size, int per_group, const float* __restrict__ part,
+                        int splits, float coef, float root, int size, int per_group, const float* __restrict__ part,
                         const float* __restrict__ xx, const float* __restrict__ bias, int* __restrict__ ids,
                         float* __restrict__ wout, float* __restrict__ logits) {
   __shared__ SelectLds<NI> L;
@@ -1133,11 +1134,14 @@ __global__ void __launch_bounds__(64, NI <= 4 ? 5 : 4)
       const uint32_t v = *(const uint32_t*)(x + m * s.H + c);
       most = max(most, max(v << 16 & 0x7FFFFFFFu, v & 0x7FFF0000u));
     }
-    xnorm = __uint_as_float(wave_max_u32(most)) * sqrtf((float)s.H);
+    xnorm = __uint_as_float(wave_max_u32(most)) * root;
   }
-  // at the end what products below the smallest normal number lose
-  float bound = xnorm * 1.001f * __uint_as_float(wave_max_u32(wn)) * coef;
-  if (xnorm != 0.0f) bound += (float)s.H * 0x1p-125f;
+  const float most = __uint_as_float(wave_max_u32(wn));
+  float bound = xnorm * 1.001f * most * coef;
+  // What numbers below the normal ones lose, at most 2^-126 each: three
+  // products of a value of x and the terms of a weight, a value of x, the terms
+  // of a weight; root = sqrt(H), and a row's magnitudes add up to root ||.||.
+  if (xnorm != 0.0f) bound += 0x1p-124f * root * (root + xnorm + most);
   if (x2 != x2) bound = 0.0f;  // a NaN in x makes every logit NaN: nothing to recompute
   int kept = -1;
   if (bound < __builtin_inff()) {
@@ -1265,10 +1269,11 @@ hipError_t launch_route(const RouterShape& s, const uint8_t* prepared, const uin
   // the magnitudes of its chain of kChain instructions, with one rounding.
   // The chains, the waves' sums and the slices are added in fp32.
   const float coef = (float)((4.0 * kChain + 8.0 + (p.per * s.planes / (kChain / 2) + 4.0) + p.splits) * 0x1p-24);
+  const float root = sqrtf((float)s.H);
   const int size = s.E / s.groups, per_group = ((1 << 20) + size - 1) / size;
 #define MOE_SELECT_G(NI, G, F32)                                                                                  \
   hipLaunchKernelGGL((route_select_kernel<NI, G, F32>), sgrid, dim3(64), 0, st, s, prepared, x, M, p.splits, coef, \
-                     size, per_group, part, xx, bias, ids, w, logits)
+                     root, size, per_group, part, xx, bias, ids, w, logits)
 #define MOE_SELECT(NI)                                                 \
   if (s.groups > 1 && s.planes == 3) MOE_SELECT_G(NI, true, true);     \
   else if (s.groups > 1) MOE_SELECT_G(NI, true, false);                \

@@ -1,12 +1,15 @@
 """The operators around the layer at the ends of their documented ranges."""
 from __future__ import annotations
 
+import math
+
 import pytest
 import torch
 
+import block_ref as ref
 from block_scaled_fp4_gather_amd import block
 from gpu_util import say
-from test_gpu_block import rand
+from test_gpu_block import make_router, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +60,25 @@ def test_block_norm_of_more_rows_than_a_launch_has_threads():
     for at in (0, 1 << 25, M - n):
         assert torch.equal(x[at:at + n], want)
     assert bool((x[n:1 << 25] == 0).all()) and bool((x[(1 << 25) + n:M - n] == 0).all())
+
+
+@pytest.mark.parametrize("M", [40, 300])
+@pytest.mark.parametrize("xe,we", [(0, -83), (0, -100), (60, -120), (-110, 20)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_route_near_ties_of_tiny_values(scoring, xe, we, M):
+    """Weights whose squares vanish in 32 bits, or whose terms of bf16 fall
+    below its normal numbers, and hidden states of that kind: without a bias
+    the order is that of the logits, however small."""
+    E, H = 64, 1024
+    w = rand(11, E, H) / math.sqrt(2 * H)
+    for e in range(8, E):
+        w[e] = w[e % 8]
+        if e % 3:
+            c = (37 * e) % H
+            w[e, c] = w[e, c] * (1 + 2.0 ** -20)
+    w = w * 2.0 ** we
+    x = (rand(21, M, H) * 2.0 ** xe).bfloat16()
+    router, w = make_router(E, H, 12, M, "fp32", None, w=w, scoring=scoring)
+    ids, _ = router(x.cuda())
+    rid, _, _ = ref.route(x, w, 12, scoring)
+    assert torch.equal(ids.cpu(), rid)
