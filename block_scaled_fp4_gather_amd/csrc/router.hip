@@ -682,6 +682,11 @@ __device__ __forceinline__ double group_top2(const SelectLds<NI>& L, int q, int 
   return v2 > kNone ? v1 + v2 : kNone;
 }
 
+// Largest bound on the logits for which scores of a softmax are bounded by it
+// (as below); past it all logits of the token are recomputed.  Hidden states
+// and weights of ordinary size stay below 0.01.
+constexpr float kScoreBound = 0.25f;
+
 // Which experts a token takes, best first, into L.taken; returns how many, or
 // -1 where all logits have to be recomputed for a softmax with a bias.
 //
@@ -723,10 +728,11 @@ __device__ __forceinline__ int select_experts(const RouterShape& s, SelectLds<NI
       const float top = uniform(1.0f / sum);  // the largest score
 #pragma unroll
       for (int i = 0; i < NI; ++i) t[i] *= top;
-      // exp(z - zmax) / sum, each part within `bound` of itself.  The terms e of
-      // the sum are off by 3 |log e| 2^-24, by log E on the mean, and the sum by
-      // at most 14 roundings.
-      err = (2.0f * bound + 0x1p-18f) * top;
+      // exp(z - zmax) / sum, each part within a factor of e^bound: off by at most
+      // e^(2 bound) - 1 <= 2 bound (1 + 1.2 bound) of itself for bounds up to
+      // kScoreBound.  The terms e of the sum are off by 3 |log e| 2^-24, by
+      // log E on the mean, and the sum by at most 14 roundings.
+      err = (2.0f * bound * (1.0f + 1.2f * bound) + 0x1p-18f) * top;
     }
     if (bias) {
       float most = 0.0f;
@@ -935,6 +941,7 @@ __device__ __forceinline__ int select_experts(const RouterShape& s, SelectLds<NI
 #pragma unroll 1
       for (int j = lane; j < n; j += 64) L.t[j] = exact_score(L.e[j], false);
       wave_sync();
+      // e^bound - 1 at most, for bounds up to 0.01 and up to kScoreBound
       const double off = whole ? (bound < 0.01f ? 1.01 * bound : 1.0) : 0.0;
       bool unsure = false;
 #pragma unroll 1
@@ -1144,9 +1151,10 @@ __global__ void __launch_bounds__(64, NI <= 4 ? 5 : 4)
   if (xnorm != 0.0f) bound += 0x1p-124f * root * (root + xnorm + most);
   if (x2 != x2) bound = 0.0f;  // a NaN in x makes every logit NaN: nothing to recompute
   int kept = -1;
-  if (bound < __builtin_inff()) {
+  const bool shares = !s.sigmoid && (GROUPS || bias != nullptr);  // scores of a softmax are compared
+  if (bound < (shares ? kScoreBound : __builtin_inff())) {
     kept = select_experts<NI, GROUPS, F32>(s, L, z, bound, bias, biases, size, per_group, lane);
-  } else if (bias == nullptr || s.sigmoid) {  // no bound on the logits' errors: all of them
+  } else if (bias == nullptr || s.sigmoid) {  // no bound that serves: all logits
     all_logits<NI, F32>(L, E, 0, 2, renew(lane));
     wave_sync();
     kept = select_all<NI>(s, L, uniform(L.bias), __builtin_amdgcn_readfirstlane(L.size), renew(lane));

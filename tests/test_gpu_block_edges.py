@@ -82,3 +82,27 @@ def test_route_near_ties_of_tiny_values(scoring, xe, we, M):
     ids, _ = router(x.cuda())
     rid, _, _ = ref.route(x, w, 12, scoring)
     assert torch.equal(ids.cpu(), rid)
+
+
+@pytest.mark.parametrize("M", [5, 300])
+@pytest.mark.parametrize("biased,groups", [(False, 8), (True, 8), (True, 1)])
+def test_route_softmax_of_logits_off_by_more_than_an_exponent(M, biased, groups):
+    """Logits near 2^40, which fp32 holds to 2^16, while what decides is a
+    difference of 1 between the two largest: the later of two near copies, in
+    another group, is e times as probable."""
+    E, H = 64, 520
+    x = (rand(70, M, H) * 2.0 ** 36).bfloat16()
+    x[:, 17] = 128.0
+    w = (0.25 * rand(71, E, H)).bfloat16()
+    top = (x[:, :16].sign().float() * 8).bfloat16()  # expert 3 and its copy 61 stand out for the rows of x[0]'s signs
+    x[:, :16] = x[:, :16].abs() * top[0].sign()
+    w[3, :16] = top[0]
+    w[3, 17] = 1.0
+    w[61] = w[3]
+    w[61, 17] = 1.0 + 2.0 ** -7
+    bias = torch.full((E,), 0.125) if biased else None
+    router, w = make_router(E, H, 1, M, "bf16", bias, w=w, scoring="softmax", groups=groups, top_groups=1)
+    ids, _ = router(x.cuda())
+    rid, _, z = ref.route(x, w, 1, "softmax", bias, groups, 1)
+    assert bool((rid == 61).all()) and torch.equal(z[:, 61] - z[:, 3], torch.ones(M, dtype=torch.float64))
+    assert torch.equal(ids.cpu(), rid)
