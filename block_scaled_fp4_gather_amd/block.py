@@ -144,13 +144,6 @@ def _need(t: torch.Tensor, what: str, dtype, shape, index: int) -> int:
     return t.data_ptr()
 
 
-def _stream(stream, device):
-    """A torch stream for `stream` (None stays None: the device's current one)."""
-    if stream is None or isinstance(stream, torch.cuda.Stream):
-        return stream
-    return torch.cuda.ExternalStream(int(stream), device=device)
-
-
 def _empty(shape, dtype, device, stream):
     """Memory that belongs to the stream that writes it."""
     if stream is None:
@@ -190,28 +183,31 @@ def _device(device) -> torch.device:
 
 
 class Router:
-    """Prepared router weights plus a workspace on one device.  Calls share
-    the workspace: run them on one stream, or order them."""
+    """Prepared router weights plus a workspace on one device, made on `stream`
+    (in order with the current one).  Calls share the workspace: run them on
+    one stream, or order them."""
 
     def __init__(self, desc: RouterDesc, weight: torch.Tensor, bias: torch.Tensor | None = None, device="cuda",
                  stream=None):
         self.desc = desc
         dev = self.device = _device(device)
-        stream = _stream(stream, dev)
+        stream = moe.as_stream(stream, dev)
         self._c = desc.c()
         self._ref = ctypes.byref(self._c)
         dtype = {"bf16": torch.bfloat16, "fp32": torch.float32}[desc.weight]
         if weight.dtype is not dtype:
             raise ValueError(f"router weights are {weight.dtype}, the descriptor says {dtype}")
-        weight = weight.to(dev).contiguous()
-        at = _need(weight, "weight", dtype, (desc.E, desc.H), dev.index)
-        self.bias = None if bias is None else bias.to(device=dev, dtype=torch.float32).contiguous()
-        self._bias_at = None if bias is None else _need(self.bias, "bias", torch.float32, (desc.E,), dev.index)
-        self.prepared = torch.empty(router_prepared_bytes(desc), dtype=torch.uint8, device=dev)
-        self.workspace = torch.empty(router_workspace_bytes(desc, desc.max_tokens), dtype=torch.uint8, device=dev)
-        self._at = self.prepared.data_ptr(), self.workspace.data_ptr(), self.workspace.numel()
-        _launch(dev.index, stream, moe.lib().moe_fp4_router_prepare,
-                (self._ref, at, self._at[0], self.prepared.numel()), (weight, self.prepared))
+        with moe.preparing(stream, dev, weight, bias) as made:
+            weight = weight.to(dev).contiguous()
+            at = _need(weight, "weight", dtype, (desc.E, desc.H), dev.index)
+            self.bias = None if bias is None else bias.to(device=dev, dtype=torch.float32).contiguous()
+            self._bias_at = None if bias is None else _need(self.bias, "bias", torch.float32, (desc.E,), dev.index)
+            self.prepared = torch.empty(router_prepared_bytes(desc), dtype=torch.uint8, device=dev)
+            self.workspace = torch.empty(router_workspace_bytes(desc, desc.max_tokens), dtype=torch.uint8, device=dev)
+            self._at = self.prepared.data_ptr(), self.workspace.data_ptr(), self.workspace.numel()
+            _launch(dev.index, stream, moe.lib().moe_fp4_router_prepare,
+                    (self._ref, at, self._at[0], self.prepared.numel()), (weight, self.prepared))
+            made += self.bias, self.prepared, self.workspace
         self._route = moe.lib().moe_fp4_route
 
     def __call__(self, x, ids=None, w=None, logits=None, stream=None):
@@ -221,7 +217,7 @@ class Router:
         at = dev.index
         M = x.shape[0]
         if stream is not None:
-            stream = _stream(stream, dev)
+            stream = moe.as_stream(stream, dev)
         if ids is None:
             ids = _empty((M, d.k), torch.int32, dev, stream)
         if w is None:
@@ -236,26 +232,29 @@ class Router:
 
 
 class Fp8Linear:
-    """Prepared FP8 weights plus a workspace on one device.  Calls share the
-    workspace: run them on one stream, or order them."""
+    """Prepared FP8 weights plus a workspace on one device, made on `stream`
+    (in order with the current one).  Calls share the workspace: run them on
+    one stream, or order them."""
 
     def __init__(self, desc: Fp8Desc, codes: torch.Tensor, scales: torch.Tensor, device="cuda", stream=None):
         self.desc = desc
         dev = self.device = _device(device)
-        stream = _stream(stream, dev)
+        stream = moe.as_stream(stream, dev)
         self._c = desc.c()
         self._ref = ctypes.byref(self._c)
         halves = desc.rows // desc.N
         if codes.dtype is torch.float8_e4m3fn:
             codes = codes.view(torch.uint8)
-        codes, scales = codes.to(dev).contiguous(), scales.to(dev).contiguous()
-        ca = _need(codes, "codes", torch.uint8, (desc.rows, desc.K), dev.index)
-        sa = _need(scales, "scales", torch.float32, (halves * (-(-desc.N // 128)), -(-desc.K // 128)), dev.index)
-        self.prepared = torch.empty(fp8_prepared_bytes(desc), dtype=torch.uint8, device=dev)
-        self.workspace = torch.empty(fp8_workspace_bytes(desc, desc.max_tokens), dtype=torch.uint8, device=dev)
-        self._at = self.prepared.data_ptr(), self.workspace.data_ptr(), self.workspace.numel()
-        _launch(dev.index, stream, moe.lib().moe_fp4_fp8_prepare,
-                (self._ref, ca, sa, self._at[0], self.prepared.numel()), (codes, scales, self.prepared))
+        with moe.preparing(stream, dev, codes, scales) as made:
+            codes, scales = codes.to(dev).contiguous(), scales.to(dev).contiguous()
+            ca = _need(codes, "codes", torch.uint8, (desc.rows, desc.K), dev.index)
+            sa = _need(scales, "scales", torch.float32, (halves * (-(-desc.N // 128)), -(-desc.K // 128)), dev.index)
+            self.prepared = torch.empty(fp8_prepared_bytes(desc), dtype=torch.uint8, device=dev)
+            self.workspace = torch.empty(fp8_workspace_bytes(desc, desc.max_tokens), dtype=torch.uint8, device=dev)
+            self._at = self.prepared.data_ptr(), self.workspace.data_ptr(), self.workspace.numel()
+            _launch(dev.index, stream, moe.lib().moe_fp4_fp8_prepare,
+                    (self._ref, ca, sa, self._at[0], self.prepared.numel()), (codes, scales, self.prepared))
+            made += self.prepared, self.workspace
         self._linear = moe.lib().moe_fp4_fp8_linear
 
     def __call__(self, x, out=None, stream=None):
@@ -264,7 +263,7 @@ class Fp8Linear:
         at = dev.index
         M = x.shape[0]
         if stream is not None:
-            stream = _stream(stream, dev)
+            stream = moe.as_stream(stream, dev)
         if out is None:
             out = _empty((M, d.N), torch.bfloat16, dev, stream)
         pa, sa, sn = self._at
@@ -291,7 +290,7 @@ def block_norm(h, y=None, y2=None, *, gate=None, post_weight=None, pre_weight=No
     M, H = h.shape
     at = h.get_device()
     if stream is not None:
-        stream = _stream(stream, h.device)
+        stream = moe.as_stream(stream, h.device)
     wt = next((t.dtype for t in (pre_weight, post_weight, gate) if t is not None), torch.bfloat16)
     if h.dtype not in _TORCH_TYPES or wt not in _TORCH_TYPES:
         raise ValueError(f"block_norm takes bf16 and fp32, got {h.dtype} and {wt}")
@@ -355,7 +354,7 @@ class Fp4MoEBlock:
 
     def __call__(self, h, x=None, gate=None, gate_sigmoid=False, next_weight=None, h_out=None, stream=None):
         """h [M][H]; x: its normed form where the block before gave it."""
-        stream = _stream(stream, h.device)
+        stream = moe.as_stream(stream, h.device)
         if stream is not None:
             for t in (h, x, gate, next_weight, h_out):
                 if t is not None:

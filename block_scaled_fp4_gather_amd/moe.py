@@ -6,6 +6,7 @@ library has not been built; there is no fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import os
@@ -151,6 +152,37 @@ def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+
+
+def as_stream(stream, device):
+    """A torch stream for `stream` (None stays None: the device's current one)."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(stream), device=device)
+
+
+@contextlib.contextmanager
+def preparing(stream, device, *given):
+    """Runs what a constructor does on `stream`, if it is given one: the copies
+    it makes of the tensors `given` and the memory it takes, not the launch
+    alone.  In order with the device's current stream both ways: the tensors
+    may have been made there, and what is made (the tensors that the caller
+    puts into the list) may be used there."""
+    made = []
+    if stream is None:
+        yield made
+        return
+    current = torch.cuda.current_stream(device)
+    stream.wait_stream(current)
+    for t in given:
+        if isinstance(t, torch.Tensor) and t.device == device:
+            t.record_stream(stream)
+    with torch.cuda.stream(stream):
+        yield made
+    current.wait_stream(stream)
+    for t in made:
+        if t is not None:
+            t.record_stream(current)
 
 
 def status_string(s: int) -> str:

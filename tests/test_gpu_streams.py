@@ -1,0 +1,75 @@
+"""Objects of the framework made on a stream of the user's."""
+from __future__ import annotations
+
+import contextlib
+import math
+
+import pytest
+import torch
+
+from block_scaled_fp4_gather_amd import block
+from gpu_util import say
+from test_gpu_block import fp8_weights, hidden, rand
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _announce(request):
+    say(f"\n[gpu] {request.node.nodeid}")
+    yield
+
+
+def late(t):
+    """t on the GPU, as a tensor whose bytes come late on the current stream."""
+    src = t.cuda()
+    out = torch.zeros_like(src)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)
+    return out.copy_(src)
+
+
+class RouterBuild:
+    E, H, k, M = 40, 328, 4, 9
+
+    def weights(self, put):
+        w = rand(3, self.E, self.H).float() / math.sqrt(2 * self.H)
+        # a transposed weight and a bf16 bias: both are copied by the constructor
+        return put(w.t().contiguous()).t(), put((0.05 * rand(9, self.E)).bfloat16())
+
+    def __call__(self, tensors, stream=None):
+        desc = block.RouterDesc(self.E, self.H, self.k, self.M, weight="fp32", scoring="sigmoid")
+        router = block.Router(desc, *tensors, stream=stream)
+        ids, w = router(hidden(1, self.M, self.H).cuda())
+        return router.prepared, router.bias, ids, w
+
+
+class Fp8Build:
+    K, N, M = 392, 264, 9
+
+    def weights(self, put):
+        codes, scales = fp8_weights(5, self.N, self.K, self.N)
+        return put(codes.t().contiguous()).t(), put(scales.t().contiguous()).t()
+
+    def __call__(self, tensors, stream=None):
+        lin = block.Fp8Linear(block.Fp8Desc(self.K, self.N, self.M), *tensors, stream=stream)
+        # rows of padding in the scales are never written
+        return lin.prepared[:16 * -(-self.N // 16) * 128 * -(-self.K // 128)], lin(hidden(2, self.M, self.K).cuda())
+
+
+@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("weights_on_side", [False, True])
+@pytest.mark.parametrize("build", [RouterBuild(), Fp8Build()], ids=["router", "fp8"])
+def test_made_on_a_side_stream(build, weights_on_side, raw):
+    """Weights that are still being written when the constructor is called, on
+    the current stream or on the one it is given: the same prepared bytes and
+    outputs as without streams."""
+    want = build(build.weights(lambda t: t.cuda()))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side) if weights_on_side else contextlib.nullcontext():
+        tensors = build.weights(late)
+    got = build(tensors, side.cuda_stream if raw else side)
+    del tensors
+    torch.cuda.synchronize()
+    assert len(want) == len(got) and all(torch.equal(a, b) for a, b in zip(want, got))
