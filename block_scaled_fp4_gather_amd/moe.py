@@ -158,7 +158,7 @@ def as_stream(stream, device):
     """A torch stream for `stream` (None stays None: the device's current one)."""
     if stream is None or isinstance(stream, torch.cuda.Stream):
         return stream
-    return torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
 
 
 @contextlib.contextmanager
@@ -270,12 +270,16 @@ def mxfp8_quantize(x, codes=None, scales=None, stream=None):
 
 
 class Fp4MoE:
-    """Prepared weights plus a workspace on one device; call with x, ids, w."""
+    """Prepared weights plus a workspace on one device, made on `stream` (in
+    order with the current one); call with x, ids, w."""
 
     def __init__(self, desc: Desc, w13_codes, w13_scales, w2_codes, w2_scales, g13=None, g2=None,
                  device="cuda", stream=None):
         self.desc = desc
         dev = torch.device(device)
+        if stream is not None and dev.index is None:
+            dev = torch.device(dev.type, torch.cuda.current_device())
+        stream = as_stream(stream, dev)
 
         def dev_t(a, dtype):
             if a is None:
@@ -283,13 +287,15 @@ class Fp4MoE:
             t = a if isinstance(a, torch.Tensor) else torch.from_numpy(a)
             return t.to(device=dev, dtype=dtype).contiguous()
 
-        tensors = [dev_t(a, torch.uint8) for a in (w13_codes, w13_scales, w2_codes, w2_scales)]
-        g13 = dev_t(g13, torch.float32)
-        g2 = dev_t(g2, torch.float32)
-        self.prepared = torch.empty(prepared_bytes(desc), dtype=torch.uint8, device=dev)
-        prepare(desc, *tensors, g13, g2, self.prepared, stream)
-        del tensors
-        self.workspace = torch.empty(workspace_bytes(desc, desc.max_tokens), dtype=torch.uint8, device=dev)
+        with preparing(stream, dev, w13_codes, w13_scales, w2_codes, w2_scales, g13, g2) as made:
+            tensors = [dev_t(a, torch.uint8) for a in (w13_codes, w13_scales, w2_codes, w2_scales)]
+            g13 = dev_t(g13, torch.float32)
+            g2 = dev_t(g2, torch.float32)
+            self.prepared = torch.empty(prepared_bytes(desc), dtype=torch.uint8, device=dev)
+            prepare(desc, *tensors, g13, g2, self.prepared, stream)
+            del tensors
+            self.workspace = torch.empty(workspace_bytes(desc, desc.max_tokens), dtype=torch.uint8, device=dev)
+            made += self.prepared, self.workspace
 
     def __call__(self, x, ids, w, out=None, stream=None, tuning=None, phases=None):
         if out is None:

@@ -7,8 +7,8 @@ import math
 import pytest
 import torch
 
-from block_scaled_fp4_gather_amd import block
-from gpu_util import say
+from block_scaled_fp4_gather_amd import block, moe, synth
+from gpu_util import say, to_dev
 from test_gpu_block import fp8_weights, hidden, rand
 
 pytestmark = pytest.mark.gpu
@@ -57,9 +57,26 @@ class Fp8Build:
         return lin.prepared[:16 * -(-self.N // 16) * 128 * -(-self.K // 128)], lin(hidden(2, self.M, self.K).cuda())
 
 
+class LayerBuild:
+    def __init__(self):
+        self.wl = synth.WORKLOADS["tiny_mxfp4"].replace(M=3)
+        self.d = synth.generate(self.wl)
+
+    def weights(self, put):
+        # all four are strided: the constructor copies them
+        return [put(torch.from_numpy(self.d[n]).transpose(1, 2).contiguous()).transpose(1, 2)
+                for n in ("w13_codes", "w13_scales", "w2_codes", "w2_scales")]
+
+    def __call__(self, tensors, stream=None):
+        w = self.wl
+        layer = moe.Fp4MoE(moe.Desc(w.fmt, w.E, w.H, w.I, w.k, w.M), *tensors, stream=stream)
+        y = layer(to_dev(self.d["x"]).view(torch.bfloat16), to_dev(self.d["ids"]), to_dev(self.d["w"]))
+        return layer.prepared, y
+
+
 @pytest.mark.parametrize("raw", [False, True])
 @pytest.mark.parametrize("weights_on_side", [False, True])
-@pytest.mark.parametrize("build", [RouterBuild(), Fp8Build()], ids=["router", "fp8"])
+@pytest.mark.parametrize("build", [RouterBuild(), Fp8Build(), LayerBuild()], ids=["router", "fp8", "layer"])
 def test_made_on_a_side_stream(build, weights_on_side, raw):
     """Weights that are still being written when the constructor is called, on
     the current stream or on the one it is given: the same prepared bytes and
