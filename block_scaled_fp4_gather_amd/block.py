@@ -352,11 +352,18 @@ class Fp4MoEBlock:
         self.kw = dict(eps=eps, residual_scale=residual_scale, branch_scale=branch_scale,
                        weight_offset=weight_offset)
 
+    def _held(self):
+        """What the block's steps read and write of their own."""
+        yield from (self.pre_weight, self.post_weight, self.router.bias)
+        for part in (self.layer, self.router, self.shared_up, self.shared_down):
+            if part is not None:
+                yield from (part.prepared, part.workspace)
+
     def __call__(self, h, x=None, gate=None, gate_sigmoid=False, next_weight=None, h_out=None, stream=None):
         """h [M][H]; x: its normed form where the block before gave it."""
         stream = moe.as_stream(stream, h.device)
         if stream is not None:
-            for t in (h, x, gate, next_weight, h_out):
+            for t in (h, x, gate, next_weight, h_out, *self._held()):
                 if t is not None:
                     t.record_stream(stream)
             with torch.cuda.stream(stream):

@@ -1,4 +1,4 @@
-"""Objects of the framework made on a stream of the user's."""
+"""Objects of the framework made and called on a stream of the user's."""
 from __future__ import annotations
 
 import contextlib
@@ -9,7 +9,7 @@ import torch
 
 from block_scaled_fp4_gather_amd import block, moe, synth
 from gpu_util import say, to_dev
-from test_gpu_block import fp8_weights, hidden, rand
+from test_gpu_block import fp8_weights, hidden, make_block, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -90,3 +90,29 @@ def test_made_on_a_side_stream(build, weights_on_side, raw):
     del tensors
     torch.cuda.synchronize()
     assert len(want) == len(got) and all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("shared", [False, True])
+def test_a_block_dropped_behind_its_call_is_kept_for_the_stream(shared, monkeypatch):
+    """A call on a stream of the user's marks everything that its steps touch as
+    used there, so that none of it is reused before the stream is past it."""
+    M = 5
+    blk, *_ = make_block(M, shared=shared)
+    h = rand(50, M, blk.layer.desc.H).bfloat16().cuda()
+    want, _ = blk(h)
+    torch.cuda.synchronize()
+    side, used, record = torch.cuda.Stream(), set(), torch.Tensor.record_stream
+
+    def note(t, stream):
+        if stream.cuda_stream == side.cuda_stream:
+            used.add(t.data_ptr())
+        return record(t, stream)
+
+    monkeypatch.setattr(torch.Tensor, "record_stream", note)
+    side.wait_stream(torch.cuda.current_stream())
+    got, _ = blk(h, stream=side)
+    parts = [blk.layer, blk.router] + ([blk.shared_up, blk.shared_down] if shared else [])
+    held = [t for p in parts for t in (p.prepared, p.workspace)] + [blk.router.bias, blk.pre_weight, blk.post_weight, h]
+    assert all(t.data_ptr() in used for t in held)
+    side.synchronize()
+    assert torch.equal(got, want)
