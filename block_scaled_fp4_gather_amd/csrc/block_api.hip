@@ -111,11 +111,11 @@ moe_fp4_status moe_fp4_route(const moe_fp4_router_desc* desc, const void* prepar
   if (!aligned(prepared, 256) || !aligned(x, 16) || !aligned(topk_ids, 4) || !aligned(topk_w, 4) ||
       !aligned(bias, 4) || !aligned(logits, 4) || !aligned(workspace, 256))
     return MOE_FP4_EINVAL;
+  const int64_t need = moe::router_workspace(s, desc->max_tokens);
   const struct {
     const void* p;
     int64_t bytes;
-  } in[] = {{x, 2ll * M * s.H}, {bias, 4ll * s.E}, {prepared, s.prepared_bytes()},
-            {workspace, moe::router_workspace(s, desc->max_tokens)}},
+  } in[] = {{x, 2ll * M * s.H}, {bias, 4ll * s.E}, {prepared, s.prepared_bytes()}, {workspace, need}},
     out[] = {{topk_ids, 4ll * M * s.k}, {topk_w, 4ll * M * s.k}, {logits, 4ll * M * s.E}};
   if (overlap(x, in[0].bytes, workspace, in[3].bytes)) return MOE_FP4_EINVAL;
   for (int o = 0; o < 3; ++o) {
@@ -124,7 +124,7 @@ moe_fp4_status moe_fp4_route(const moe_fp4_router_desc* desc, const void* prepar
     for (int q = 0; q < o; ++q)
       if (overlap(out[o].p, out[o].bytes, out[q].p, out[q].bytes)) return MOE_FP4_EINVAL;
   }
-  if ((int64_t)workspace_bytes < moe::router_workspace(s, desc->max_tokens)) return MOE_FP4_EWORKSPACE;
+  if ((int64_t)workspace_bytes < need) return MOE_FP4_EWORKSPACE;
   return from_hip(moe::launch_route(s, (const uint8_t*)prepared, x, M, bias, topk_ids, topk_w, logits,
                                     (uint8_t*)workspace, (hipStream_t)stream));
 }

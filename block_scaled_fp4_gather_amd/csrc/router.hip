@@ -118,6 +118,13 @@ struct LogitPlan {
 constexpr int gemm_step(int planes) { return planes == 1 ? 2 : 1; }
 static_assert(RouterShape::kPadBlocks % kChain == 0, "the tiled kernel takes whole chains");
 
+// Workgroups that one slice of the tiled kernel may leave idle are used by
+// further ones, up to kMostSplits.
+constexpr int64_t kMostSplits = 8;
+int64_t gemm_workgroups(int be) { return be == 256 ? 256 : 512; }
+int gemm_experts(const RouterShape& s) { return s.E <= 128 || s.planes == 3 ? 128 : 256; }
+int gemm_tokens(const RouterShape& s) { return gemm_experts(s) == 256 || s.planes == 3 ? 128 : 64; }
+
 LogitPlan logit_plan(const RouterShape& s, int64_t M) {
   LogitPlan p{};
   p.gemm = M > 256;
@@ -127,11 +134,11 @@ LogitPlan logit_plan(const RouterShape& s, int64_t M) {
     p.tt = M <= 16 ? 1 : M <= 32 ? 2 : 4;
     splits = (kb + 31) / 32;
   } else {
-    p.be = s.E <= 128 || s.planes == 3 ? 128 : 256;
-    p.bm = p.be == 256 || s.planes == 3 ? 128 : 64;
+    p.be = gemm_experts(s);
+    p.bm = gemm_tokens(s);
     const int64_t tiles = ((M + p.bm - 1) / p.bm) * ((s.E + p.be - 1) / p.be);
-    splits = (p.be == 256 ? 256 : 512) / tiles;
-    splits = splits < 1 ? 1 : splits > 8 ? 8 : splits;
+    splits = gemm_workgroups(p.be) / tiles;
+    splits = splits < 1 ? 1 : splits > kMostSplits ? kMostSplits : splits;
   }
   const int unit = p.gemm ? kChain / s.planes : 4;  // whole chains; a block for each wave
   const int64_t units = (kb + unit - 1) / unit;
@@ -141,8 +148,8 @@ LogitPlan logit_plan(const RouterShape& s, int64_t M) {
   return p;
 }
 
-// Partial logits f32 [split][M][16 subtiles] and partial sums of (2^32 x)^2
-// f32 [split][M].
+// Partial logits f32 [split][M][16 subtiles] and partial sums of x^2 f32
+// [split][M].
 int64_t partial_floats(const RouterShape& s, int64_t M) {
   const LogitPlan p = logit_plan(s, M);
   return p.splits * M * (16 * (int64_t)s.subtiles() + 1);
@@ -1210,15 +1217,20 @@ __global__ void __launch_bounds__(512)
 }  // namespace
 
 int64_t router_workspace(const RouterShape& s, int64_t max_tokens) {
-  // The slices change only from one number of token tiles to the next, and
-  // partial_floats() grows with M in between: its largest value is at a full
-  // last tile (up to where one slice is left) or at the last M.
+  // partial_floats() grows with M while the slices stay as many, so its
+  // largest value is at the largest M of some number of slices: that of the
+  // few tokens' kernel, or of the token tiles that leave room for n slices, or
+  // the last M.  (Called for each call: not in a loop over M.)
   const int64_t last = max_tokens < 1 ? 1 : max_tokens;
   int64_t most = partial_floats(s, last);
-  for (int64_t M = 16; M < last && M <= 64 * 512; M = M < 64 ? 2 * M : M + 64) {
-    const int64_t n = partial_floats(s, M);
+  auto take = [&](int64_t M) {
+    const int64_t n = M < last ? partial_floats(s, M) : 0;
     if (n > most) most = n;
-  }
+  };
+  take(256);
+  const int be = gemm_experts(s);
+  const int64_t tiles = gemm_workgroups(be) / ((s.E + be - 1) / be);
+  for (int n = 1; n <= kMostSplits; ++n) take(tiles / n * gemm_tokens(s));
   return align256(4 * most);
 }
 

@@ -3,6 +3,7 @@ rejected before any HIP call (so these run without a GPU)."""
 from __future__ import annotations
 
 import ctypes
+import time
 
 import pytest
 import torch
@@ -149,3 +150,55 @@ def test_binding_refuses_what_does_not_fit():
         block.block_norm(h, pre_weight=torch.ones(64))  # not on a GPU
     with pytest.raises(ValueError):
         block.block_norm(h, h.bfloat16(), gate=torch.ones(3), pre_weight=torch.ones(64))
+
+
+def _route_floats(E, H, planes, M):
+    """What a call of M tokens keeps, by the plan of its slices: f32 logits per
+    slice, token and expert (to a multiple of 16), and a norm per slice and
+    token."""
+    blocks = (H + 31) // 32
+    if M <= 256:
+        kb, unit, splits = blocks, 4, (blocks + 31) // 32
+    else:
+        kb, unit = (blocks + 7) // 8 * 8, 8 // planes
+        be = 128 if E <= 128 or planes == 3 else 256
+        bm = 128 if be == 256 or planes == 3 else 64
+        tiles = -(-M // bm) * -(-E // be)
+        splits = min(8, max(1, (256 if be == 256 else 512) // tiles))
+    units = -(-kb // unit)
+    per = -(-units // min(splits, units)) * unit
+    return -(-kb // per) * M * (-(-E // 16) * 16 + 1)
+
+
+@pytest.mark.parametrize("E,H,weight", [(256, 7168, "bf16"), (128, 4096, "bf16"), (512, 2560, "fp32"), (8, 8, "fp32"),
+                                        (100, 264, "bf16"), (300, 65536, "bf16"), (130, 1000, "fp32"), (512, 520, "bf16")])
+def test_router_workspace_is_the_most_that_any_call_needs(E, H, weight):
+    planes, most, M = 3 if weight == "fp32" else 1, 0, 0
+    for cap in (1, 15, 16, 100, 256, 257, 300, 511, 600, 1000, 1030, 2047, 4096, 5000, 8200, 16384, 20000, 32768, 33000,
+                40000):
+        while M < cap:
+            M += 1
+            most = max(most, _route_floats(E, H, planes, M))
+        need = -(-4 * most // 256) * 256
+        assert block.router_workspace_bytes(block.RouterDesc(E, H, 1, cap, weight=weight), 1) == need, cap
+
+
+def test_route_takes_the_host_no_longer_for_a_large_capacity(L):
+    """A call refused at its last check (a workspace of one byte too few) takes
+    on the host what it takes whatever max_tokens is: at most twice as long,
+    and half a microsecond."""
+    best = []
+    for cap in (1, 4096, 32768, 1 << 20):
+        d = block.RouterDesc(256, 7168, 8, cap, scoring="sigmoid")
+        need = block.router_workspace_bytes(d, 1)
+        P, X, I, W, S = (1 << b for b in (28, 30, 31, 32, 40))
+        args = (ctypes.byref(d.c()), P, X, 1, None, I, W, None, S, need - 1, None)
+        times = []
+        for _ in range(15):
+            t = time.perf_counter()
+            for _ in range(400):
+                status = L.moe_fp4_route(*args)
+            times.append((time.perf_counter() - t) / 400)
+        assert status == EWORKSPACE
+        best.append(min(times))
+    assert max(best) <= 2 * best[0] + 0.5e-6, best
