@@ -87,6 +87,7 @@ moe_fp4_status moe_fp4_router_prepare(const moe_fp4_router_desc* desc, const voi
   if (st != MOE_FP4_OK) return st;
   if (!weight || !prepared || !aligned(weight, 16) || !aligned(prepared, 256)) return MOE_FP4_EINVAL;
   if ((int64_t)prepared_bytes < s.prepared_bytes()) return MOE_FP4_EWORKSPACE;
+  if (overlap(weight, (s.planes == 3 ? 4ll : 2ll) * s.E * s.H, prepared, s.prepared_bytes())) return MOE_FP4_EINVAL;
   return from_hip(moe::launch_router_prepare(s, weight, (uint8_t*)prepared, (hipStream_t)stream));
 }
 
@@ -117,7 +118,8 @@ moe_fp4_status moe_fp4_route(const moe_fp4_router_desc* desc, const void* prepar
     int64_t bytes;
   } in[] = {{x, 2ll * M * s.H}, {bias, 4ll * s.E}, {prepared, s.prepared_bytes()}, {workspace, need}},
     out[] = {{topk_ids, 4ll * M * s.k}, {topk_w, 4ll * M * s.k}, {logits, 4ll * M * s.E}};
-  if (overlap(x, in[0].bytes, workspace, in[3].bytes)) return MOE_FP4_EINVAL;
+  for (int i = 0; i < 3; ++i)
+    if (overlap(in[i].p, in[i].bytes, workspace, need)) return MOE_FP4_EINVAL;
   for (int o = 0; o < 3; ++o) {
     for (const auto& i : in)
       if (overlap(out[o].p, out[o].bytes, i.p, i.bytes)) return MOE_FP4_EINVAL;
@@ -146,6 +148,10 @@ moe_fp4_status moe_fp4_fp8_prepare(const moe_fp4_fp8_desc* desc, const uint8_t* 
   if (!codes || !scales || !prepared || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(prepared, 256))
     return MOE_FP4_EINVAL;
   if ((int64_t)prepared_bytes < s.prepared_bytes()) return MOE_FP4_EWORKSPACE;
+  const int64_t nb = (s.N + 127) / 128;
+  if (overlap(codes, (int64_t)s.halves() * s.N * s.K, prepared, s.prepared_bytes()) ||
+      overlap(scales, 4 * s.halves() * nb * s.kblocks(), prepared, s.prepared_bytes()))
+    return MOE_FP4_EINVAL;
   return from_hip(moe::launch_fp8_prepare(s, codes, scales, (uint8_t*)prepared, (hipStream_t)stream));
 }
 
@@ -170,7 +176,8 @@ moe_fp4_status moe_fp4_fp8_linear(const moe_fp4_fp8_desc* desc, const void* prep
     return MOE_FP4_EINVAL;
   const int64_t need = moe::fp8_workspace(s, desc->max_tokens), out_bytes = 2ll * M * s.N;
   if (overlap(out, out_bytes, x, 2ll * M * s.K) || overlap(out, out_bytes, prepared, s.prepared_bytes()) ||
-      overlap(out, out_bytes, workspace, need) || overlap(x, 2ll * M * s.K, workspace, need))
+      overlap(out, out_bytes, workspace, need) || overlap(x, 2ll * M * s.K, workspace, need) ||
+      overlap(prepared, s.prepared_bytes(), workspace, need))
     return MOE_FP4_EINVAL;
   if ((int64_t)workspace_bytes < need) return MOE_FP4_EWORKSPACE;
   return from_hip(moe::launch_fp8_linear(s, (const uint8_t*)prepared, x, M, out, (uint8_t*)workspace,

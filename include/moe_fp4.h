@@ -366,7 +366,7 @@ typedef struct {
 /* Bytes of the prepared router weights, and the preparation, once per
  * router: a permutation of Wr ([E][H], device, 16-byte aligned; fp32 as three
  * bf16 terms that sum to it), the experts' 2-norms and Wr's rows as they are,
- * into `prepared` (device, 256-byte aligned). */
+ * into `prepared` (device, 256-byte aligned, not overlapping Wr). */
 moe_fp4_status moe_fp4_router_prepared_bytes(const moe_fp4_router_desc* desc, size_t* bytes);
 moe_fp4_status moe_fp4_router_prepare(const moe_fp4_router_desc* desc, const void* weight, void* prepared,
                                       size_t prepared_bytes, void* stream);
@@ -378,8 +378,8 @@ moe_fp4_status moe_fp4_router_workspace_bytes(const moe_fp4_router_desc* desc, i
 /* Routes M tokens.  x: bf16 [M][H], 16-byte aligned; bias: fp32 [E] or NULL;
  * topk_ids: int32 [M][k] and topk_w: fp32 [M][k], overwritten; logits: fp32
  * [M][E], overwritten, or NULL.  No output may overlap another, the workspace
- * or anything that is read, nor x the workspace.  M may be 0 (nothing is
- * launched). */
+ * or anything that is read, nor the workspace anything that is read.  M may be
+ * 0 (nothing is launched). */
 moe_fp4_status moe_fp4_route(const moe_fp4_router_desc* desc, const void* prepared, const uint16_t* x, int32_t M,
                              const float* bias, int32_t* topk_ids, float* topk_w, float* logits, void* workspace,
                              size_t workspace_bytes, void* stream);
@@ -414,10 +414,11 @@ typedef struct {
 } moe_fp4_fp8_desc;
 
 /* Bytes of the prepared weights, and the preparation, once per map: a
- * permutation of the bytes into `prepared` (device, 256-byte aligned).
- * codes: E4M3 bytes [N][K] (device, 16-byte aligned), scales: fp32
- * [ceil(N / 128)][ceil(K / 128)]; for a gated activation both hold the gate's
- * and then the up's ([2N][K], [2 ceil(N / 128)][ceil(K / 128)]). */
+ * permutation of the bytes into `prepared` (device, 256-byte aligned, not
+ * overlapping what is read).  codes: E4M3 bytes [N][K] (device, 16-byte
+ * aligned), scales: fp32 [ceil(N / 128)][ceil(K / 128)]; for a gated
+ * activation both hold the gate's and then the up's ([2N][K],
+ * [2 ceil(N / 128)][ceil(K / 128)]). */
 moe_fp4_status moe_fp4_fp8_prepared_bytes(const moe_fp4_fp8_desc* desc, size_t* bytes);
 moe_fp4_status moe_fp4_fp8_prepare(const moe_fp4_fp8_desc* desc, const uint8_t* codes, const float* scales,
                                    void* prepared, size_t prepared_bytes, void* stream);
@@ -427,7 +428,8 @@ moe_fp4_status moe_fp4_fp8_prepare(const moe_fp4_fp8_desc* desc, const uint8_t* 
 moe_fp4_status moe_fp4_fp8_workspace_bytes(const moe_fp4_fp8_desc* desc, int32_t M, size_t* bytes);
 
 /* The map on M tokens.  x: bf16 [M][K], out: bf16 [M][N], overwritten; both
- * 16-byte aligned, not overlapping each other or the workspace.  M may be 0 (nothing is launched). */
+ * 16-byte aligned.  Neither may overlap the other or the workspace, nor out or
+ * the workspace the prepared weights.  M may be 0 (nothing is launched). */
 moe_fp4_status moe_fp4_fp8_linear(const moe_fp4_fp8_desc* desc, const void* prepared, const uint16_t* x, int32_t M,
                                   uint16_t* out, void* workspace, size_t workspace_bytes, void* stream);
 

@@ -202,3 +202,27 @@ def test_route_takes_the_host_no_longer_for_a_large_capacity(L):
         assert status == EWORKSPACE
         best.append(min(times))
     assert max(best) <= 2 * best[0] + 0.5e-6, best
+
+
+def test_workspaces_and_prepared_weights_lie_apart_from_what_is_read(L):
+    d = _router()
+    ref = ctypes.byref(d.c())
+    need, prep = block.router_workspace_bytes(d, 8), block.router_prepared_bytes(d)
+    P, X, I, W, S = (1 << b for b in range(20, 25))
+
+    def route(prepared=P, bias=None, ws=S):
+        return L.moe_fp4_route(ref, prepared, X, 8, bias, I, W, None, ws, need, None)
+
+    assert route(ws=P) == EINVAL and route(ws=P + prep - 256) == EINVAL  # over the prepared weights
+    assert route(bias=S + need - 4) == EINVAL and route(bias=S - 252) == EINVAL  # the bias in it
+    assert L.moe_fp4_router_prepare(ref, P, P, 1 << 30, None) == EINVAL
+    assert L.moe_fp4_router_prepare(ref, P - 2 * 64 * 256 + 16, P, 1 << 30, None) == EINVAL  # the weights' last bytes
+    assert L.moe_fp4_router_prepare(ref, P + prep - 16, P, 1 << 30, None) == EINVAL
+    f = block.Fp8Desc(264, 136, 8, fn="silu")
+    ref = ctypes.byref(f.c())
+    need, prep = block.fp8_workspace_bytes(f, 8), block.fp8_prepared_bytes(f)
+    assert L.moe_fp4_fp8_linear(ref, P, X, 8, I, P + prep - 256, need, None) == EINVAL
+    assert L.moe_fp4_fp8_linear(ref, P, X, 8, I, P, need, None) == EINVAL
+    assert L.moe_fp4_fp8_prepare(ref, P - 272 * 264 + 16, X, P, 1 << 30, None) == EINVAL  # the codes' last bytes
+    assert L.moe_fp4_fp8_prepare(ref, X, P - 4 * 4 * 3 + 4, P, 1 << 30, None) == EINVAL  # the scales' last
+    assert L.moe_fp4_fp8_prepare(ref, X, P + prep - 4, P, 1 << 30, None) == EINVAL
