@@ -17,6 +17,11 @@ moe_fp4_status from_hip(hipError_t e) { return e == hipSuccess ? MOE_FP4_OK : MO
 // Largest max_tokens of the router and the FP8 map.
 constexpr int kMaxTokens = 1 << 20;
 
+// Largest out_features of the FP8 map: the few tokens' kernel takes 16 rows a
+// workgroup of 256 threads (K up to 512; N is smaller for larger ones), gate
+// and up twice N, and a launch has fewer than 2^32 threads.
+constexpr int kMaxOutFeatures = 1 << 26;
+
 // Whether [p, p + n) and [q, q + m) share a byte.
 bool overlap(const void* p, int64_t n, const void* q, int64_t m) {
   const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
@@ -58,8 +63,8 @@ moe_fp4_status fp8_shape(const moe_fp4_fp8_desc* d, moe::Fp8Shape* s) {
   if (d->act_fn == MOE_FP4_FN_SWIGLUOAI &&
       (!std::isfinite(d->act_alpha) || !std::isfinite(d->act_beta) || !(d->act_limit > 0.0f)))
     return MOE_FP4_EINVAL;
-  if (d->in_features > 1 << 20 || (int64_t)d->in_features * d->out_features > (int64_t)1 << 30 ||
-      d->max_tokens > kMaxTokens)
+  if (d->in_features > 1 << 20 || d->out_features > kMaxOutFeatures ||
+      (int64_t)d->in_features * d->out_features > (int64_t)1 << 30 || d->max_tokens > kMaxTokens)
     return MOE_FP4_EUNSUPPORTED;
   const bool act = d->act_fn != MOE_FP4_FN_NONE;
   *s = moe::Fp8Shape{d->in_features, d->out_features, act && d->act_fn != MOE_FP4_FN_RELU2,

@@ -405,7 +405,7 @@ moe_fp4_status moe_fp4_route(const moe_fp4_router_desc* desc, const void* prepar
  * and not to y. */
 typedef struct {
   int32_t in_features;  /* K, a multiple of 8, at most 2^20 */
-  int32_t out_features; /* N, a multiple of 8; K * N at most 2^30 */
+  int32_t out_features; /* N, a multiple of 8, at most 2^26; K * N at most 2^30 */
   int32_t max_tokens;   /* capacity for workspace sizing, at most 2^20 */
   int32_t act_fn;       /* MOE_FP4_FN_NONE or a moe_fp4_act_fn */
   float act_alpha;      /* SWIGLUOAI only, else ignored */

@@ -226,3 +226,9 @@ def test_workspaces_and_prepared_weights_lie_apart_from_what_is_read(L):
     assert L.moe_fp4_fp8_prepare(ref, P - 272 * 264 + 16, X, P, 1 << 30, None) == EINVAL  # the codes' last bytes
     assert L.moe_fp4_fp8_prepare(ref, X, P - 4 * 4 * 3 + 4, P, 1 << 30, None) == EINVAL  # the scales' last
     assert L.moe_fp4_fp8_prepare(ref, X, P + prep - 4, P, 1 << 30, None) == EINVAL
+
+
+@pytest.mark.parametrize("N,fn,status", [(1 << 26, "silu", 0), (1 << 26, "none", 0), ((1 << 26) + 8, "none", EUNSUPPORTED),
+                                         (1 << 27, "silu", EUNSUPPORTED)])
+def test_fp8_rows_that_a_launch_has_threads_for(L, N, fn, status):
+    assert _sized(L.moe_fp4_fp8_prepared_bytes, block.Fp8Desc(8, N, 1, fn=fn))[0] == status
