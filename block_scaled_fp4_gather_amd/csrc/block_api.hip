@@ -215,8 +215,9 @@ moe_fp4_status moe_fp4_block_norm(const moe_fp4_norm_desc* desc, int32_t M, cons
   if (!aligned(h, 16) || !aligned(y, 16) || !aligned(y2, 16) || !aligned(gate, gate_align) ||
       !aligned(post_weight, 16) || !aligned(pre_weight, 16) || !aligned(h_out, 16) || !aligned(x_out, 16))
     return MOE_FP4_EINVAL;
-  // a row is read whole before it is written, so an output may take the place
-  // of an input row for row (same address and type), and nothing else
+  // h, y and y2 are read, a row whole, before it is written, so an output may
+  // take their place row for row (same address and type); the gate and the
+  // norms' weights are read in between
   const int64_t rb = d.residual_type == MOE_FP4_TYPE_F32 ? 4 : 2, wb = d.weight_type == MOE_FP4_TYPE_F32 ? 4 : 2;
   const int64_t n = (int64_t)M * d.hidden;
   const int64_t gate_n = d.gate == MOE_FP4_GATE_FULL ? n : d.gate == MOE_FP4_GATE_TOKEN ? M : d.hidden;

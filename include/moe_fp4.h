@@ -466,9 +466,9 @@ typedef struct {
  * MOE_FP4_GATE_NONE; post_weight, pre_weight: [H] or NULL; h_out: [M][H],
  * given exactly when y is; x_out: bf16 [M][H], given exactly when pre_weight
  * is.  Device pointers, 16-byte aligned (a token gate: its element's size).
- * An output may be one of the [M][H] inputs itself where the types agree
- * (h_out = h updates the residual in place); any other overlap is refused.
- * M may be 0 (nothing is launched). */
+ * An output may be h, y or y2 itself where the types agree (h_out = h updates
+ * the residual in place); any other overlap is refused, that with a gate of
+ * [M][H] too.  M may be 0 (nothing is launched). */
 moe_fp4_status moe_fp4_block_norm(const moe_fp4_norm_desc* desc, int32_t M, const void* h, const uint16_t* y,
                                   const uint16_t* y2, const void* gate, const void* post_weight,
                                   const void* pre_weight, void* h_out, uint16_t* x_out, void* stream);

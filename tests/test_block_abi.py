@@ -232,3 +232,14 @@ def test_workspaces_and_prepared_weights_lie_apart_from_what_is_read(L):
                                          (1 << 27, "silu", EUNSUPPORTED)])
 def test_fp8_rows_that_a_launch_has_threads_for(L, N, fn, status):
     assert _sized(L.moe_fp4_fp8_prepared_bytes, block.Fp8Desc(8, N, 1, fn=fn))[0] == status
+
+
+@pytest.mark.parametrize("out", ["h_out", "x_out"])
+def test_block_norm_writes_over_no_gate(L, out):
+    """A gate of [M][H] in the residual's type is no place for an output."""
+    H, M = 64, 4
+    at = dict(h=1 << 12, y=1 << 14, gate=1 << 16, pre=1 << 18, h_out=1 << 20, x_out=1 << 22)
+    at[out] = at["gate"]
+    c = block._NormDesc(H, 0, 0, block.GATE_FULL, 0, 1e-6, 1.0, 1.0, 0.0)
+    assert L.moe_fp4_block_norm(ctypes.byref(c), M, at["h"], at["y"], None, at["gate"], None, at["pre"], at["h_out"],
+                                at["x_out"], None) == EINVAL

@@ -106,3 +106,19 @@ def test_route_softmax_of_logits_off_by_more_than_an_exponent(M, biased, groups)
     rid, _, z = ref.route(x, w, 1, "softmax", bias, groups, 1)
     assert bool((rid == 61).all()) and torch.equal(z[:, 61] - z[:, 3], torch.ones(M, dtype=torch.float64))
     assert torch.equal(ids.cpu(), rid)
+
+
+@pytest.mark.parametrize("H", [264, 4096, 16384])
+@pytest.mark.parametrize("h_in,x_in", [("h", "y"), ("y", "h"), ("y2", "y"), ("h", "y2"), (None, "h"), ("y", None)])
+def test_block_norm_over_its_inputs(H, h_in, x_in):
+    """Outputs in the place of h, y and y2: what they are elsewhere."""
+    M = 5
+    t = {n: rand(i, M, H).bfloat16().cuda() for i, n in enumerate(("h", "y", "y2"))}
+    w = (1 + 0.1 * rand(7, H)).bfloat16().cuda()
+    gate = (1 + 0.1 * rand(8, M, H)).bfloat16().cuda()
+    kw = dict(gate=gate, post_weight=w, pre_weight=w, residual_scale=0.75)
+    want = block.block_norm(t["h"], t["y"], t["y2"], **kw)
+    got = block.block_norm(t["h"], t["y"], t["y2"], h_out=t.get(h_in), x_out=t.get(x_in), **kw)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert h_in is None or got[0] is t[h_in]
+    assert x_in is None or got[1] is t[x_in]
