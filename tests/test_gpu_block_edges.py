@@ -9,7 +9,7 @@ import torch
 import block_ref as ref
 from block_scaled_fp4_gather_amd import block
 from gpu_util import say
-from test_gpu_block import make_router, rand
+from test_gpu_block import fp8_weights, hidden, make_router, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -122,3 +122,110 @@ def test_block_norm_over_its_inputs(H, h_in, x_in):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert h_in is None or got[0] is t[h_in]
     assert x_in is None or got[1] is t[x_in]
+
+
+def logits_coefficient(E, H, planes, M):
+    """The kernel's bound on a logit's error over the magnitudes of its
+    products, from the plan of a call: chains of 8 instructions of four groups
+    each, a group's cuts, the sums over chains, waves and slices."""
+    blocks = -(-H // 32)
+    if M <= 256:
+        kb, unit, splits = blocks, 4, -(-blocks // 32)
+    else:
+        kb, unit = -(-blocks // 8) * 8, 8 // planes
+        wide = E > 128 and planes == 1
+        tiles = -(-M // (128 if wide or planes == 3 else 64)) * -(-E // (256 if wide else 128))
+        splits = min(8, max(1, (256 if wide else 512) // tiles))
+    units = -(-kb // unit)
+    per = -(-units // min(splits, units)) * unit
+    return (4 * 8 + 8 + per * planes // 4 + 4 + -(-kb // per)) * 2.0 ** -24
+
+
+LOGITS = [  # M, H, E, weight: every kernel of the logits, in one slice and in several
+    (5, 512, 40, "bf16"), (16, 7168, 256, "bf16"), (30, 4096, 100, "fp32"), (200, 2560, 200, "bf16"),
+    (256, 7168, 300, "fp32"), (257, 7168, 64, "bf16"), (300, 7168, 256, "bf16"), (300, 2560, 512, "fp32"),
+    (17000, 1096, 100, "bf16"), (17000, 2048, 256, "bf16"), (16500, 1096, 130, "fp32"),
+]
+
+
+@pytest.mark.parametrize("signs", ["mixed", "alike"])
+@pytest.mark.parametrize("M,H,E,weight", LOGITS)
+def test_logits_are_within_the_bound_that_the_choice_goes_by(M, H, E, weight, signs):
+    """Values of very different sizes, of both signs and of one, where cuts
+    towards zero add up.  Recomputed logits are exact."""
+    x = rand(1, M, H) * torch.exp2(3 * rand(2, 1, H))
+    w = rand(3, E, H) * torch.exp2(rand(4, E, H)) / math.sqrt(H)
+    if signs == "alike":
+        x, w = x.abs(), w.abs()
+    x = x.bfloat16()
+    router, w = make_router(E, H, min(E, 4), M, weight, None, w=w)
+    lg = torch.empty(M, E, device="cuda")
+    router(x.cuda(), logits=lg)
+    rows = torch.unique(torch.cat([torch.arange(0, M, max(1, M // 300)), torch.arange(max(0, M - 70), M)]))
+    xd, wd = x[rows].double(), w.double()
+    z = xd @ wd.t()
+    bound = logits_coefficient(E, H, 3 if weight == "fp32" else 1, M) * xd.norm(dim=1, keepdim=True) * wd.norm(dim=1).max()
+    off = (lg.cpu().double()[rows] - z).abs()
+    say(f"  largest error over the bound {float((off / bound).max()):.3f}, over the magnitudes' "
+        f"{float((off / (bound / (xd.norm(dim=1, keepdim=True) * wd.norm(dim=1).max()) * (xd.abs() @ wd.abs().t()))).max()):.3f}")
+    assert bool((off <= bound + z.abs() * 2.0 ** -24).all())
+
+
+@pytest.mark.parametrize("scoring,biased,groups,top_groups", [
+    ("softmax", False, 1, 1), ("sigmoid", True, 1, 1), ("sigmoid", True, 8, 3), ("softmax", True, 8, 3)])
+@pytest.mark.parametrize("M,H,E,weight", [
+    (300, 1024, 64, "bf16"), (300, 256, 64, "bf16"), (17000, 1024, 64, "bf16"),     # tiles of 64 x 128
+    (300, 1024, 200, "bf16"), (300, 256, 200, "bf16"), (17000, 520, 200, "bf16"),   # of 128 x 256
+    (300, 1024, 64, "fp32"), (300, 64, 200, "fp32"), (8500, 1024, 200, "fp32")])    # of three planes
+def test_route_near_ties_of_many_tokens(M, H, E, weight, scoring, biased, groups, top_groups):
+    """Near copies of eight experts, as in the few tokens' test, through the
+    tiled kernels with several slices of H and with one."""
+    w = rand(11, E, H) / math.sqrt(2 * H)
+    w = w.bfloat16() if weight == "bf16" else w
+    for e in range(8, E):
+        w[e] = w[e % 8]
+        if e % 3:
+            c = (37 * e) % H
+            w[e, c] = w[e, c] * (1 + (2.0 ** -7 if weight == "bf16" else 2.0 ** -20))
+    bias = (0.02 * rand(12, 8)).repeat(E // 8) if biased else None
+    x = hidden(21, min(M, 600), H).repeat(-(-M // 600), 1)[:M] if M > 600 else hidden(21, M, H)
+    router, w = make_router(E, H, 12, M, weight, bias, w=w, scoring=scoring, groups=groups, top_groups=top_groups)
+    ids, wt = router(x.cuda())
+    # Copies of an expert have one logit.  A product over all experts does not
+    # give them that (it may sum some columns in another order: 2^-52 apart,
+    # seen once in 600 rows), so it is taken over the distinct ones; the
+    # identity passes it on as it is.
+    kinds, of = torch.unique(w, dim=0, return_inverse=True)
+    z = (x[:600].double() @ kinds.double().t())[:, of]
+    rid, rw, _ = ref.route(z, torch.eye(E), 12, scoring, bias, groups, top_groups)
+    at = torch.arange(M) % 600
+    assert torch.equal(ids.cpu(), rid[at])
+    delta = logits_coefficient(E, H, 3 if weight == "fp32" else 1, M) * float(x.double().norm(dim=1).max() * w.double().norm(dim=1).max())
+    # a weight is a quotient of p and their sum, each within e^delta of its own, and a few roundings
+    assert bool(((wt.cpu().double() - rw[at]).abs() <= rw[at] * (4 * delta + 2.0 ** -22)).all())
+
+
+def test_a_long_prompt_in_sampled_rows():
+    """The largest plans whole: 16384 tokens through the grouped router of 256
+    experts, 8192 through the gated FP8 map.  Rows at the borders of tiles and
+    some between them, each against 64 bits."""
+    M, H, E = 16384, 7168, 256
+    bias = 0.05 * rand(9, E)
+    x = hidden(90, M, H)
+    router, w = make_router(E, H, 8, M, "bf16", bias, scoring="sigmoid", groups=8, top_groups=4, scale=1.5)
+    ids, wt = router(x.cuda())
+    rows = torch.unique(torch.cat([torch.arange(0, M, 257), torch.arange(127, M, 1024), torch.arange(128, M, 1024),
+                                   torch.arange(M - 5, M)]))
+    rid, rw, _ = ref.route(x[rows], w, 8, "sigmoid", bias, 8, 4, True, 1.5)
+    assert torch.equal(ids.cpu()[rows], rid)
+    delta = logits_coefficient(E, H, 1, M) * float(x[rows].double().norm(dim=1).max() * w.double().norm(dim=1).max())
+    assert bool(((wt.cpu().double()[rows] - rw).abs() <= rw * (4 * delta + 2.0 ** -22)).all())
+    M, K, N = 8192, 7168, 2048
+    act = dict(alpha=1.702, beta=1.0, limit=7.0)
+    desc = block.Fp8Desc(K, N, M, fn="swigluoai", **act)
+    codes, scales = fp8_weights(91, desc.rows, K, N)
+    y = block.Fp8Linear(desc, codes, scales)(x[:M].cuda()).cpu().double()
+    rows = torch.unique(torch.cat([torch.arange(0, M, 409), torch.arange(255, M, 2048), torch.arange(256, M, 2048),
+                                   torch.tensor([M - 1])]))
+    want, tol = ref.fp8_linear(x[rows], codes, scales, N, "swigluoai", **act)
+    assert bool(((y[rows] - want).abs() <= tol + (want.abs() + tol) * 2.0 ** -8 + 2.0 ** -133).all())
