@@ -41,7 +41,10 @@ class RouterBuild:
         desc = block.RouterDesc(self.E, self.H, self.k, self.M, weight="fp32", scoring="sigmoid")
         router = block.Router(desc, *tensors, stream=stream)
         ids, w = router(hidden(1, self.M, self.H).cuda())
-        return router.prepared, router.bias, ids, w
+        # operands and norms, then from the next multiple of 256 the rows; the bytes between are not written
+        end = 3 * -(-self.E // 16) * (-(-self.H // 256) * 8) * 1024 + 4 * self.E
+        rows = -(-end // 256) * 256
+        return router.prepared[:end], router.prepared[rows:rows + 4 * self.E * self.H], router.bias, ids, w
 
 
 class Fp8Build:
@@ -53,7 +56,7 @@ class Fp8Build:
 
     def __call__(self, tensors, stream=None):
         lin = block.Fp8Linear(block.Fp8Desc(self.K, self.N, self.M), *tensors, stream=stream)
-        # rows of padding in the scales are never written
+        # columns of padding in the scales are not written; the scales show in the output
         return lin.prepared[:16 * -(-self.N // 16) * 128 * -(-self.K // 128)], lin(hidden(2, self.M, self.K).cuda())
 
 
@@ -71,7 +74,10 @@ class LayerBuild:
         w = self.wl
         layer = moe.Fp4MoE(moe.Desc(w.fmt, w.E, w.H, w.I, w.k, w.M), *tensors, stream=stream)
         y = layer(to_dev(self.d["x"]).view(torch.bfloat16), to_dev(self.d["ids"]), to_dev(self.d["w"]))
-        return layer.prepared, y
+        back = [torch.empty(self.d[n].shape, dtype=torch.uint8, device="cuda")
+                for n in ("w13_codes", "w13_scales", "w2_codes", "w2_scales")]
+        moe.unprepare(layer.desc, layer.prepared, *back, None, None)
+        return *back, y
 
 
 @pytest.mark.parametrize("raw", [False, True])
