@@ -229,3 +229,62 @@ def test_a_long_prompt_in_sampled_rows():
                                    torch.tensor([M - 1])]))
     want, tol = ref.fp8_linear(x[rows], codes, scales, N, "swigluoai", **act)
     assert bool(((y[rows] - want).abs() <= tol + (want.abs() + tol) * 2.0 ** -8 + 2.0 ** -133).all())
+
+
+@pytest.mark.parametrize("weight,scoring,biased", [("fp32", "sigmoid", True), ("bf16", "softmax", False)])
+@pytest.mark.parametrize("M", [1, 37, 300])
+def test_route_at_the_largest_sizes(M, weight, scoring, biased):
+    """65536 values, 512 experts in 64 groups, 64 experts a token."""
+    E, H, k = 512, 65536, 64
+    bias = 0.05 * rand(9, E) if biased else None
+    x = hidden(1, M, H)
+    w = (rand(3, E, H) / math.sqrt(2 * H)).to(torch.bfloat16 if weight == "bf16" else torch.float32)
+    router, w = make_router(E, H, k, M, weight, bias, w=w, scoring=scoring, groups=64, top_groups=9)
+    ids, wt = router(x.cuda())
+    rid, rw, _ = ref.route(x, w, k, scoring, bias, 64, 9)
+    assert torch.equal(ids.cpu(), rid)
+    delta = logits_coefficient(E, H, 3 if weight == "fp32" else 1, M) * float(x.double().norm(dim=1).max() * w.double().norm(dim=1).max())
+    assert bool(((wt.cpu().double() - rw).abs() <= rw * (4 * delta + 2.0 ** -22)).all())
+
+
+def test_route_of_a_million_tokens():
+    E, H, k, M = 16, 64, 3, 1 << 20
+    x = hidden(1, M, H)
+    router, w = make_router(E, H, k, M, "bf16", None, scoring="sigmoid")
+    ids, _ = router(x.cuda())
+    rid, _, z = ref.route(x, w, k, "sigmoid")
+    assert torch.equal(ids.cpu(), rid)
+
+
+@pytest.mark.parametrize("M", [1, 3, 16, 40, 300])
+def test_fp8_longest_rows(M):
+    K, N = 1 << 20, 8
+    codes, scales = fp8_weights(4, N, K, N)
+    x = hidden(5, M, K)
+    y = block.Fp8Linear(block.Fp8Desc(K, N, M), codes, scales)(x.cuda()).cpu().double()
+    want, tol = ref.fp8_linear(x, codes, scales, N)
+    assert bool(((y - want).abs() <= tol + (want.abs() + tol) * 2.0 ** -8).all())
+
+
+@pytest.mark.parametrize("M", [1, 20])
+def test_fp8_most_rows(M):
+    """2^26 outputs of 8 values with gate and up, the last ones at their place."""
+    K, N = 8, 1 << 26
+    g = torch.Generator(device="cuda").manual_seed(6)
+    codes = torch.randint(0, 120, (2 * N, K), generator=g, dtype=torch.uint8, device="cuda")
+    scales = torch.rand(2 * N // 128, 1, generator=g, device="cuda") + 0.5
+    x = torch.eye(8)[torch.arange(M) % 8].bfloat16()  # one value a token: one weight an output, and no cut
+    y = block.Fp8Linear(block.Fp8Desc(K, N, M, fn="relu2"), codes[:N], scales[:N // 128])(x.cuda())
+    for m in range(M):
+        c = m % 8
+        v = codes[:N, c].view(torch.float8_e4m3fn).float().view(-1, 128) * scales[:N // 128]
+        assert torch.equal(y[m].view(-1, 128), (v * v).bfloat16()), m
+    del y, v
+    y = block.Fp8Linear(block.Fp8Desc(K, N, M, fn="silu"), codes, scales)(x.cuda())
+    for m in range(0, M, 7):
+        c = m % 8
+        gate, up = (codes[i * N:(i + 1) * N, c].view(torch.float8_e4m3fn).float().view(-1, 128) *
+                    scales[i * (N // 128):(i + 1) * (N // 128)] for i in (0, 1))
+        want = gate / (1 + torch.exp(-gate)) * up
+        # the activation within 2^-16 as elsewhere, and the rounding to bf16
+        assert bool(((y[m].view(-1, 128).float() - want).abs() <= want.abs() * (2.0 ** -8 + 2.0 ** -15)).all()), m
