@@ -1054,7 +1054,9 @@ __device__ __forceinline__ void finish(const RouterShape& shape, SelectLds<NI>& 
   const bool on = lane < kept;
   const int taken = on ? L.taken[lane] : 0;
   const double zw = L.z[taken];
-  const double mx = s.sigmoid || kept == 0 ? 0.0 : wave_max(on ? zw : kNone);  // of those taken
+  // the largest logit of those taken, from a finite one on: weights of -infinity
+  // leave logits of -infinity, which a bias may have taken, with p = 0
+  const double mx = s.sigmoid || kept == 0 ? 0.0 : fmax(wave_max(on ? zw : kNone), -0x1p1000);
   double p = exp(s.sigmoid ? -zw : zw - mx);
   if (s.sigmoid) {
     p = on ? 1.0 / (1.0 + p) : 0.0;

@@ -346,10 +346,13 @@ typedef enum {
  *     times scale.
  * The choice is that of z in exact arithmetic and t in 64 bits, whatever M:
  * logits are fp32 matrix products, and those that decide something within
- * their error bound are recomputed in 64 bits.  An expert whose t is NaN or
- * -infinity (a bias of -infinity masks one) is never taken; a token with
- * fewer than top_k experts to take gets id -1 and weight 0 in the slots
- * left, which the layer's calls skip.  Weights that sum to 0 stay 0. */
+ * their error bound are recomputed in 64 bits.  An expert whose t (without a
+ * bias, whose z) is NaN or -infinity (a bias of -infinity masks one) is never
+ * taken, and a group with fewer than two others has the score -infinity; a
+ * token with fewer than top_k experts to take gets id -1 and weight 0 in the
+ * slots left, which the layer's calls skip.  Weights that sum to 0 stay 0; a
+ * softmax's, renormalised, are those of a softmax over the taken experts, also
+ * where p itself is too small for a number. */
 typedef struct {
   int32_t num_experts; /* E, at most 512 */
   int32_t hidden;      /* H, a multiple of 8, at most 65536 */

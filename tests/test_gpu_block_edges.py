@@ -288,3 +288,36 @@ def test_fp8_most_rows(M):
         want = gate / (1 + torch.exp(-gate)) * up
         # the activation within 2^-16 as elsewhere, and the rounding to bf16
         assert bool(((y[m].view(-1, 128).float() - want).abs() <= want.abs() * (2.0 ** -8 + 2.0 ** -15)).all()), m
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("biased", [True, False])
+@pytest.mark.parametrize("k", [1, 3])
+def test_route_with_infinite_and_nan_weights(k, biased, renorm, scoring):
+    """Experts with a weight of -infinity, of +infinity or of NaN next to
+    ordinary ones: logits of +-infinity and NaN by the sign of x.  An infinity
+    that a bias has taken weighs nothing; no weight is NaN."""
+    E, H, M = 12, 264, 16
+    x = hidden(33, M, H)
+    x[:, 5] = x[:, 5].abs() + 1
+    x[::2, 9] = 2.0
+    x[1::2, 9] = -2.0
+    w = rand(34, E, H) / math.sqrt(2 * H)
+    w[2, 5] = -math.inf          # -infinity for every token
+    w[7, 5] = -math.inf
+    if scoring == "sigmoid":     # a softmax has no probabilities then
+        w[4, 9] = math.inf       # by turns
+        w[9, 100] = math.nan
+    bias = 0.05 * rand(35, E) if biased else None
+    if biased:
+        bias[2] = bias[7] = 8.0  # these first
+    router, w = make_router(E, H, k, M, "fp32", bias, w=w, scoring=scoring, renorm=renorm)
+    ids, wt = router(x.cuda())
+    rid, rw, _ = ref.route(x, w, k, scoring, bias, renorm=renorm)
+    assert torch.equal(ids.cpu(), rid)
+    if biased:
+        assert bool((ids[:, 0].cpu() == (2 if bias[2] >= bias[7] else 7)).all())
+    assert bool(torch.isfinite(wt).all())
+    # exact logits, weights in 64 bits but for an fp32 sum of 12 terms
+    assert bool(((wt.cpu().double() - rw).abs() <= rw * 16 * 2.0 ** -23).all())
