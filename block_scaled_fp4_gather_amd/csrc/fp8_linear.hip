@@ -168,8 +168,8 @@ constexpr int kFusedUnits = 4 * 4 * NW;  // 4 passes of the workgroup's 16-lane 
 // HALVES (a gated map): instead of a pair of subtiles a workgroup takes 8 gate
 // rows and the 8 up rows of the same outputs as one operand of 16 rows, so
 // that twice as many workgroups share the weights.  K = 7168, N = 2048, M = 1:
-// 8.2 us for 8.4 by pairs.  (M = 4: 9.5 for 9.0, since each quantises x: there
-// pairs are taken.)
+// 7.7 us for 8.0 by pairs.  (M = 4: 9.0 for 8.5, since each quantises x: there
+// pairs are taken; with two blocks in flight instead of four, 8.4.)
 template <int FS, int TT, int NW, int U, bool GATED, bool HALVES, bool FUSED>
 __global__ void __launch_bounds__(NW * 64)
     fp8_few_kernel(Fp8Shape s, const uint8_t* __restrict__ prepared, const uint8_t* __restrict__ codes,
@@ -325,11 +325,14 @@ __global__ void __launch_bounds__(NW * 64)
 // (WT x WF), one K block per step.  Tokens and weights, both in operand order,
 // go to LDS by direct copies, SLOTS - 1 steps ahead in a ring of SLOTS, with
 // the scales of the weights and, 4 K blocks to a dword, of the tokens.
-// M = 4096, K = 2048, N = 4096: 35 us, 1.96 PFLOP/s; M = 8192, K = 7168, gate
-// and up of N = 2048: 203 to 244 us, 2.0 to 2.4 PFLOP/s (a library product of
-// 8192^3 in FP8 reaches 2.7).  What bounds it: the products' 16 cycles and the
-// 4 multiply-adds behind each, which a SIMD's two waves take in turn, and a
-// barrier per K block.
+// M = 4096, K = 2048, N = 4096: 36 us, 1.9 PFLOP/s; M = 8192, K = 7168, gate
+// and up of N = 2048: 204 to 242 us, 2.0 to 2.4 PFLOP/s (a library product of
+// 8192^3 in FP8 reaches 2.7).  A product takes a SIMD's matrix core 32 cycles,
+// and the cores are busy 55% and 62% of the waves' time by the counters; 27%
+// and 24% of a wave's time are waits (operands from LDS, copies, the barrier of
+// a K block) and 31% waiting to issue.  Which of these bounds it has not been
+// told apart.  (The 4 multiply-adds behind a product take 16 cycles and fit
+// beside the other wave's product.)
 template <int BM, int BN, int WT, int WF, int SLOTS>
 struct Fp8Tile {
   static constexpr int FS = BN / 16 / WF, TT = BM / 16 / WT;
@@ -558,6 +561,14 @@ hipError_t launch_fp8_linear(const Fp8Shape& s, const uint8_t* prepared, const u
   uint8_t* const xscale = ws + s.code_bytes(M);
   const int kb = s.kblocks();
 #define MOE_FEW(...) launch_few<__VA_ARGS__>(s, prepared, codes, xscale, x, M, out, st)
+  // Up to 4 tokens one launch, if x fits its LDS.  Times of a call in a graph,
+  // in brackets with the quantisation as a launch of its own: K7168 gated N2048,
+  // M = 1 7.7 us (10.2), M = 4 8.5 (10.4); K4096 N4096 5.3 (7.8) and 6.1 (8.0);
+  // K1024 N4096 3.3 (5.2) and 3.5 (5.4); K320 N2560 3.0 (4.6).  Waves and the
+  // blocks that each has in flight go by the K blocks; M = 1: K7168 N2560 with 8
+  // waves 5.8 us for 6.0 with 16; K4096 N4096 with 16 5.3 for 5.4 with 4 (8 take
+  // 5.1); K2048 N4096 with 4 3.5 for 4.1 with 8; K512 N4096 with one block at a
+  // time 3.1 for 3.3 with four.
   if (M <= 4 && M * kb <= (kb > 16 ? kFusedUnits<16> : kFusedUnits<4>))
     return kb > 32 && M * kb <= kFusedUnits<8> ? MOE_FEW(1, 1, 8, 4, true)
            : kb > 32 && s.gated ? MOE_FEW(2, 1, 16, 2, true)
@@ -567,26 +578,33 @@ hipError_t launch_fp8_linear(const Fp8Shape& s, const uint8_t* prepared, const u
                      st, x, M, s.K, s.kblocks(), codes, xscale, s.scale_rows(M));
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  // One subtile a workgroup up to 16 tokens: K4096 N4096, M = 16: 8.3 us for 8.7
-  // with two; K7168 N2048 gated: 11.0 and 11.0.  Past that two, which share the
-  // tokens' operands.
+  // One subtile a workgroup up to 16 tokens: K4096 N4096, M = 16: 8.2 us for 9.1
+  // with two; K7168 gated N2048: 10.6 for 10.8.  Waves as above: K4096 N4096 with
+  // 16 8.2 for 8.6 with 4; K2048 N4096 with 4 6.5 for 6.8 with 16; K512 N4096
+  // with one block at a time 4.9 for 5.3.  Past that two subtiles, which share
+  // the tokens' operands: M = 24, K4096 N4096 9.0 for 9.7 with one, K7168 gated
+  // N2048 11.2 for 13.1 (K512 N4096 5.9 for 5.3).
   if (M <= 16)
     return kb > 16 ? MOE_FEW(1, 1, 16, 2, false) : kb > 4 ? MOE_FEW(1, 1, 4, 4, false) : MOE_FEW(1, 1, 4, 1, false);
   if (M <= 32) return MOE_FEW(2, 2, 8, 1, false);
   // Up to two workgroups of 64 tokens x 64 rows per CU the tiles are no match:
-  // K4096 N4096, M = 256: 14.5 against 20.9 us, M = 512: 23.1 against 25.5;
-  // K1024 N1024, M = 512: 7.7 against 14.3.  Past it they are: K2048 N7168,
-  // M = 320: 15.9 against 21.0.  With 32 rows each while that leaves one per
-  // CU: K4096 N4096, M = 128: 11.7 against 14.4, M = 256: 16.3 against 14.5.
+  // K4096 N4096, M = 256: 14.4 against 23.0 us, M = 512: 22.8 against 23.9;
+  // K1024 N4096, M = 256: 8.4 against 10.8.  Past it they are: K2048 N7168,
+  // M = 384: 15.8 against 20.7; K7168 gated N2048, M = 768: 37 against 44.  (At
+  // K512 N1024 from M = 1100 on: 12.4 against 9.2.)  With 32 rows each while
+  // that leaves one per CU: K4096 N4096, M = 128: 11.3 against 14.3, M = 256: 15.7
+  // against 14.4.
   const int64_t groups = (M + 63) / 64;
   if (groups * ((s.subtiles() + 1) / 2) <= 256) return MOE_FEW(2, 4, 8, 1, false);
   if (groups * ((s.subtiles() + 3) / 4) <= 512) return MOE_FEW(4, 4, 8, 1, false);
 #undef MOE_FEW
   // One workgroup fits a CU, so a launch takes as many rounds as it has 256s of
-  // tiles, and a round of 128 x 128, 256 x 128 or 256 x 256 about 10 : 14 : 20 by
-  // the operands that it reads from LDS.  K4096 N4096, by tile: M = 900 30.2,
-  // 38.9, 52.1 us; M = 1400 46.2, 40.4, 53.2; M = 2500 68.9, 73.2, 57.9; M = 4096
-  // 93.9, 82.6, 71.6.
+  // tiles.  One that is not full of 128 x 128, 256 x 128 or 256 x 256 takes about
+  // 10 : 14 : 20, by the operands that it reads from LDS: K4096 N4096, M = 768,
+  // with the quantisation, 25, 36 and 50 us.  Full ones are dearer for the larger
+  // tiles (M = 4096, 4, 2 and 1 of them: 91, 79, 67), but where they are full the
+  // larger tile is the better in any case: of 34 shapes from K 512 to 7168 and M
+  // 384 to 6000 none takes more than 3% over the best of the three.
   auto rounds = [&](int bm, int bn) {
     return ((M + bm - 1) / bm * (int64_t)((s.subtiles() * 16 + bn - 1) / bn) + 255) / 256;
   };
