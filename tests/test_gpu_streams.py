@@ -122,3 +122,34 @@ def test_a_block_dropped_behind_its_call_is_kept_for_the_stream(shared, monkeypa
     assert all(t.data_ptr() in used for t in held)
     side.synchronize()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("M", [3, 40, 700])
+def test_captured_router_with_a_softmax_and_a_bias(M):
+    """Three launches, the last of which finds its tokens by what the second
+    left in the ids: captured, replayed on new inputs, with eager calls of the
+    same router between the replays."""
+    E, H, k = 96, 520, 6
+    w = (rand(92, E, H) / math.sqrt(2 * H)).bfloat16()
+    xs = [hidden(91 + i, M, H).cuda() for i in range(4)]
+    p = torch.softmax(xs[1][M // 2].cpu().double() @ w.double().t(), 0)
+    bias = (0.1 - p).float()  # evens the scores of one token of xs[1]: all its logits decide
+    router = block.Router(block.RouterDesc(E, H, k, M), w.cuda(), bias.cuda())
+    want = [tuple(t.clone() for t in router(x)) for x in xs]
+    static = xs[0].clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        router(static)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ids, wt = router(static)
+    for i in (1, 0, 1, 3, 2, 1):
+        static.copy_(xs[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(ids, want[i][0]) and torch.equal(wt, want[i][1])
+        eager = router(xs[(i + 1) % 4])
+        torch.cuda.synchronize()
+        assert torch.equal(eager[0], want[(i + 1) % 4][0]) and torch.equal(eager[1], want[(i + 1) % 4][1])
