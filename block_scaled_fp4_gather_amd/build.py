@@ -16,7 +16,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoe_fp4.so")
 SOURCES = ["api.hip", "prepare.hip", "decode_path.hip", "prefill.hip", "prefill_a8.hip", "mxfp8.hip",
-           "router.hip", "fp8_linear.hip", "block_norm.hip", "block_api.hip"]
+           "router.hip", "fp8_linear.hip", "block_norm.hip", "block_api.hip",
+           "fp4_quant.hip", "fp4_linear.hip", "grouped.hip", "routes.hip", "experts_api.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

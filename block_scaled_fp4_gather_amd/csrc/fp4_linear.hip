@@ -1,0 +1,491 @@
+// Linear map with MXFP4 weights and MXFP4 activations:
+//   y[m][n] = sum over blocks b of 32:  sw[n][b] sx[m][b] sum_{k in b} c[n][k] q[m][k]
+// with E2M1 codes c and q and UE8M0 scales, on v_mfma_scale_f32_16x16x128_
+// f8f6f4, which takes codes and scales as they are stored: both operands E2M1,
+// at twice the rate of its FP8 forms.  Sums are fp32; a product of two codes
+// has at most 4 significant bits.  An activation of the framework follows where
+// asked for, and one rounding to bf16.
+//
+// Tokens are quantised as fp4_quant.hip does, and kept in the operand order of
+// the prepared weights (Fp4Shape), so that a wave's load or copy is 1 KiB in a
+// row.  Operands: A = weights (16 rows), B = tokens (16): a lane's four
+// accumulators are consecutive outputs of one token.
+#include <hip/hip_runtime.h>
+
+#include "act.h"
+#include "experts.h"
+#include "fp4_codes.h"
+#include "tile_loop.h"
+
+namespace moe {
+namespace {
+
+// ---- operand order of rows that have codes and scales
+
+// Rows of a matrix [rows][K] as subtiles of 16; `gated` pairs row blocks of
+// two halves of N rows.
+struct RowMap {
+  int64_t N;
+  bool gated;
+  __device__ int64_t row(int64_t sub, int r) const {  // < 0: none
+    const int64_t n = (gated ? sub >> 1 : sub) * 16 + r;
+    return n >= N ? -1 : gated && (sub & 1) ? N + n : n;
+  }
+};
+
+__global__ void __launch_bounds__(256)
+    fp4_pack_kernel(RowMap map, int K, int64_t subs, int ksteps, int64_t pairs, const uint8_t* __restrict__ codes,
+                    const uint8_t* __restrict__ scales, uint8_t* __restrict__ packed, uint32_t* __restrict__ pscales) {
+  const int units = K / 32, kb = 2 * ksteps;
+  const int64_t step = (int64_t)gridDim.x * blockDim.x, me = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  for (int64_t it = me; it < subs * kb * 64; it += step) {
+    const int lane = (int)(it & 63);
+    const int64_t sb = it >> 6, sub = sb / kb;
+    const int u = (int)(sb - sub * kb) * 4 + (lane >> 4);
+    const int64_t row = map.row(sub, lane & 15);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (row >= 0 && u < units) v = *(const uint4*)(codes + (row * units + u) * 16);
+    ((uint4*)packed)[it] = v;
+  }
+  for (int64_t it = me; it < ksteps * pairs * 64; it += step) {
+    const int lane = (int)(it & 63);
+    const int64_t sp = it >> 6, s = sp / pairs, pair = sp - s * pairs;
+    uint32_t v = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t sub = 2 * pair + i / 2;
+      const int u = (int)(2 * s + i % 2) * 4 + (lane >> 4);
+      const int64_t row = map.row(sub, lane & 15);
+      if (row >= 0 && u < units) v |= (uint32_t)scales[row * units + u] << (8 * i);
+    }
+    pscales[it] = v;
+  }
+}
+
+// ---- tokens
+
+// A workgroup per 16 tokens and 512 values: each wave takes 4 tokens, and the
+// codes are put in operand order in LDS.
+__global__ void __launch_bounds__(256)
+    fp4_tokens_kernel(const uint16_t* __restrict__ x, int M, int K, int ksteps, int64_t pairs,
+                      uint8_t* __restrict__ packed, uint8_t* __restrict__ pscales) {
+  __shared__ uint4 turned[256];
+  __shared__ uint8_t bytes[16][16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t group = blockIdx.x;
+  const int q = blockIdx.y;
+  const int c = q * 512 + lane * 8;
+  uint4 raw[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = group * 16 + wave * 4 + i;
+    raw[i] = make_uint4(0, 0, 0, 0);
+    if (c < K && row < M) raw[i] = *(const uint4*)(x + row * K + c);
+  }
+  // this lane's unit of 32 values: K block unit / 4, lane group unit % 4
+  const int unit = lane / 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = wave * 4 + i;
+    uint32_t m = amax8(raw[i]);
+    m = max(m, (uint32_t)__shfl_xor((int)m, 1));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 2));
+    const uint32_t byte = mxfp4_scale_byte(m);
+    ((uint32_t*)turned)[((unit / 4) * 64 + unit % 4 * 16 + r) * 4 + lane % 4] = mxfp4_codes8(raw[i], byte);
+    if (lane % 4 == 0) bytes[r][unit] = (uint8_t)byte;
+  }
+  __syncthreads();
+  const int t = threadIdx.x, kb = 2 * ksteps;
+  if (q * 4 + t / 64 < kb) ((uint4*)(packed + (group * kb + q * 4) * 1024))[t] = turned[t];
+  const int s = q * 2 + t / 64;
+  if (t < 128 && s < ksteps) {
+    const int r = lane & 15, u = (t / 64) * 8 + (lane >> 4);
+    *(uint16_t*)(pscales + ((s * pairs + group / 2) * 64 + lane) * 4 + (group & 1) * 2) =
+        (uint16_t)(bytes[r][u] | bytes[r][u + 4] << 8);
+  }
+}
+
+__device__ __forceinline__ i32x8_t wide(const i32x4_t& v) { return i32x8_t{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
+
+// ---- few tokens: FS subtiles x 16 TT tokens per workgroup, whose NW waves
+// share K in runs of consecutive steps of 256 and join their sums in LDS in
+// wave order.  U steps of a wave are in flight.
+//
+// FUSED: x is quantised by each workgroup itself into LDS, while the first
+// weights are on their way.
+// HALVES (a gated map): instead of a pair of subtiles a workgroup takes 8 gate
+// rows and the 8 up rows of the same outputs as one operand of 16 rows, so that
+// twice as many workgroups share the weights.
+
+template <int NW>
+constexpr int kFusedUnits = 4 * NW * 16;  // blocks of 32 that 4 passes of the workgroup quantise
+
+template <int FS, int TT, int NW, int U, bool GATED, bool HALVES, bool FUSED>
+__global__ void __launch_bounds__(NW * 64)
+    fp4_few_kernel(Fp4Shape s, const uint8_t* __restrict__ prepared, const uint8_t* __restrict__ packed,
+                   const uint8_t* __restrict__ pscales, const uint16_t* __restrict__ x, int M,
+                   uint16_t* __restrict__ out) {
+  static_assert(!GATED || (HALVES ? FS == 1 : FS % 2 == 0), "whole gate and up pairs");
+  static_assert(!FUSED || TT == 1, "few tokens");
+  __shared__ f32x4_t part[NW][FS * TT][64];
+  __shared__ uint4 qcodes[FUSED ? kFusedUnits<NW> : 1];
+  __shared__ uint8_t qscale[FUSED ? kFusedUnits<NW> : 4];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int ks = s.ksteps(), kb = s.kblocks(), ns = s.subtiles(), units = 4 * kb;
+  const int sub0 = blockIdx.x * FS;
+  const int64_t groups = (M + 15) / 16, tok0 = (int64_t)blockIdx.y * (16 * TT);
+  const int r = lane & 15, g = lane >> 4;
+  // HALVES: the half blockIdx.x % 2 of both subtiles of pair blockIdx.x / 2
+  const int hsub = (blockIdx.x & ~1u) + (r >> 3);
+  const int hlane = 16 * g + (blockIdx.x & 1) * 8 + (r & 7);
+  const int64_t wpairs = Fp4Shape::pair_cols(ns), xpairs = Fp4Shape::pair_cols(groups);
+  const uint32_t* const ws = (const uint32_t*)(prepared + s.codes_bytes(ns));
+  const int per = (ks + NW - 1) / NW, s0 = wave * per, s1 = min(ks, s0 + per);
+
+  struct Operands {
+    i32x4_t a[U][FS][2], b[U][TT][2];
+    uint32_t sa[U][FS], sb[U][TT];  // scales of both halves in bytes 0 and 1
+  };
+  auto load = [&](int at, Operands& o) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      // steps past the run are loaded again, and not multiplied
+      const int su = min(at + u, ks - 1);
+#pragma unroll
+      for (int f = 0; f < FS; ++f) {
+        const int64_t sub = HALVES ? hsub : min(sub0 + f, ns - 1);
+        const int l = HALVES ? hlane : lane;
+        const uint8_t* const p = prepared + (sub * kb + 2 * su) * 1024 + l * 16;
+        o.a[u][f][0] = *(const i32x4_t*)p;
+        o.a[u][f][1] = *(const i32x4_t*)(p + 1024);
+        o.sa[u][f] = ws[(su * wpairs + (sub >> 1)) * 64 + l] >> (16 * (sub & 1));
+      }
+      if constexpr (!FUSED)
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          const int64_t group = min(tok0 / 16 + t, groups - 1);
+          const uint8_t* const p = packed + (group * kb + 2 * su) * 1024 + lane * 16;
+          o.b[u][t][0] = *(const i32x4_t*)p;
+          o.b[u][t][1] = *(const i32x4_t*)(p + 1024);
+          o.sb[u][t] = ((const uint32_t*)pscales)[(su * xpairs + (group >> 1)) * 64 + lane] >> (16 * (group & 1));
+        }
+    }
+  };
+  f32x4_t acc[FS][TT];
+#pragma unroll
+  for (int f = 0; f < FS; ++f)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) acc[f][t] = f32x4_t{};
+  auto multiply = [&](int at, Operands& o) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (at + u >= s1) break;  // uniform
+      if constexpr (FUSED) {
+        const int unit = min(r, M - 1) * units + min(at + u, ks - 1) * 8 + g;
+        o.b[u][0][0] = *(const i32x4_t*)(qcodes + unit);
+        o.b[u][0][1] = *(const i32x4_t*)(qcodes + unit + 4);
+        o.sb[u][0] = qscale[unit] | (uint32_t)qscale[unit + 4] << 8;
+      }
+#pragma unroll
+      for (int f = 0; f < FS; ++f)
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          acc[f][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(o.a[u][f][0]), wide(o.b[u][t][0]), acc[f][t],
+                                                                       4, 4, 0, (int)o.sa[u][f], 0, (int)o.sb[u][t]);
+          acc[f][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(o.a[u][f][1]), wide(o.b[u][t][1]), acc[f][t],
+                                                                       4, 4, 1, (int)o.sa[u][f], 1, (int)o.sb[u][t]);
+        }
+    }
+  };
+
+  Operands o;
+  if constexpr (FUSED) {
+    // 4 lanes per block of 32; block `unit` of all tokens is K block unit % units
+    // of token unit / units
+    const int all = M * units;
+    uint4 raw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int unit = (i * NW * 64 + (int)threadIdx.x) / 4, row = unit / units;
+      const int c = (unit - row * units) * 32 + (lane & 3) * 8;
+      raw[i] = make_uint4(0, 0, 0, 0);
+      if (unit < all && c < s.K) raw[i] = *(const uint4*)(x + (int64_t)row * s.K + c);
+    }
+    __builtin_amdgcn_sched_barrier(0);  // x first: it is needed first
+    load(s0, o);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int unit = (i * NW * 64 + (int)threadIdx.x) / 4;
+      uint32_t m = amax8(raw[i]);
+      m = max(m, (uint32_t)__shfl_xor((int)m, 1));
+      m = max(m, (uint32_t)__shfl_xor((int)m, 2));
+      const uint32_t byte = mxfp4_scale_byte(m), code = mxfp4_codes8(raw[i], byte);
+      if (unit < all) {
+        ((uint32_t*)qcodes)[unit * 4 + (lane & 3)] = code;
+        if ((lane & 3) == 0) qscale[unit] = (uint8_t)byte;
+      }
+    }
+    __syncthreads();
+  } else {
+    load(s0, o);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  multiply(s0, o);
+#pragma unroll 1
+  for (int b = s0 + U; b < s1; b += U) {
+    load(b, o);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(b, o);
+  }
+#pragma unroll
+  for (int f = 0; f < FS; ++f)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) part[wave][f * TT + t][lane] = acc[f][t];
+  __syncthreads();
+  // output tiles of 16 features x 16 tokens, dealt to the waves
+  constexpr int kTiles = (GATED && !HALVES ? FS / 2 : FS) * TT;
+  for (int i = wave; i < kTiles; i += NW) {
+    const int f = i / TT, t = i % TT;
+    f32x4_t v{}, w{};
+#pragma unroll
+    for (int j = 0; j < NW; ++j) {
+      v += part[j][(GATED && !HALVES ? 2 * f : f) * TT + t][lane];
+      if (HALVES) w += part[j][t][lane ^ 32];
+      if (GATED && !HALVES) w += part[j][(2 * f + 1) * TT + t][lane];
+    }
+    const int n = HALVES ? blockIdx.x * 8 + 4 * g : (GATED ? sub0 / 2 + f : sub0 + f) * 16 + 4 * g;
+    const int64_t m = tok0 + 16 * t + r;
+    if ((HALVES && g >= 2) || n >= s.N || m >= M) continue;  // N % 8 == 0: the lane's four outputs are all in or all out
+    if (s.has_act)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = gated_act(s.act, v[e], w[e]);
+    *(uint2*)(out + m * s.N + n) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+  }
+}
+
+// ---- many tokens
+
+// Rows in operand order: a slot holds ROWS / 16 subtiles x 2 halves x 1 KiB.
+// Subtiles past the last are the last again.
+template <int ROWS>
+struct PackSource {
+  static constexpr int kCopies = ROWS / 32;
+  const uint8_t* base;
+  uint32_t off[kCopies];
+  uint32_t at;
+  __device__ void init(const uint8_t* p, int kb, int64_t sub0, int64_t subs, int first, int wave, int lane) {
+    base = p + sub0 * kb * 1024;
+    const int64_t last = subs - 1 - sub0;
+#pragma unroll
+    for (int c = 0; c < kCopies; ++c)
+      off[c] = (uint32_t)min((int64_t)(c * 2 + wave / 2), last) * (uint32_t)(kb * 1024) + (wave & 1) * 1024 + lane * 16;
+    at = (uint32_t)first * 128 + lane * 16;
+  }
+  template <bool TAIL>
+  __device__ __forceinline__ void copy(int step, int c, uint32_t lds) const {
+    dma16_at(base + (int64_t)step * 2048, off[c], lds + c * 4096);
+  }
+  __device__ __forceinline__ i32x4_t read(const uint8_t* area, int half, int f) const {
+    return *(const i32x4_t*)(area + at + half * 1024 + f * 2048);
+  }
+};
+
+// The scaled instruction and its scales, which come with each step: a dword per
+// lane and pair of fragments, the tokens' BM / 32 and then the weights' BN / 32.
+template <class T>
+struct Fp4Op {
+  static constexpr int kPairs = (T::BM + T::BN) / 32;
+  static constexpr bool kWide = T::BM == 256 && T::BN == 256;  // 4 pairs, 1 KiB, a wave: one copy
+  static constexpr int kCopies = kWide ? 1 : kPairs / 4;
+  static constexpr int kRing = kPairs * 256;
+  static_assert(T::FM % 2 == 0 && T::FN % 2 == 0 && kPairs % 4 == 0, "whole pairs");
+  const uint8_t* src[kCopies];
+  int64_t stride[kCopies];
+  uint32_t lds, lane_off;
+  const uint8_t* mine;  // this lane's dword of the wave's first token pair
+  int npairs;           // from there to its first weight pair, bytes
+  struct Scales {
+    uint32_t m[T::FM / 2], n[T::FN / 2];
+  };
+  __device__ void init(uint8_t* ring, const uint8_t* xs, int64_t xpairs, int64_t xpair0, const uint8_t* ws,
+                       int64_t wpairs, int64_t wpair0, int wm, int wn, int wave, int lane) {
+    lane_off = lane * (kWide ? 16 : 4);
+#pragma unroll
+    for (int c = 0; c < kCopies; ++c) {
+      const int pair = kWide ? wave * 4 : wave * kCopies + c;
+      const bool tokens = pair < T::BM / 32;
+      stride[c] = (tokens ? xpairs : wpairs) * 256;
+      src[c] = tokens ? xs + (xpair0 + pair) * 256 : ws + (wpair0 + pair - T::BM / 32) * 256;
+    }
+    lds = lds_addr(ring) + wave * kCopies * (kWide ? 1024 : 256);
+    mine = ring + wm * (T::FM / 2) * 256 + lane * 4;
+    npairs = (T::BM / 32 + wn * (T::FN / 2) - wm * (T::FM / 2)) * 256;
+  }
+  __device__ __forceinline__ void copy(int step, int c) const {
+    const uint32_t to = lds + (step & 1) * kRing + c * 256;
+    if (kWide)
+      dma16_at(src[c] + step * stride[c], lane_off, to);
+    else
+      dma4_at(src[c] + step * stride[c], lane_off, to);
+  }
+  __device__ __forceinline__ void read(int step, Scales& s) const {
+    const uint8_t* const p = mine + (step & 1) * kRing;
+#pragma unroll
+    for (int i = 0; i < T::FM / 2; ++i) s.m[i] = *(const uint32_t*)(p + i * 256);
+#pragma unroll
+    for (int i = 0; i < T::FN / 2; ++i) s.n[i] = *(const uint32_t*)(p + npairs + i * 256);
+  }
+  template <int HALF, int F, int M>
+  __device__ __forceinline__ f32x4_t mul(const i32x4_t& a, const i32x4_t& b, const f32x4_t& c, const Scales& s) const {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(a), wide(b), c, 4, 4, 2 * (F & 1) + HALF,
+                                                            (int)s.n[F / 2], 2 * (M & 1) + HALF, (int)s.m[M / 2]);
+  }
+};
+
+template <class T>
+constexpr int kFp4Lds = 2 * T::kSlot + 2 * Fp4Op<T>::kRing;
+
+template <class T, bool GATED>
+__global__ void __launch_bounds__(256, 1)
+    fp4_tile_kernel(Fp4Shape s, const uint8_t* __restrict__ prepared, const uint8_t* __restrict__ packed,
+                    const uint8_t* __restrict__ pscales, int M, int tiles_m, int tiles_n, uint16_t* __restrict__ out) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // Workgroups are dealt to the 8 XCDs in turn: give each XCD a contiguous
+  // range of tiles, in bands of 4 token tiles, so that what runs together on
+  // it shares token and weight tiles in its L2.
+  const int per = gridDim.x / 8;
+  const int logical = (blockIdx.x % 8) * per + blockIdx.x / 8;
+  if (logical >= tiles_m * tiles_n) return;
+  const int band = logical / (4 * tiles_n), in_band = logical - band * 4 * tiles_n;
+  const int bm = min(4, tiles_m - 4 * band);
+  const int tn = in_band / bm, tm = 4 * band + in_band % bm;
+  const int wm = wave % T::WM, wn = wave / T::WM;
+  const int kb = s.kblocks(), ns = s.subtiles();
+  const int64_t groups = (M + 15) / 16;
+  PackSource<T::BM> p;
+  PackSource<T::BN> q;
+  Fp4Op<T> op;
+  p.init(packed, kb, (int64_t)tm * (T::BM / 16), groups, wm * T::FM * 16, wave, lane);
+  q.init(prepared, kb, (int64_t)tn * (T::BN / 16), ns, wn * T::FN * 16, wave, lane);
+  op.init(smem + 2 * T::kSlot, pscales, Fp4Shape::pair_cols(groups), (int64_t)tm * (T::BM / 32),
+          prepared + s.codes_bytes(ns), Fp4Shape::pair_cols(ns), (int64_t)tn * (T::BN / 32), wm, wn, wave, lane);
+  f32x4_t acc[T::FN][T::FM];
+#pragma unroll
+  for (int f = 0; f < T::FN; ++f)
+#pragma unroll
+    for (int t = 0; t < T::FM; ++t) acc[f][t] = f32x4_t{};
+  tile_loop<T>(s.ksteps(), false, p, q, op, smem, wave, acc);
+  __syncthreads();
+  const int64_t m1 = (int64_t)tm * T::BM + wm * T::FM * 16;
+  const int n1 = (tn * T::BN + wn * T::FN * 16) / (GATED ? 2 : 1);
+  auto put = [&](auto kind) __attribute__((always_inline)) {
+    store_rows<T, GATED>(smem, wave, lane, out + m1 * s.N + n1, s.N, M - m1, s.N - n1,
+                         [&](int f, int t, int i) __attribute__((always_inline)) {
+                           constexpr int kKind = decltype(kind)::value;
+                           if constexpr (kKind < 0)
+                             return acc[f][t][i];
+                           else
+                             return act_of<kKind>(s.act, acc[f][t][i], GATED ? acc[f + (GATED ? 1 : 0)][t][i] : 0.0f);
+                         });
+  };
+  if constexpr (GATED) {
+    if (s.act.kind == kActGeluTanh) put(std::integral_constant<int, kActGeluTanh>{});
+    else if (s.act.kind == kActSwigluOai) put(std::integral_constant<int, kActSwigluOai>{});
+    else put(std::integral_constant<int, kActSilu>{});
+  } else {
+    if (s.has_act) put(std::integral_constant<int, kActRelu2>{});
+    else put(std::integral_constant<int, -1>{});
+  }
+}
+
+// ---- launches
+
+struct Tokens {
+  const uint8_t* packed;
+  const uint8_t* scales;
+  const uint16_t* x;
+};
+
+template <class T>
+hipError_t launch_tile(const Fp4Shape& s, const uint8_t* prepared, const Tokens& x, int M, uint16_t* out,
+                       hipStream_t st) {
+  const int tm = (M + T::BM - 1) / T::BM, tn = (s.subtiles() + T::BN / 16 - 1) / (T::BN / 16);
+  const dim3 grid(grid8((int64_t)tm * tn));
+  if (s.gated)
+    hipLaunchKernelGGL((fp4_tile_kernel<T, true>), grid, dim3(256), kFp4Lds<T>, st, s, prepared, x.packed, x.scales, M,
+                       tm, tn, out);
+  else
+    hipLaunchKernelGGL((fp4_tile_kernel<T, false>), grid, dim3(256), kFp4Lds<T>, st, s, prepared, x.packed, x.scales, M,
+                       tm, tn, out);
+  return hipGetLastError();
+}
+
+template <int FS, int TT, int NW, int U, bool FUSED>
+hipError_t launch_few(const Fp4Shape& s, const uint8_t* prepared, const Tokens& x, int M, uint16_t* out,
+                      hipStream_t st) {
+  constexpr bool kHalves = FS == 1;
+  const dim3 grid((unsigned)((s.subtiles() + FS - 1) / FS), (unsigned)((M + 16 * TT - 1) / (16 * TT)));
+  if (s.gated)
+    hipLaunchKernelGGL((fp4_few_kernel<FS, TT, NW, U, true, kHalves, FUSED>), grid, dim3(NW * 64), 0, st, s, prepared,
+                       x.packed, x.scales, x.x, M, out);
+  else
+    hipLaunchKernelGGL((fp4_few_kernel<FS, TT, NW, U, false, false, FUSED>), grid, dim3(NW * 64), 0, st, s, prepared,
+                       x.packed, x.scales, x.x, M, out);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t fp4_workspace(const Fp4Shape& s, int64_t max_tokens) {
+  const int64_t groups = max_tokens < 1 ? 1 : (max_tokens + 15) / 16;
+  return align256(s.codes_bytes(groups) + s.scales_bytes(groups));
+}
+
+hipError_t launch_fp4_prepare(const Fp4Shape& s, const uint8_t* codes, const uint8_t* scales, uint8_t* prepared,
+                              hipStream_t st) {
+  const int64_t ns = s.subtiles(), subs = Fp4Shape::padded(ns);
+  const int64_t blocks = (subs * s.kblocks() * 64 + 255) / 256;
+  hipLaunchKernelGGL(fp4_pack_kernel, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, st,
+                     RowMap{s.N, s.gated}, s.K, subs, s.ksteps(), Fp4Shape::pair_cols(ns), codes, scales, prepared,
+                     (uint32_t*)(prepared + s.codes_bytes(ns)));
+  return hipGetLastError();
+}
+
+hipError_t launch_fp4_linear(const Fp4Shape& s, const uint8_t* prepared, const uint16_t* x, const uint8_t* xcodes,
+                             const uint8_t* xscales, int M, uint16_t* out, uint8_t* ws, hipStream_t st) {
+  const int64_t groups = (M + 15) / 16, pairs = Fp4Shape::pair_cols(groups);
+  uint8_t* const packed = ws;
+  uint8_t* const pscales = ws + s.codes_bytes(groups);
+  const Tokens t{packed, pscales, x};
+  const int ks = s.ksteps();
+#define MOE_FEW(...) launch_few<__VA_ARGS__>(s, prepared, t, M, out, st)
+  if (x && M <= 4 && M * ks * 8 <= kFusedUnits<16>) {
+    if (M * ks * 8 <= kFusedUnits<8>) return ks > 8 ? MOE_FEW(1, 1, 8, 4, true) : MOE_FEW(1, 1, 8, 1, true);
+    return s.gated ? MOE_FEW(2, 1, 16, 2, true) : MOE_FEW(1, 1, 16, 2, true);
+  }
+  if (x) {
+    hipLaunchKernelGGL(fp4_tokens_kernel, dim3((unsigned)groups, (unsigned)((s.K + 511) / 512)), dim3(256), 0, st, x, M, s.K,
+                       ks, pairs, packed, pscales);
+  } else {
+    const int64_t blocks = (groups * s.kblocks() * 64 + 255) / 256;
+    hipLaunchKernelGGL(fp4_pack_kernel, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, st,
+                       RowMap{M, false}, s.K, groups, ks, pairs, xcodes, xscales, packed, (uint32_t*)pscales);
+  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (M <= 16) return ks > 8 ? MOE_FEW(1, 1, 16, 1, false) : MOE_FEW(1, 1, 4, 1, false);
+  if (M <= 32) return MOE_FEW(2, 2, 8, 1, false);
+  const int64_t wide = (M + 63) / 64;
+  if (wide * ((s.subtiles() + 1) / 2) <= 256) return MOE_FEW(2, 4, 8, 1, false);
+  if (wide * ((s.subtiles() + 3) / 4) <= 512) return MOE_FEW(4, 4, 8, 1, false);
+#undef MOE_FEW
+  auto rounds = [&](int bm, int bn) {
+    return ((M + bm - 1) / bm * (int64_t)((s.subtiles() * 16 + bn - 1) / bn) + 255) / 256;
+  };
+  if (20 * rounds(256, 256) <= 10 * rounds(128, 128)) return launch_tile<Tile<256, 256, 2, 2>>(s, prepared, t, M, out, st);
+  return launch_tile<Tile<128, 128, 2, 2>>(s, prepared, t, M, out, st);
+}
+
+}  // namespace moe

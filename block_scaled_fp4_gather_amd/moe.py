@@ -297,6 +297,22 @@ class Fp4MoE:
             self.workspace = torch.empty(workspace_bytes(desc, desc.max_tokens), dtype=torch.uint8, device=dev)
             made += self.prepared, self.workspace
 
+    @classmethod
+    def from_float(cls, desc: Desc, w13, w2, device="cuda", stream=None):
+        """The layer of bf16 or fp32 experts, w13 [E][2 I][H] (relu2: [E][I][H]) and
+        w2 [E][H][I], quantised on the GPU (experts.fp4_quantize); NVFP4 with a
+        global scale per expert and matrix."""
+        from . import experts
+
+        if stream is not None:
+            stream = as_stream(stream, w13.device)
+            for t in (w13, w2):
+                t.record_stream(stream)
+            with torch.cuda.stream(stream):
+                return cls.from_float(desc, w13, w2, device)
+        q13, q2 = (experts.fp4_quantize(t.to(device).contiguous(), desc.fmt) for t in (w13, w2))
+        return cls(desc, q13.codes, q13.scales, q2.codes, q2.scales, q13.global_scale, q2.global_scale, device)
+
     def __call__(self, x, ids, w, out=None, stream=None, tuning=None, phases=None):
         if out is None:
             out = torch.empty_like(x)

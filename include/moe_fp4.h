@@ -476,6 +476,153 @@ moe_fp4_status moe_fp4_block_norm(const moe_fp4_norm_desc* desc, int32_t M, cons
                                   const uint16_t* y2, const void* gate, const void* post_weight,
                                   const void* pre_weight, void* h_out, uint16_t* x_out, void* stream);
 
+/* ------------------------------------------------------------------------
+ * From 16- and 32-bit experts to FP4 ones, and beside them: the quantisation
+ * that makes the layer's weights, a linear map on FP4 activations, and the
+ * parts of a layer whose experts are bf16, with their gradients (the routes'
+ * grouping, products grouped by expert, the weighted join).  The conventions
+ * above hold; outputs may not overlap anything that is read nor each other. */
+
+/* FP4 quantisation of x [experts][rows][cols] (bf16 or fp32, a moe_fp4_type;
+ * device, 16-byte aligned; rows `row_stride` values apart, a multiple of 8 (bf16)
+ * or 4 (fp32) and cols at least, experts rows * row_stride) into codes
+ * [experts][rows][cols / 2], the element of even index in the low nibble, and a
+ * scale byte per block of G values along cols, [experts][rows][cols / G]: the
+ * logical layout of moe_fp4_prepare.  cols: a multiple of G, at most 2^20.
+ *   MXFP4 (G = 32): scale s = 2^(floor(log2(max |x|)) - 2) over the block, at
+ *     least 2^-127 (OCP MX); code = x / s rounded to nearest-even E2M1, at most 6.
+ *   NVFP4 (G = 16): s = max |x| / (6 g) rounded to nearest-even E4M3, at most 448;
+ *     code = x / (s g) rounded to nearest-even E2M1, at most 6 (0 where s is 0);
+ *     both roundings are those of the exact quotient.  g is the expert's global
+ *     scale: global_scale [experts] where given (not negative, finite: a 0 makes
+ *     codes and scales 0, anything else NaN scales), else the largest finite |x|
+ *     of the expert over 2688 (= 6 * 448) in fp32, written to global_out
+ *     [experts].  Exactly one of the two is given; MXFP4 takes neither.
+ * A block that holds a NaN or an infinity gets the scale NaN (byte 255, E4M3
+ * 0x7F) and codes 7.  The workspace is needed where global_out is
+ * (moe_fp4_quantize_workspace_bytes; 0 otherwise and for MXFP4).  experts or
+ * rows may be 0 (nothing is launched). */
+moe_fp4_status moe_fp4_quantize_workspace_bytes(int32_t format, int64_t experts, size_t* bytes);
+moe_fp4_status moe_fp4_quantize(int32_t format, int32_t type, const void* x, int64_t experts, int64_t rows,
+                                int32_t cols, int64_t row_stride, uint8_t* codes, uint8_t* scales,
+                                const float* global_scale, float* global_out, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/* The values of codes and scales as moe_fp4_quantize lays them out: code *
+ * scale in fp32, NVFP4 times global_scale [experts], rounded once more to bf16
+ * where `type` says so.  out [experts][rows][cols], codes and out 16-byte aligned. */
+moe_fp4_status moe_fp4_dequantize(int32_t format, int32_t type, const uint8_t* codes, const uint8_t* scales,
+                                  const float* global_scale, int64_t experts, int64_t rows, int32_t cols, void* out,
+                                  void* stream);
+
+/* Linear map with MXFP4 weights and MXFP4 activations:
+ *     y[n] = sum_k q(x)[k] * W[n][k]
+ * where q(x) is x as moe_fp4_quantize gives it, on the matrix instruction's
+ * form for two FP4 operands, with fp32 sums (a sum below 2^-126 may count as
+ * zero).  An activation where asked for
+ * (the gated ones over gate and up rows), one rounding to bf16.  A block of x
+ * that holds a NaN or an infinity makes its token's outputs NaN; other tokens
+ * are not touched. */
+typedef struct {
+  int32_t in_features;  /* K, a multiple of 32, at most 2^20 */
+  int32_t out_features; /* N, a multiple of 8, at most 2^26; K * N at most 2^31 */
+  int32_t max_tokens;   /* capacity for workspace sizing, at most 2^20 */
+  int32_t act_fn;       /* MOE_FP4_FN_NONE or a moe_fp4_act_fn */
+  float act_alpha;      /* SWIGLUOAI only, else ignored */
+  float act_beta;
+  float act_limit;
+} moe_fp4_linear_desc;
+
+/* Bytes of the prepared weights, and the preparation, once per map: a
+ * permutation of the bytes into `prepared` (device, 256-byte aligned).  codes
+ * [N][K / 2] (device, 16-byte aligned), scales [N][K / 32]; for a gated
+ * activation both hold the gate's rows and then the up's. */
+moe_fp4_status moe_fp4_linear_prepared_bytes(const moe_fp4_linear_desc* desc, size_t* bytes);
+moe_fp4_status moe_fp4_linear_prepare(const moe_fp4_linear_desc* desc, const uint8_t* codes, const uint8_t* scales,
+                                      void* prepared, size_t prepared_bytes, void* stream);
+
+/* Workspace bytes for calls on `desc` (device, 256-byte aligned), enough for
+ * every M <= max_tokens; M is checked against max_tokens. */
+moe_fp4_status moe_fp4_linear_workspace_bytes(const moe_fp4_linear_desc* desc, int32_t M, size_t* bytes);
+
+/* The map on M tokens, x bf16 [M][K], or on tokens that are quantised already
+ * (codes [M][K / 2], scales [M][K / 32]); out: bf16 [M][N], overwritten.  x,
+ * codes and out are 16-byte aligned.  Neither out nor the workspace may overlap
+ * each other or what is read.  M may be 0 (nothing is launched). */
+moe_fp4_status moe_fp4_linear(const moe_fp4_linear_desc* desc, const void* prepared, const uint16_t* x, int32_t M,
+                              uint16_t* out, void* workspace, size_t workspace_bytes, void* stream);
+moe_fp4_status moe_fp4_linear_quantized(const moe_fp4_linear_desc* desc, const void* prepared, const uint8_t* codes,
+                                        const uint8_t* scales, int32_t M, uint16_t* out, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
+/* Groups the routes topk_ids [tokens][top_k] by expert, in route order: expert
+ * e's routes get the rows offsets[e] .. offsets[e + 1] - 1 (offsets int32 [E +
+ * 1]); order int32 [tokens * top_k] holds each row's route t * top_k + j and
+ * place int32 [tokens][top_k] each route's row.  A route whose id is negative or
+ * >= E gets the place -1, and the rows from offsets[E] on the order -1.  E at
+ * most 4096, tokens * top_k at most 2^22 (else MOE_FP4_EUNSUPPORTED).  Ids are
+ * aligned to their size; tokens may be 0 (offsets are written). */
+moe_fp4_status moe_fp4_group_routes_workspace_bytes(int32_t tokens, int32_t top_k, int32_t num_experts,
+                                                    size_t* bytes);
+moe_fp4_status moe_fp4_group_routes(const int32_t* topk_ids, int32_t tokens, int32_t top_k, int32_t num_experts,
+                                    int32_t* offsets, int32_t* order, int32_t* place, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+moe_fp4_status moe_fp4_group_routes_i64(const int64_t* topk_ids, int32_t tokens, int32_t top_k, int32_t num_experts,
+                                        int32_t* offsets, int32_t* order, int32_t* place, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
+/* Rows in grouped order: out[p] = x[order[p] / top_k], zeros where order[p] is
+ * negative.  x bf16 [tokens][hidden], out bf16 [tokens * top_k][hidden]; hidden
+ * a multiple of 8, at most 2^15.  order and place (below) are what
+ * moe_fp4_group_routes wrote; entries outside their range are not valid. */
+moe_fp4_status moe_fp4_gather_routes(const uint16_t* x, const int32_t* order, int32_t tokens, int32_t top_k,
+                                     int32_t hidden, uint16_t* out, void* stream);
+
+/* The weighted join: out[t] = bf16(sum over j with place[t][j] >= 0, in the
+ * order of j, of w[t][j] * y[place[t][j]]) in fp32; w fp32 [tokens][top_k], NULL
+ * for ones (which makes it the gradient of moe_fp4_gather_routes).  y bf16
+ * [tokens * top_k][hidden], out bf16 [tokens][hidden]. */
+moe_fp4_status moe_fp4_combine_routes(const uint16_t* y, const int32_t* place, const float* w, int32_t tokens,
+                                      int32_t top_k, int32_t hidden, uint16_t* out, void* stream);
+
+/* Its gradients: dy[place[t][j]] = bf16(w[t][j] * dout[t]), zeros in the rows of
+ * no route; dw[t][j] = sum_h dout[t][h] * y[place[t][j]][h] in fp32, 0 where
+ * place is negative. */
+moe_fp4_status moe_fp4_combine_routes_grad(const uint16_t* dout, const uint16_t* y, const int32_t* place,
+                                           const int32_t* order, const float* w, int32_t tokens, int32_t top_k,
+                                           int32_t hidden, uint16_t* dy, float* dw, void* stream);
+
+/* Layout of a grouped weight: [E][out][in], or [E][in][out]. */
+typedef enum {
+  MOE_FP4_WEIGHT_OUT_IN = 0,
+  MOE_FP4_WEIGHT_IN_OUT = 1
+} moe_fp4_weight_layout;
+
+/* Products grouped by expert over ragged rows, bf16 with fp32 sums.  Rows
+ * offsets[e] .. offsets[e + 1] - 1 (offsets int32 [E + 1], device) belong to
+ * expert e.  Offsets do not decrease and lie in [0, rows]; others give wrong
+ * rows but no access out of range.  Rows of no expert (before offsets[0], from
+ * offsets[E] on) are set to zeros. */
+typedef struct {
+  int32_t num_experts;   /* E, at most 4096 */
+  int32_t in_features;   /* K, a multiple of 8, at most 2^20 */
+  int32_t out_features;  /* N, a multiple of 8, at most 2^20 */
+  int32_t weight_layout; /* moe_fp4_weight_layout */
+} moe_fp4_grouped_desc;
+
+/* y[t] = W[e(t)] x[t], rounded once to bf16.  x bf16 [rows][K], y bf16
+ * [rows][N], rows at most 2^22, all 16-byte aligned.  The gradient of x is the
+ * same call on dy with K and N swapped and the other weight layout. */
+moe_fp4_status moe_fp4_grouped_linear(const moe_fp4_grouped_desc* desc, const uint16_t* x, int32_t rows,
+                                      const uint16_t* weight, const int32_t* offsets, uint16_t* y, void* stream);
+
+/* dW[e] = sum over e's rows t of dy[t] x[t]^T, [E][N][K] (MOE_FP4_WEIGHT_OUT_IN
+ * only; for the other layout swap dy and x), bf16 or fp32 by `type`; zeros for
+ * an expert without rows. */
+moe_fp4_status moe_fp4_grouped_weight_grad(const moe_fp4_grouped_desc* desc, int32_t type, const uint16_t* dy,
+                                           const uint16_t* x, int32_t rows, const int32_t* offsets, void* dw,
+                                           void* stream);
+
 #ifdef __cplusplus
 }
 #endif
