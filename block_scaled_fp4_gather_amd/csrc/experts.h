@@ -71,11 +71,12 @@ hipError_t launch_combine_routes_grad(const uint16_t* dout, const uint16_t* y, c
 //   codes  [subtile][K block of 128][lane][16 B]: lane l holds row l % 16, K
 //          values 128 b + 32 (l / 16) .. + 31, the operand of
 //          v_mfma_scale_f32_16x16x128_f8f6f4 and one scale block
-//   scales [K step of 256][pair of subtiles][lane] dwords: byte 2 o + h the
-//          scale of subtile 2 pair + o, K block 2 step + h, in lane l that of
-//          the values whose codes lane l holds
+//   scales [K step of 256][pair of subtiles][lane] dwords: lane l has row
+//          l % 32 of the pair, its byte q the scale of the 32 values from
+//          256 step + 64 q + 32 (l / 32) on, the scale operands of v_mfma_scale_
+//          f32_32x32x64_f8f6f4 for a step
 // K is padded to whole steps and rows to whole pairs of subtiles with zero
-// codes and scale bytes of 2^-127; the scales' pairs to `pair_cols`, so that
+// codes and scale bytes; the scales' pairs to `pair_cols`, so that
 // a tile of 256 rows can copy its 8 pairs from any of its starts.
 struct Fp4Shape {
   int K, N;

@@ -50,12 +50,11 @@ __global__ void __launch_bounds__(256)
   for (int64_t it = me; it < ksteps * pairs * 64; it += step) {
     const int lane = (int)(it & 63);
     const int64_t sp = it >> 6, s = sp / pairs, pair = sp - s * pairs;
+    const int64_t row = map.row(2 * pair + ((lane >> 4) & 1), lane & 15);
     uint32_t v = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int64_t sub = 2 * pair + i / 2;
-      const int u = (int)(2 * s + i % 2) * 4 + (lane >> 4);
-      const int64_t row = map.row(sub, lane & 15);
+      const int u = (int)(8 * s) + 2 * i + (lane >> 5);
       if (row >= 0 && u < units) v |= (uint32_t)scales[row * units + u] << (8 * i);
     }
     pscales[it] = v;
@@ -97,11 +96,12 @@ __global__ void __launch_bounds__(256)
   __syncthreads();
   const int t = threadIdx.x, kb = 2 * ksteps;
   if (q * 4 + t / 64 < kb) ((uint4*)(packed + (group * kb + q * 4) * 1024))[t] = turned[t];
-  const int s = q * 2 + t / 64;
-  if (t < 128 && s < ksteps) {
-    const int r = lane & 15, u = (t / 64) * 8 + (lane >> 4);
-    *(uint16_t*)(pscales + ((s * pairs + group / 2) * 64 + lane) * 4 + (group & 1) * 2) =
-        (uint16_t)(bytes[r][u] | bytes[r][u + 4] << 8);
+  // dwords of 16 rows x 2 halves of a step's quarters
+  const int s = q * 2 + t / 32;
+  if (t < 64 && s < ksteps) {
+    const int r = t & 15, h = (t >> 4) & 1, u = (t / 32) * 8 + h;
+    *(uint32_t*)(pscales + ((s * pairs + group / 2) * 64 + 32 * h + 16 * (group & 1) + r) * 4) =
+        bytes[r][u] | bytes[r][u + 2] << 8 | bytes[r][u + 4] << 16 | (uint32_t)bytes[r][u + 6] << 24;
   }
 }
 
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(NW * 64)
 
   struct Operands {
     i32x4_t a[U][FS][2], b[U][TT][2];
-    uint32_t sa[U][FS], sb[U][TT];  // scales of both halves in bytes 0 and 1
+    uint32_t sa[U][FS], sb[U][TT];  // scales of the two K blocks in bytes 0 and 2
   };
   auto load = [&](int at, Operands& o) __attribute__((always_inline)) {
 #pragma unroll
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(NW * 64)
         const uint8_t* const p = prepared + (sub * kb + 2 * su) * 1024 + l * 16;
         o.a[u][f][0] = *(const i32x4_t*)p;
         o.a[u][f][1] = *(const i32x4_t*)(p + 1024);
-        o.sa[u][f] = ws[(su * wpairs + (sub >> 1)) * 64 + l] >> (16 * (sub & 1));
+        o.sa[u][f] = ws[(su * wpairs + (sub >> 1)) * 64 + 32 * (g & 1) + 16 * (int)(sub & 1) + (l & 15)] >> (8 * (g >> 1));
       }
       if constexpr (!FUSED)
 #pragma unroll
@@ -167,7 +167,8 @@ __global__ void __launch_bounds__(NW * 64)
           const uint8_t* const p = packed + (group * kb + 2 * su) * 1024 + lane * 16;
           o.b[u][t][0] = *(const i32x4_t*)p;
           o.b[u][t][1] = *(const i32x4_t*)(p + 1024);
-          o.sb[u][t] = ((const uint32_t*)pscales)[(su * xpairs + (group >> 1)) * 64 + lane] >> (16 * (group & 1));
+          o.sb[u][t] = ((const uint32_t*)pscales)[(su * xpairs + (group >> 1)) * 64 + 32 * (g & 1) + 16 * (int)(group & 1) + r] >>
+                       (8 * (g >> 1));
         }
     }
   };
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(NW * 64)
         const int unit = min(r, M - 1) * units + min(at + u, ks - 1) * 8 + g;
         o.b[u][0][0] = *(const i32x4_t*)(qcodes + unit);
         o.b[u][0][1] = *(const i32x4_t*)(qcodes + unit + 4);
-        o.sb[u][0] = qscale[unit] | (uint32_t)qscale[unit + 4] << 8;
+        o.sb[u][0] = qscale[unit] | (uint32_t)qscale[unit + 4] << 16;
       }
 #pragma unroll
       for (int f = 0; f < FS; ++f)
@@ -193,7 +194,7 @@ __global__ void __launch_bounds__(NW * 64)
           acc[f][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(o.a[u][f][0]), wide(o.b[u][t][0]), acc[f][t],
                                                                        4, 4, 0, (int)o.sa[u][f], 0, (int)o.sb[u][t]);
           acc[f][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(o.a[u][f][1]), wide(o.b[u][t][1]), acc[f][t],
-                                                                       4, 4, 1, (int)o.sa[u][f], 1, (int)o.sb[u][t]);
+                                                                       4, 4, 2, (int)o.sa[u][f], 2, (int)o.sb[u][t]);
         }
     }
   };
@@ -280,33 +281,34 @@ struct PackSource {
 #pragma unroll
     for (int c = 0; c < kCopies; ++c)
       off[c] = (uint32_t)min((int64_t)(c * 2 + wave / 2), last) * (uint32_t)(kb * 1024) + (wave & 1) * 1024 + lane * 16;
-    at = (uint32_t)first * 128 + lane * 16;
+    at = (uint32_t)first * 128 + ((lane >> 4) & 1) * 2048 + (lane >> 5) * 256 + (lane & 15) * 16;
   }
   template <bool TAIL>
   __device__ __forceinline__ void copy(int step, int c, uint32_t lds) const {
     dma16_at(base + (int64_t)step * 2048, off[c], lds + c * 4096);
   }
-  __device__ __forceinline__ i32x4_t read(const uint8_t* area, int half, int f) const {
-    return *(const i32x4_t*)(area + at + half * 1024 + f * 2048);
+  // 64 values of 32 rows: two of a K block's four lane groups, of two subtiles
+  __device__ __forceinline__ i32x4_t read(const uint8_t* area, int quarter, int f) const {
+    return *(const i32x4_t*)(area + at + quarter * 512 + f * 4096);
   }
 };
 
 // The scaled instruction and its scales, which come with each step: a dword per
-// lane and pair of fragments, the tokens' BM / 32 and then the weights' BN / 32.
+// lane and fragment, the tokens' BM / 32 and then the weights' BN / 32.
 template <class T>
 struct Fp4Op {
   static constexpr int kPairs = (T::BM + T::BN) / 32;
   static constexpr bool kWide = T::BM == 256 && T::BN == 256;  // 4 pairs, 1 KiB, a wave: one copy
   static constexpr int kCopies = kWide ? 1 : kPairs / 4;
   static constexpr int kRing = kPairs * 256;
-  static_assert(T::FM % 2 == 0 && T::FN % 2 == 0 && kPairs % 4 == 0, "whole pairs");
+  static_assert(kPairs % 4 == 0, "whole copies");
   const uint8_t* src[kCopies];
   int64_t stride[kCopies];
   uint32_t lds, lane_off;
   const uint8_t* mine;  // this lane's dword of the wave's first token pair
   int npairs;           // from there to its first weight pair, bytes
   struct Scales {
-    uint32_t m[T::FM / 2], n[T::FN / 2];
+    uint32_t m[T::FM], n[T::FN];
   };
   __device__ void init(uint8_t* ring, const uint8_t* xs, int64_t xpairs, int64_t xpair0, const uint8_t* ws,
                        int64_t wpairs, int64_t wpair0, int wm, int wn, int wave, int lane) {
@@ -319,8 +321,8 @@ struct Fp4Op {
       src[c] = tokens ? xs + (xpair0 + pair) * 256 : ws + (wpair0 + pair - T::BM / 32) * 256;
     }
     lds = lds_addr(ring) + wave * kCopies * (kWide ? 1024 : 256);
-    mine = ring + wm * (T::FM / 2) * 256 + lane * 4;
-    npairs = (T::BM / 32 + wn * (T::FN / 2) - wm * (T::FM / 2)) * 256;
+    mine = ring + wm * T::FM * 256 + lane * 4;
+    npairs = (T::BM / 32 + wn * T::FN - wm * T::FM) * 256;
   }
   __device__ __forceinline__ void copy(int step, int c) const {
     const uint32_t to = lds + (step & 1) * kRing + c * 256;
@@ -332,14 +334,14 @@ struct Fp4Op {
   __device__ __forceinline__ void read(int step, Scales& s) const {
     const uint8_t* const p = mine + (step & 1) * kRing;
 #pragma unroll
-    for (int i = 0; i < T::FM / 2; ++i) s.m[i] = *(const uint32_t*)(p + i * 256);
+    for (int i = 0; i < T::FM; ++i) s.m[i] = *(const uint32_t*)(p + i * 256);
 #pragma unroll
-    for (int i = 0; i < T::FN / 2; ++i) s.n[i] = *(const uint32_t*)(p + npairs + i * 256);
+    for (int i = 0; i < T::FN; ++i) s.n[i] = *(const uint32_t*)(p + npairs + i * 256);
   }
-  template <int HALF, int F, int M>
-  __device__ __forceinline__ f32x4_t mul(const i32x4_t& a, const i32x4_t& b, const f32x4_t& c, const Scales& s) const {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(a), wide(b), c, 4, 4, 2 * (F & 1) + HALF,
-                                                            (int)s.n[F / 2], 2 * (M & 1) + HALF, (int)s.m[M / 2]);
+  template <int QUARTER, int F, int M>
+  __device__ __forceinline__ f32x16_t mul(const i32x4_t& a, const i32x4_t& b, const f32x16_t& c, const Scales& s) const {
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wide(a), wide(b), c, 4, 4, QUARTER, (int)s.n[F], QUARTER,
+                                                           (int)s.m[M]);
   }
 };
 
@@ -367,19 +369,19 @@ __global__ void __launch_bounds__(256, 1)
   PackSource<T::BM> p;
   PackSource<T::BN> q;
   Fp4Op<T> op;
-  p.init(packed, kb, (int64_t)tm * (T::BM / 16), groups, wm * T::FM * 16, wave, lane);
-  q.init(prepared, kb, (int64_t)tn * (T::BN / 16), ns, wn * T::FN * 16, wave, lane);
+  p.init(packed, kb, (int64_t)tm * (T::BM / 16), groups, wm * T::FM * 32, wave, lane);
+  q.init(prepared, kb, (int64_t)tn * (T::BN / 16), ns, wn * T::FN * 32, wave, lane);
   op.init(smem + 2 * T::kSlot, pscales, Fp4Shape::pair_cols(groups), (int64_t)tm * (T::BM / 32),
           prepared + s.codes_bytes(ns), Fp4Shape::pair_cols(ns), (int64_t)tn * (T::BN / 32), wm, wn, wave, lane);
-  f32x4_t acc[T::FN][T::FM];
+  f32x16_t acc[T::FN][T::FM];
 #pragma unroll
   for (int f = 0; f < T::FN; ++f)
 #pragma unroll
-    for (int t = 0; t < T::FM; ++t) acc[f][t] = f32x4_t{};
+    for (int t = 0; t < T::FM; ++t) acc[f][t] = f32x16_t{};
   tile_loop<T>(s.ksteps(), false, p, q, op, smem, wave, acc);
   __syncthreads();
-  const int64_t m1 = (int64_t)tm * T::BM + wm * T::FM * 16;
-  const int n1 = (tn * T::BN + wn * T::FN * 16) / (GATED ? 2 : 1);
+  const int64_t m1 = (int64_t)tm * T::BM + wm * T::FM * 32;
+  const int n1 = (tn * T::BN + wn * T::FN * 32) / (GATED ? 2 : 1);
   auto put = [&](auto kind) __attribute__((always_inline)) {
     store_rows<T, GATED>(smem, wave, lane, out + m1 * s.N + n1, s.N, M - m1, s.N - n1,
                          [&](int f, int t, int i) __attribute__((always_inline)) {
@@ -387,7 +389,7 @@ __global__ void __launch_bounds__(256, 1)
                            if constexpr (kKind < 0)
                              return acc[f][t][i];
                            else
-                             return act_of<kKind>(s.act, acc[f][t][i], GATED ? acc[f + (GATED ? 1 : 0)][t][i] : 0.0f);
+                             return act_of<kKind>(s.act, acc[f][t][i], GATED ? acc[f][t][i + 8] : 0.0f);  // rows 16 on: up
                          });
   };
   if constexpr (GATED) {

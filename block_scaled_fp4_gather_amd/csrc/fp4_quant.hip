@@ -44,14 +44,22 @@ __device__ __forceinline__ float raw_value(const Raw<F32>& r, int i) {
   return __uint_as_float(i % 2 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
 }
 
-// Address of item `it` (8 values) of rows of c8 items.  Rows without gaps need
-// no division.
+// Rows of c8 items of 8 values, ld values apart.
+struct Rows {
+  int c8;
+  uint64_t inverse;  // 2^64 / c8, rounded up
+  int64_t gap;       // values between two rows
+};
+
+// Item `it`.  Rows without gaps need no division; that of the others is a
+// product, too large by one at most (it has fewer than 41 bits, c8 fewer than 18).
 template <bool F32, bool STRIDED>
-__device__ __forceinline__ Raw<F32> load_raw(const void* x, int64_t it, int c8, int64_t ld) {
+__device__ __forceinline__ Raw<F32> load_raw(const void* x, int64_t it, const Rows& rows) {
   int64_t at = it * 8;
   if (STRIDED) {
-    const int64_t row = it / c8;
-    at = row * ld + (it - row * c8) * 8;
+    int64_t row = (int64_t)__umul64hi((uint64_t)it, rows.inverse);
+    row -= row * rows.c8 > it;
+    at += row * rows.gap;
   }
   Raw<F32> r;
   const uint4* const p = (const uint4*)((const uint8_t*)x + at * (F32 ? 4 : 2));
@@ -174,8 +182,7 @@ __device__ __forceinline__ uint32_t nvfp4_codes(const Raw<F32>& r, uint32_t byte
 }
 
 template <bool NV, bool F32, bool STRIDED>
-__global__ void __launch_bounds__(256) fp4_quantize_kernel(QuantArgs a, int64_t items, int parts) {
-  const int c8 = a.K / 8;
+__global__ void __launch_bounds__(256) fp4_quantize_kernel(QuantArgs a, Rows rows, int64_t items, int parts) {
   const int64_t step = (int64_t)gridDim.x * 256;
   for (int64_t e = blockIdx.y; e < a.experts; e += gridDim.y) {
     const uint8_t* const x = (const uint8_t*)a.x + e * a.rows * a.ld * (F32 ? 4 : 2);
@@ -205,7 +212,7 @@ __global__ void __launch_bounds__(256) fp4_quantize_kernel(QuantArgs a, int64_t 
       Raw<F32> r[kU];
 #pragma unroll
       for (int u = 0; u < kU; ++u)
-        if (it0 + u * step < items) r[u] = load_raw<F32, STRIDED>(x, it0 + u * step, c8, a.ld);
+        if (it0 + u * step < items) r[u] = load_raw<F32, STRIDED>(x, it0 + u * step, rows);
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         const int64_t it = it0 + u * step;
@@ -232,9 +239,8 @@ __global__ void __launch_bounds__(256) fp4_quantize_kernel(QuantArgs a, int64_t 
 
 // The largest finite magnitude of each expert, a part per workgroup.
 template <bool F32, bool STRIDED>
-__global__ void __launch_bounds__(256) fp4_amax_kernel(QuantArgs a, int64_t items) {
+__global__ void __launch_bounds__(256) fp4_amax_kernel(QuantArgs a, Rows rows, int64_t items) {
   __shared__ uint32_t wmax[4];
-  const int c8 = a.K / 8;
   const int64_t step = (int64_t)gridDim.x * 256;
   for (int64_t e = blockIdx.y; e < a.experts; e += gridDim.y) {
     const uint8_t* const x = (const uint8_t*)a.x + e * a.rows * a.ld * (F32 ? 4 : 2);
@@ -242,7 +248,7 @@ __global__ void __launch_bounds__(256) fp4_amax_kernel(QuantArgs a, int64_t item
     for (int64_t it0 = (int64_t)blockIdx.x * 256 + threadIdx.x; it0 < items; it0 += kU * step) {
       Raw<F32> r[kU];
 #pragma unroll
-      for (int u = 0; u < kU; ++u) r[u] = load_raw<F32, STRIDED>(x, min(it0 + u * step, items - 1), c8, a.ld);
+      for (int u = 0; u < kU; ++u) r[u] = load_raw<F32, STRIDED>(x, min(it0 + u * step, items - 1), rows);
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         const uint32_t all = raw_amax(r[u]);
@@ -333,23 +339,25 @@ hipError_t quantize(QuantArgs a, hipStream_t st) {
     a.experts = 1;
   }
   const int64_t items = a.rows * (a.K / 8);
+  // K / 8 is 2 or more
+  const Rows rows{a.K / 8, UINT64_MAX / (uint64_t)(a.K / 8) + 1, a.ld - a.K};
   int parts = 0;
   if (NV && a.partial) {
     dim3 grid = grid_for(items, a.experts, 2048);
     if (grid.x > kQuantParts) grid.x = kQuantParts;
     parts = (int)grid.x;
     if (strided)
-      hipLaunchKernelGGL((fp4_amax_kernel<F32, true>), grid, dim3(256), 0, st, a, items);
+      hipLaunchKernelGGL((fp4_amax_kernel<F32, true>), grid, dim3(256), 0, st, a, rows, items);
     else
-      hipLaunchKernelGGL((fp4_amax_kernel<F32, false>), grid, dim3(256), 0, st, a, items);
+      hipLaunchKernelGGL((fp4_amax_kernel<F32, false>), grid, dim3(256), 0, st, a, rows, items);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   const dim3 grid = grid_for(items, a.experts, kMaxBlocks);
   if (strided)
-    hipLaunchKernelGGL((fp4_quantize_kernel<NV, F32, true>), grid, dim3(256), 0, st, a, items, parts);
+    hipLaunchKernelGGL((fp4_quantize_kernel<NV, F32, true>), grid, dim3(256), 0, st, a, rows, items, parts);
   else
-    hipLaunchKernelGGL((fp4_quantize_kernel<NV, F32, false>), grid, dim3(256), 0, st, a, items, parts);
+    hipLaunchKernelGGL((fp4_quantize_kernel<NV, F32, false>), grid, dim3(256), 0, st, a, rows, items, parts);
   return hipGetLastError();
 }
 

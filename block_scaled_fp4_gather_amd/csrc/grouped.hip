@@ -104,24 +104,24 @@ __global__ void __launch_bounds__(256, 1) grouped_tile_kernel(GroupedArgs a, int
   const int wm = wave % T::WM, wn = wave / T::WM;
   const int n0 = t.tn * T::BN;
   RowSource<T::BM> p;
-  p.init(a.x + (int64_t)t.row0 * a.K, 2ll * a.K, t.rows, a.K, wm * T::FM * 16, wave, lane);
+  p.init(a.x + (int64_t)t.row0 * a.K, 2ll * a.K, t.rows, a.K, wm * T::FM * 32, wave, lane);
   const uint16_t* const w = a.w + (int64_t)t.e * a.N * a.K;
-  f32x4_t acc[T::FN][T::FM];
+  f32x16_t acc[T::FN][T::FM];
 #pragma unroll
   for (int f = 0; f < T::FN; ++f)
 #pragma unroll
-    for (int m = 0; m < T::FM; ++m) acc[f][m] = f32x4_t{};
+    for (int m = 0; m < T::FM; ++m) acc[f][m] = f32x16_t{};
   if constexpr (KN) {
     ColSource<T::BN> q;
-    q.init(w + n0, 2ll * a.N, a.K, a.N - n0, wn * T::FN * 16, wave, lane);
+    q.init(w + n0, 2ll * a.N, a.K, a.N - n0, wn * T::FN * 32, wave, lane);
     tile_loop<T>(p.steps(), p.ragged(), p, q, Bf16Op{}, smem, wave, acc);
   } else {
     RowSource<T::BN> q;
-    q.init(w + (int64_t)n0 * a.K, 2ll * a.K, min(T::BN, a.N - n0), a.K, wn * T::FN * 16, wave, lane);
+    q.init(w + (int64_t)n0 * a.K, 2ll * a.K, min(T::BN, a.N - n0), a.K, wn * T::FN * 32, wave, lane);
     tile_loop<T>(p.steps(), p.ragged(), p, q, Bf16Op{}, smem, wave, acc);
   }
   __syncthreads();
-  const int m1 = wm * T::FM * 16, n1 = n0 + wn * T::FN * 16;
+  const int m1 = wm * T::FM * 32, n1 = n0 + wn * T::FN * 32;
   store_rows<T, false>(smem, wave, lane, a.y + (int64_t)(t.row0 + m1) * a.N + n1, a.N, t.rows - m1, a.N - n1,
                        [&](int f, int m, int i) { return acc[f][m][i]; });
 }
@@ -144,29 +144,33 @@ __global__ void __launch_bounds__(256, 1) grouped_grad_kernel(GroupedGradArgs a,
   expert_rows(a.offsets, e, a.rows, r0, r1);
   const int n0 = tn * T::BM, k0 = tk * T::BN;
   const int wm = wave % T::WM, wn = wave / T::WM;
-  f32x4_t acc[T::FN][T::FM];
+  f32x16_t acc[T::FN][T::FM];
 #pragma unroll
   for (int f = 0; f < T::FN; ++f)
 #pragma unroll
-    for (int m = 0; m < T::FM; ++m) acc[f][m] = f32x4_t{};
+    for (int m = 0; m < T::FM; ++m) acc[f][m] = f32x16_t{};
   if (r1 > r0) {
     ColSource<T::BM> p;
     ColSource<T::BN> q;
-    p.init(a.dy + (int64_t)r0 * a.N + n0, 2ll * a.N, r1 - r0, a.N - n0, wm * T::FM * 16, wave, lane);
-    q.init(a.x + (int64_t)r0 * a.K + k0, 2ll * a.K, r1 - r0, a.K - k0, wn * T::FN * 16, wave, lane);
+    p.init(a.dy + (int64_t)r0 * a.N + n0, 2ll * a.N, r1 - r0, a.N - n0, wm * T::FM * 32, wave, lane);
+    q.init(a.x + (int64_t)r0 * a.K + k0, 2ll * a.K, r1 - r0, a.K - k0, wn * T::FN * 32, wave, lane);
     tile_loop<T>(p.steps(), p.ragged(), p, q, Bf16Op{}, smem, wave, acc);
     __syncthreads();
   }
-  const int n1 = n0 + wm * T::FM * 16, k1 = k0 + wn * T::FN * 16;
+  const int n1 = n0 + wm * T::FM * 32, k1 = k0 + wn * T::FN * 32;
   const int64_t at = ((int64_t)e * a.N + n1) * a.K + k1;
   if constexpr (F32) {
-    const int r = lane & 15, g = lane >> 4;
+    const int r = lane & 31, h = lane >> 5;
 #pragma unroll
     for (int m = 0; m < T::FM; ++m)
 #pragma unroll
       for (int f = 0; f < T::FN; ++f)
-        if (n1 + 16 * m + r < a.N && k1 + 16 * f + 4 * g < a.K)
-          *(f32x4_t*)((float*)a.dw + at + (int64_t)(16 * m + r) * a.K + 16 * f + 4 * g) = acc[f][m];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x4_t v = {acc[f][m][4 * q], acc[f][m][4 * q + 1], acc[f][m][4 * q + 2], acc[f][m][4 * q + 3]};
+          const int n = 32 * m + r, k = 32 * f + 8 * q + 4 * h;
+          if (n1 + n < a.N && k1 + k < a.K) *(f32x4_t*)((float*)a.dw + at + (int64_t)n * a.K + k) = v;
+        }
   } else {
     store_rows<T, false>(smem, wave, lane, (uint16_t*)a.dw + at, a.K, a.N - n1, a.K - k1,
                          [&](int f, int m, int i) { return acc[f][m][i]; });
