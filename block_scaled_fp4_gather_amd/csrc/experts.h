@@ -48,6 +48,7 @@ hipError_t launch_fp4_dequantize(const DequantArgs& a, hipStream_t st);
 // ---------------------------------------------------------------- routes
 
 constexpr int kGroupMaxExperts = 4096;
+constexpr int kProductMaxExperts = 2048;  // of the grouped products, whose tables are in LDS
 constexpr int64_t kGroupMaxRoutes = (int64_t)1 << 22;
 
 int64_t group_routes_workspace(int64_t routes, int E);
@@ -115,8 +116,6 @@ struct GroupedArgs {
   bool w_kn;
 };
 
-// Whether a launch of the tiles stays below 2^32 threads.
-bool grouped_fits(const GroupedArgs& a);
 hipError_t launch_grouped(const GroupedArgs& a, hipStream_t st);
 
 struct GroupedGradArgs {
@@ -129,7 +128,6 @@ struct GroupedGradArgs {
   bool f32;
 };
 
-bool grouped_fits(const GroupedGradArgs& a);
 hipError_t launch_grouped_weight_grad(const GroupedGradArgs& a, hipStream_t st);
 
 }  // namespace moe

@@ -125,7 +125,7 @@ moe_fp4_status grouped_shape(const moe_fp4_grouped_desc* d, int32_t rows) {
       d->out_features % 8 || rows < 0)
     return MOE_FP4_EINVAL;
   if (d->weight_layout != MOE_FP4_WEIGHT_OUT_IN && d->weight_layout != MOE_FP4_WEIGHT_IN_OUT) return MOE_FP4_EINVAL;
-  if (d->num_experts > moe::kGroupMaxExperts || d->in_features > kMaxCols || d->out_features > kMaxCols ||
+  if (d->num_experts > moe::kProductMaxExperts || d->in_features > kMaxCols || d->out_features > kMaxCols ||
       rows > moe::kGroupMaxRoutes)
     return MOE_FP4_EUNSUPPORTED;
   return MOE_FP4_OK;
@@ -312,8 +312,9 @@ moe_fp4_status moe_fp4_grouped_linear(const moe_fp4_grouped_desc* desc, const ui
   const int E = desc->num_experts, K = desc->in_features, N = desc->out_features;
   if (overlapping({{x, 2ll * rows * K}, {weight, 2ll * E * N * K}, {offsets, 4ll * (E + 1)}}, {{y, 2ll * rows * N}}))
     return MOE_FP4_EINVAL;
+  // row tiles times column tiles are counted in 32 bits
+  if (((int64_t)rows / 128 + E) * ((N + 127) / 128) > 0x7FFFFFFF) return MOE_FP4_EUNSUPPORTED;
   const moe::GroupedArgs a{x, weight, offsets, y, rows, E, K, N, desc->weight_layout == MOE_FP4_WEIGHT_IN_OUT};
-  if (!moe::grouped_fits(a)) return MOE_FP4_EUNSUPPORTED;
   return from_hip(moe::launch_grouped(a, (hipStream_t)stream));
 }
 
@@ -331,7 +332,6 @@ moe_fp4_status moe_fp4_grouped_weight_grad(const moe_fp4_grouped_desc* desc, int
                   {{dw, (f32 ? 4ll : 2ll) * E * N * K}}))
     return MOE_FP4_EINVAL;
   const moe::GroupedGradArgs a{dy, x, offsets, dw, rows, E, K, N, f32};
-  if (!moe::grouped_fits(a)) return MOE_FP4_EUNSUPPORTED;
   return from_hip(moe::launch_grouped_weight_grad(a, (hipStream_t)stream));
 }
 

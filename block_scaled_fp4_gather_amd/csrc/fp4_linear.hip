@@ -107,6 +107,25 @@ __global__ void __launch_bounds__(256)
 
 __device__ __forceinline__ i32x8_t wide(const i32x4_t& v) { return i32x8_t{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
 
+// The gated activations of act.h with the hardware's reciprocal (off by a unit
+// in the last place) for their quotients: a tile of 256 x 256 has 128 of them a
+// lane, and nothing beside them.
+template <int KIND>
+__device__ __forceinline__ float quick_act(const ActParams& p, float g, float u) {
+  if constexpr (KIND == kActGeluTanh) {
+    const float z = 0.7978845608028654f * (g + 0.044715f * g * g * g);
+    return g * (1.0f - __builtin_amdgcn_rcpf(1.0f + __expf(2.0f * z))) * u;  // 0.5 (1 + tanh z)
+  } else if constexpr (KIND == kActSwigluOai) {
+    const float gc = g > p.limit ? p.limit : g;
+    const float uc = u > p.limit ? p.limit : (u < -p.limit ? -p.limit : u);
+    return gc * __builtin_amdgcn_rcpf(1.0f + __expf(-p.alpha * gc)) * (uc + p.beta);
+  } else if constexpr (KIND == kActRelu2) {
+    return relu2(g);
+  } else {
+    return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+  }
+}
+
 // ---- few tokens: FS subtiles x 16 TT tokens per workgroup, whose NW waves
 // share K in runs of consecutive steps of 256 and join their sums in LDS in
 // wave order.  U steps of a wave are in flight.
@@ -268,28 +287,41 @@ __global__ void __launch_bounds__(NW * 64)
 // ---- many tokens
 
 // Rows in operand order: a slot holds ROWS / 16 subtiles x 2 halves x 1 KiB.
-// Subtiles past the last are the last again.
-template <int ROWS>
+// Subtiles past the last are zero.  A wave's fragments are STRIDE fragments
+// apart.
+template <int ROWS, int STRIDE>
 struct PackSource {
   static constexpr int kCopies = ROWS / 32;
-  const uint8_t* base;
-  uint32_t off[kCopies];
+  i32x4_t buffer, now;  // kept, and for the next copies
+  uint32_t stride;     // bytes of two subtiles
+  uint32_t off, soff, gap;  // this lane's bytes of a copy; of the next copy; from one to the next
   uint32_t at;
-  __device__ void init(const uint8_t* p, int kb, int64_t sub0, int64_t subs, int first, int wave, int lane) {
-    base = p + sub0 * kb * 1024;
-    const int64_t last = subs - 1 - sub0;
-#pragma unroll
-    for (int c = 0; c < kCopies; ++c)
-      off[c] = (uint32_t)min((int64_t)(c * 2 + wave / 2), last) * (uint32_t)(kb * 1024) + (wave & 1) * 1024 + lane * 16;
-    at = (uint32_t)first * 128 + ((lane >> 4) & 1) * 2048 + (lane >> 5) * 256 + (lane & 15) * 16;
+  int wave;
+  __device__ void lanes(int first, int w, int lane) {
+    wave = w;
+    off = lane * 16;
+    at = (uint32_t)first * 4096 + ((lane >> 4) & 1) * 2048 + (lane >> 5) * 256 + (lane & 15) * 16;
   }
-  template <bool TAIL>
-  __device__ __forceinline__ void copy(int step, int c, uint32_t lds) const {
-    dma16_at(base + (int64_t)step * 2048, off[c], lds + c * 4096);
+  __device__ void set(const uint8_t* p, int kb, int64_t sub0, int64_t subs) {
+    // a wave copies one half of every other subtile
+    const int64_t mine = (int64_t)(wave / 2) * kb * 1024 + (wave & 1) * 1024;
+    const int64_t all = min((int64_t)(ROWS / 16), subs - sub0) * kb * 1024 - mine;
+    buffer = buffer_of(uniform(p + sub0 * kb * 1024 + mine), all > 0 ? (uint32_t)all : 0u);
+    stride = __builtin_amdgcn_readfirstlane(2 * kb * 1024);
+  }
+  __device__ void none() { buffer[2] = 0; }
+  __device__ __forceinline__ void start(int step) {
+    now = scalar(buffer);
+    soff = (uint32_t)__builtin_amdgcn_readfirstlane(step * 2048);
+    gap = (uint32_t)__builtin_amdgcn_readfirstlane((int)stride);
+  }
+  __device__ __forceinline__ void copy(int c, uint32_t lds) {
+    copy16(now, off, soff, lds + c * 4096);
+    soff += gap;
   }
   // 64 values of 32 rows: two of a K block's four lane groups, of two subtiles
   __device__ __forceinline__ i32x4_t read(const uint8_t* area, int quarter, int f) const {
-    return *(const i32x4_t*)(area + at + quarter * 512 + f * 4096);
+    return *(const i32x4_t*)(area + at + quarter * 512 + f * (STRIDE * 4096));
   }
 };
 
@@ -303,40 +335,47 @@ struct Fp4Op {
   static constexpr int kRing = kPairs * 256;
   static_assert(kPairs % 4 == 0, "whole copies");
   const uint8_t* src[kCopies];
-  int64_t stride[kCopies];
-  uint32_t lds, lane_off;
-  const uint8_t* mine;  // this lane's dword of the wave's first token pair
-  int npairs;           // from there to its first weight pair, bytes
+  uint32_t stride[kCopies];
+  const uint8_t* from[kCopies];  // of the next step
+  uint32_t lds, lane_off, to;
+  const uint8_t* mine;  // this lane's dword of the wave's first token fragment
+  int weights;          // from there to its first weight fragment, bytes
   struct Scales {
     uint32_t m[T::FM], n[T::FN];
   };
-  __device__ void init(uint8_t* ring, const uint8_t* xs, int64_t xpairs, int64_t xpair0, const uint8_t* ws,
-                       int64_t wpairs, int64_t wpair0, int wm, int wn, int wave, int lane) {
+  __device__ void lanes(uint8_t* ring, int wm, int wn, int wave, int lane) {
     lane_off = lane * (kWide ? 16 : 4);
+    lds = lds_addr(ring) + wave * kCopies * (kWide ? 1024 : 256);
+    mine = ring + wm * 256 + lane * 4;
+    weights = (T::BM / 32 + wn * T::FN - wm) * 256;
+  }
+  __device__ void set(const uint8_t* xs, int64_t xpairs, int64_t xpair0, const uint8_t* ws, int64_t wpairs,
+                      int64_t wpair0, int wave) {
 #pragma unroll
     for (int c = 0; c < kCopies; ++c) {
       const int pair = kWide ? wave * 4 : wave * kCopies + c;
       const bool tokens = pair < T::BM / 32;
-      stride[c] = (tokens ? xpairs : wpairs) * 256;
-      src[c] = tokens ? xs + (xpair0 + pair) * 256 : ws + (wpair0 + pair - T::BM / 32) * 256;
+      stride[c] = (uint32_t)((tokens ? xpairs : wpairs) * 256);
+      src[c] = uniform(tokens ? xs + (xpair0 + pair) * 256 : ws + (wpair0 + pair - T::BM / 32) * 256);
     }
-    lds = lds_addr(ring) + wave * kCopies * (kWide ? 1024 : 256);
-    mine = ring + wm * T::FM * 256 + lane * 4;
-    npairs = (T::BM / 32 + wn * T::FN - wm * T::FM) * 256;
   }
-  __device__ __forceinline__ void copy(int step, int c) const {
-    const uint32_t to = lds + (step & 1) * kRing + c * 256;
+  __device__ __forceinline__ void start(int step, int ring) {
+    to = lds + ring * kRing;
+#pragma unroll
+    for (int c = 0; c < kCopies; ++c) from[c] = src[c] + (uint64_t)step * stride[c];
+  }
+  __device__ __forceinline__ void copy(int c) const {
     if (kWide)
-      dma16_at(src[c] + step * stride[c], lane_off, to);
+      dma16_at(from[c], lane_off, to);
     else
-      dma4_at(src[c] + step * stride[c], lane_off, to);
+      dma4_at(from[c], lane_off, to + c * 256);
   }
-  __device__ __forceinline__ void read(int step, Scales& s) const {
-    const uint8_t* const p = mine + (step & 1) * kRing;
+  __device__ __forceinline__ void read(int ring, Scales& s) const {
+    const uint8_t* const p = mine + ring * kRing;
 #pragma unroll
-    for (int i = 0; i < T::FM; ++i) s.m[i] = *(const uint32_t*)(p + i * 256);
+    for (int i = 0; i < T::FM; ++i) s.m[i] = *(const uint32_t*)(p + i * T::WM * 256);
 #pragma unroll
-    for (int i = 0; i < T::FN; ++i) s.n[i] = *(const uint32_t*)(p + npairs + i * 256);
+    for (int i = 0; i < T::FN; ++i) s.n[i] = *(const uint32_t*)(p + weights + i * 256);
   }
   template <int QUARTER, int F, int M>
   __device__ __forceinline__ f32x16_t mul(const i32x4_t& a, const i32x4_t& b, const f32x16_t& c, const Scales& s) const {
@@ -348,58 +387,117 @@ struct Fp4Op {
 template <class T>
 constexpr int kFp4Lds = 2 * T::kSlot + 2 * Fp4Op<T>::kRing;
 
+struct TileArgs {
+  Fp4Shape s;
+  const uint8_t* prepared;
+  const uint8_t* packed;
+  const uint8_t* pscales;
+  int M, tiles_m, tiles_n;
+  uint16_t* out;
+};
+
 template <class T, bool GATED>
-__global__ void __launch_bounds__(256, 1)
-    fp4_tile_kernel(Fp4Shape s, const uint8_t* __restrict__ prepared, const uint8_t* __restrict__ packed,
-                    const uint8_t* __restrict__ pscales, int M, int tiles_m, int tiles_n, uint16_t* __restrict__ out) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // Workgroups are dealt to the 8 XCDs in turn: give each XCD a contiguous
-  // range of tiles, in bands of 4 token tiles, so that what runs together on
-  // it shares token and weight tiles in its L2.
-  const int per = gridDim.x / 8;
-  const int logical = (blockIdx.x % 8) * per + blockIdx.x / 8;
-  if (logical >= tiles_m * tiles_n) return;
-  const int band = logical / (4 * tiles_n), in_band = logical - band * 4 * tiles_n;
-  const int bm = min(4, tiles_m - 4 * band);
-  const int tn = in_band / bm, tm = 4 * band + in_band % bm;
-  const int wm = wave % T::WM, wn = wave / T::WM;
-  const int kb = s.kblocks(), ns = s.subtiles();
-  const int64_t groups = (M + 15) / 16;
-  PackSource<T::BM> p;
-  PackSource<T::BN> q;
+struct LinearWork {
+  PackSource<T::BM, T::WM> p;
+  PackSource<T::BN, 1> q;
   Fp4Op<T> op;
-  p.init(packed, kb, (int64_t)tm * (T::BM / 16), groups, wm * T::FM * 32, wave, lane);
-  q.init(prepared, kb, (int64_t)tn * (T::BN / 16), ns, wn * T::FN * 32, wave, lane);
-  op.init(smem + 2 * T::kSlot, pscales, Fp4Shape::pair_cols(groups), (int64_t)tm * (T::BM / 32),
-          prepared + s.codes_bytes(ns), Fp4Shape::pair_cols(ns), (int64_t)tn * (T::BN / 32), wm, wn, wave, lane);
-  f32x16_t acc[T::FN][T::FM];
-#pragma unroll
-  for (int f = 0; f < T::FN; ++f)
-#pragma unroll
-    for (int t = 0; t < T::FM; ++t) acc[f][t] = f32x16_t{};
-  tile_loop<T>(s.ksteps(), false, p, q, op, smem, wave, acc);
-  __syncthreads();
-  const int64_t m1 = (int64_t)tm * T::BM + wm * T::FM * 32;
-  const int n1 = (tn * T::BN + wn * T::FN * 32) / (GATED ? 2 : 1);
-  auto put = [&](auto kind) __attribute__((always_inline)) {
-    store_rows<T, GATED>(smem, wave, lane, out + m1 * s.N + n1, s.N, M - m1, s.N - n1,
-                         [&](int f, int t, int i) __attribute__((always_inline)) {
-                           constexpr int kKind = decltype(kind)::value;
-                           if constexpr (kKind < 0)
-                             return acc[f][t][i];
-                           else
-                             return act_of<kKind>(s.act, acc[f][t][i], GATED ? acc[f][t][i + 8] : 0.0f);  // rows 16 on: up
-                         });
-  };
-  if constexpr (GATED) {
-    if (s.act.kind == kActGeluTanh) put(std::integral_constant<int, kActGeluTanh>{});
-    else if (s.act.kind == kActSwigluOai) put(std::integral_constant<int, kActSwigluOai>{});
-    else put(std::integral_constant<int, kActSilu>{});
-  } else {
-    if (s.has_act) put(std::integral_constant<int, kActRelu2>{});
-    else put(std::integral_constant<int, -1>{});
+  int active;
+
+  Places places;
+  int lane, wave, wm, wn;
+  Parked row0, col0;  // of the tile that is computed
+
+  __device__ LinearWork(const Places& tiles, uint8_t* ring, int w)
+      : places(tiles), lane(threadIdx.x & 63), wave(w), wm(w % T::WM), wn(w / T::WM) {
+    p.lanes(wm, wave, lane);
+    q.lanes(wn * T::FN, wave, lane);
+    op.lanes(ring, wm, wn, wave, lane);
   }
+  // Workgroups are dealt to the 8 XCDs in turn: each XCD has a contiguous range
+  // of tiles, in bands of 4 token tiles, so that what runs together on it shares
+  // token and weight tiles in its L2.
+  __device__ bool locate(int i, int& m, int& n) const {
+    const auto& a = kernel_args<TileArgs>();
+    const int total = a.tiles_m * a.tiles_n, share = (total + 7) / 8;
+    const int64_t slot = blockIdx.x / 8 + (int64_t)i * (gridDim.x / 8);
+    const int64_t at = (blockIdx.x % 8) * (int64_t)share + slot;
+    if (slot >= share || at >= total) return false;
+    const int band = (int)at / (4 * a.tiles_n), in_band = (int)at - band * 4 * a.tiles_n;
+    const int bm = min(4, a.tiles_m - 4 * band);
+    n = in_band / bm;
+    m = 4 * band + in_band % bm;
+    return true;
+  }
+  __device__ int fetch(int i) {
+    int m, n;
+    if (!locate(i, m, n)) {
+      places.put(i, make_int4(0, 0, 0, 0));
+      return 0;
+    }
+    const auto& a = kernel_args<TileArgs>();
+    places.put(i, make_int4(m * T::BM, n * T::BN, min(T::FM, (a.M - m * T::BM + 32 * T::WM - 1) / (32 * T::WM)),
+                            (a.s.K + 255) / 256));
+    Fp4Shape s;
+    s.K = a.s.K;
+    s.N = a.s.N;
+    s.gated = GATED;
+    const int kb = s.kblocks(), ns = s.subtiles();
+    const int64_t groups = ((int64_t)a.M + 15) / 16;
+    p.set(a.packed, kb, (int64_t)m * (T::BM / 16), groups);
+    q.set(a.prepared, kb, (int64_t)n * (T::BN / 16), ns);
+    op.set(a.pscales, Fp4Shape::pair_cols(groups), (int64_t)m * (T::BM / 32), a.prepared + s.codes_bytes(ns),
+           Fp4Shape::pair_cols(ns), (int64_t)n * (T::BN / 32), wave);
+    return s.ksteps();
+  }
+  __device__ int begin(int i) {
+    const int4 t = places.get(i);
+    row0 = t.x;
+    col0 = t.y;
+    active = t.z;
+    return t.w;
+  }
+  template <int A>
+  __device__ __forceinline__ void store(f32x16_t (&acc)[T::FN][A]) {
+    const auto& a = kernel_args<TileArgs>();
+    const ActParams act = {a.s.act.kind, a.s.act.alpha, a.s.act.beta, a.s.act.limit};
+    constexpr int kCols = GATED ? 16 : 32;  // outputs of a fragment
+    const int m0 = row0, N = a.s.N, n1 = (int)col0 / (GATED ? 2 : 1) + wn * T::FN * kCols;
+    const TileOut o(a.out + (int64_t)m0 * N + n1, 2ll * N, min(T::BM, a.M - m0));
+    auto put = [&](auto kind) __attribute__((always_inline)) {
+      constexpr int kKind = decltype(kind)::value;
+#pragma unroll
+      for (int t = 0; t < A; ++t) {
+        hold<T>(acc, t);
+        const uint32_t row = ((t * T::WM + wm) * 32 + (threadIdx.x & 31)) * o.ld;
+#pragma unroll
+        for (int f = 0; f < T::FN; ++f) {
+          store_fragment(o, row + 2 * kCols * f, N - n1 - kCols * f, kCols / 8, [&](int i) __attribute__((always_inline)) {
+            if constexpr (kKind < 0)
+              return acc[f][t][i];
+            else
+              return quick_act<kKind>(act, acc[f][t][i], GATED ? acc[f][t][i + 8] : 0.0f);  // rows 16 on: up
+          });
+        }
+      }
+    };
+    if constexpr (GATED) {
+      if (act.kind == kActGeluTanh) put(std::integral_constant<int, kActGeluTanh>{});
+      else if (act.kind == kActSwigluOai) put(std::integral_constant<int, kActSwigluOai>{});
+      else put(std::integral_constant<int, kActSilu>{});
+    } else {
+      if (a.s.has_act) put(std::integral_constant<int, kActRelu2>{});
+      else put(std::integral_constant<int, -1>{});
+    }
+  }
+};
+
+template <class T, bool GATED>
+__global__ void __launch_bounds__(256, T::kPerCu) fp4_tile_kernel(TileArgs) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  __shared__ int4 tiles[4][4];
+  LinearWork<T, GATED> work(Places{tiles[wave]}, smem + 2 * T::kSlot, wave);
+  tile_loop<T>(work, smem, wave);
 }
 
 // ---- launches
@@ -414,13 +512,13 @@ template <class T>
 hipError_t launch_tile(const Fp4Shape& s, const uint8_t* prepared, const Tokens& x, int M, uint16_t* out,
                        hipStream_t st) {
   const int tm = (M + T::BM - 1) / T::BM, tn = (s.subtiles() + T::BN / 16 - 1) / (T::BN / 16);
-  const dim3 grid(grid8((int64_t)tm * tn));
+  const int64_t n = (int64_t)tm * tn;
+  const dim3 grid(n < T::kGrid ? grid8(n) : (unsigned)T::kGrid);
+  const TileArgs a{s, prepared, x.packed, x.scales, M, tm, tn, out};
   if (s.gated)
-    hipLaunchKernelGGL((fp4_tile_kernel<T, true>), grid, dim3(256), kFp4Lds<T>, st, s, prepared, x.packed, x.scales, M,
-                       tm, tn, out);
+    hipLaunchKernelGGL((fp4_tile_kernel<T, true>), grid, dim3(256), kFp4Lds<T>, st, a);
   else
-    hipLaunchKernelGGL((fp4_tile_kernel<T, false>), grid, dim3(256), kFp4Lds<T>, st, s, prepared, x.packed, x.scales, M,
-                       tm, tn, out);
+    hipLaunchKernelGGL((fp4_tile_kernel<T, false>), grid, dim3(256), kFp4Lds<T>, st, a);
   return hipGetLastError();
 }
 

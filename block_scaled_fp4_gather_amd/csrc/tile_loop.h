@@ -1,8 +1,8 @@
 // Main loop of the products of many rows (grouped.hip, fp4_linear.hip): a
-// workgroup of 4 waves computes BM x BN outputs, each wave BM / WM x BN / WN of
-// them from 32 x 32 matrix instructions whose operands are 32 bytes of a row:
-// 16 bf16 or 64 E2M1 values, 16 bytes a lane.  A step is 128 bytes of the
-// contraction, two halves of two such quarters.
+// workgroup of 4 waves computes one tile of BM x BN outputs after the other,
+// each wave BM / WM x BN / WN of them from 32 x 32 matrix instructions whose
+// operands are 32 bytes of a row: 16 bf16 or 64 E2M1 values, 16 bytes a lane.  A
+// step is 128 bytes of the contraction, two halves of two such quarters.
 //
 // Both operands come to LDS by direct copies, in a ring of two slots, and from
 // there to registers half a step before they are multiplied:
@@ -11,8 +11,11 @@
 //   half 1             multiply half 1; copy step s + 2 over slot s; read half
 //                      0 of step s + 1
 // so that a copy has a whole step (2048 cycles of the matrix cores at 256 x
-// 256) and an LDS read half of one to arrive, with one barrier a step.  One
-// wave per SIMD then keeps its matrix core busy by itself; a wave's 128 x 128
+// 256) and an LDS read half of one to arrive, with one barrier a step.  The
+// steps of a tile and those of the next follow each other without a gap: what
+// is copied runs two steps ahead of what is multiplied, across tiles, and the
+// outputs go from the accumulators to memory beside it.
+// One wave per SIMD keeps its matrix core busy by itself; a wave's 128 x 128
 // outputs, which halve the LDS reads of 128 x 64, need 256 accumulators.
 // One wave issues a 16 x 16 instruction every 30 cycles or so, though bf16 and
 // E2M1 ones take 16 (measured: 1.4 and 5.0 PFLOP/s of zeros; 2.1 and 6.5 with
@@ -34,9 +37,6 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
 
-// What copies read in the place of values past the end of a contraction.
-static __device__ const uint4 zero_chunk = {0, 0, 0, 0};
-
 // f(integral_constant<int, 0>) .. f(integral_constant<int, N - 1>).  (The loop
 // over a half's products is past what the compiler unrolls by itself, and an
 // accumulator with an index of run time would be memory.)
@@ -54,52 +54,115 @@ struct Tile {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
   static constexpr int FM = BM / 32 / WM, FN = BN / 32 / WN;  // a wave's fragments of 32 rows
   static constexpr int kM = BM * 128, kSlot = (BM + BN) * 128;
+  // workgroups of a launch: as many as run at once on the 256 CUs, and of them on an XCD
+  static constexpr int kPerCu = kSlot <= 32768 ? 2 : 1, kGrid = 256 * kPerCu, kPerXcd = kGrid / 8;
   static_assert(WM * WN == 4 && BM % 32 == 0 && BN % 32 == 0 && FM > 0 && FN > 0, "4 waves, whole copies");
 };
 
-// A value that is not computed ahead of its place: what the cut step alone
-// needs stays out of the registers of the whole loop.
-__device__ __forceinline__ uint32_t here(uint32_t v) {
-  asm volatile("" : "+v"(v));
-  return v;
+__device__ __forceinline__ const uint8_t* uniform(const void* p) {
+  const uint64_t v = (uint64_t)p;
+  return (const uint8_t*)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)v) |
+                          (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32)) << 32);
+}
+
+// `bytes` of memory as a buffer: loads at or past its end give zeros, stores do
+// nothing.
+__device__ __forceinline__ i32x4_t buffer_of(const uint8_t* p, uint32_t bytes) {
+  const uint64_t v = (uint64_t)p;
+  return i32x4_t{(int)(uint32_t)v, (int)(uint32_t)(v >> 32), __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
+}
+// The same in scalar registers, wherever it has been kept.
+__device__ __forceinline__ i32x4_t scalar(const i32x4_t& b) {
+  return i32x4_t{__builtin_amdgcn_readfirstlane(b[0]), __builtin_amdgcn_readfirstlane(b[1]),
+                 __builtin_amdgcn_readfirstlane(b[2]), __builtin_amdgcn_readfirstlane(b[3])};
+}
+constexpr uint32_t kOutside = 0x80000000u;  // an offset past every buffer's end (2^30 bytes at most)
+
+// Direct copy as in gemm_util.h from a buffer: lane l's 16 bytes at off + scalar
+// land at LDS byte lds + 16 l.  One wave of a SIMD has to issue all of its own
+// copies beside its products, so m0 is neither saved nor restored: nothing else
+// in the kernels of this loop uses it.
+__device__ __forceinline__ void copy16(const i32x4_t& buffer, uint32_t off, uint32_t scalar, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+               :
+               : "v"(off), "s"(buffer), "s"(scalar), "s"(lds));
+}
+
+// A wave's value that waits in a vector register, of which there are some left.
+struct Parked {
+  int v;
+  __device__ __forceinline__ void operator=(int x) {
+    v = x;
+    asm volatile("" : "+v"(v));
+  }
+  __device__ __forceinline__ operator int() const { return __builtin_amdgcn_readfirstlane(v); }
+};
+
+// What a workgroup's tiles are, from when they are first copied until they are
+// multiplied (up to 3 tiles later): each wave keeps them for itself in LDS.
+struct Places {
+  int4* at;  // of the wave's: 4
+  __device__ __forceinline__ void put(int i, int4 v) const {
+    if ((threadIdx.x & 63) == 0) at[i & 3] = v;
+    wave_sync();
+  }
+  __device__ __forceinline__ int4 get(int i) const {
+    const int4 v = at[i & 3];
+    return make_int4(__builtin_amdgcn_readfirstlane(v.x), __builtin_amdgcn_readfirstlane(v.y),
+                     __builtin_amdgcn_readfirstlane(v.z), __builtin_amdgcn_readfirstlane(v.w));
+  }
+};
+
+// A kernel's arguments (one struct) where they are used: read again each time, so
+// that the loop's scalar registers do not hold what a tile needs once.
+template <class A>
+__device__ __forceinline__ const __attribute__((address_space(4))) A& kernel_args() {
+  auto p = (const __attribute__((address_space(4))) A*)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *p;
 }
 
 // Rows whose contraction is contiguous (bf16): a slot holds ROWS x 128 bytes,
-// 16-byte chunk c of row r at position c ^ row_swz(r).  Rows past the last are
-// the last again; contraction past its end is zero.
-template <int ROWS>
+// 16-byte chunk c of row r at position c ^ row_swz(r).  Rows past the last and
+// contraction past its end are zero.  A wave's fragments are STRIDE fragments
+// apart.
+template <int ROWS, int STRIDE>
 struct RowSource {
   static constexpr int kCopies = ROWS / 32;
-  const uint8_t* base;
-  uint32_t off[kCopies];  // of this lane's chunk of each copy (8 rows a wave, 32 a workgroup)
-  uint32_t chunk;
-  uint32_t bytes;  // of the contraction
-  uint32_t at;     // of this lane's chunk of quarter 0 in fragment 0
+  i32x4_t buffer, now;  // kept, and for the next copies
+  uint32_t bytes;      // of the contraction, and of a row
+  uint32_t off, last;  // this lane's row and chunk of copy 0 (8 rows a wave, 32 a workgroup); the same in the cut step
+  uint32_t voff, soff, gap;  // of the next copy; from one to the next
+  int row, chunk;
+  uint32_t at;         // of this lane's chunk of quarter 0 in fragment 0
 
-  __device__ void init(const void* p, int64_t ld_bytes, int rows, int64_t k, int first, int wave, int lane) {
-    base = (const uint8_t*)p;
-    bytes = (uint32_t)(2 * k);
-    const int row = wave * 8 + lane / 8;
+  // first: the wave's first fragment
+  __device__ void lanes(int first, int wave, int lane) {
+    row = wave * 8 + lane / 8;
     chunk = ((lane & 7) ^ row_swz<128>(row)) * 16;
-#pragma unroll
-    for (int c = 0; c < kCopies; ++c) off[c] = (uint32_t)min(c * 32 + row, rows - 1) * (uint32_t)ld_bytes + chunk;
     const int r = lane & 31, h = lane >> 5;
-    at = (uint32_t)(first + r) * 128 + (h ^ row_swz<128>(r)) * 16;
+    at = (uint32_t)(first * 32 + r) * 128 + (h ^ row_swz<128>(r)) * 16;
   }
-  __device__ int steps() const { return (int)((bytes + 127) / 128); }
-  __device__ bool ragged() const { return bytes % 128 != 0; }
-  template <bool TAIL>
-  __device__ __forceinline__ void copy(int step, int c, uint32_t lds) const {
-    const uint8_t* const from = base + (int64_t)step * 128;
-    if (TAIL) {
-      const bool in = (uint32_t)step * 128 + chunk < bytes;
-      dma16(in ? (const void*)(from + here(off[c])) : (const void*)&zero_chunk, lds + c * 4096);
-    } else {
-      dma16_at(from, off[c], lds + c * 4096);
-    }
+  __device__ void set(const void* p, int rows, int k) {
+    bytes = __builtin_amdgcn_readfirstlane(2 * k);
+    buffer = buffer_of(uniform(p), (uint32_t)min(rows, ROWS) * bytes);
+    off = (uint32_t)row * bytes + chunk;
+    last = (bytes & ~127u) + chunk < bytes ? off : kOutside;
+  }
+  __device__ int steps() const { return (bytes + 127) / 128; }
+  __device__ void none() { buffer[2] = 0; }
+  __device__ __forceinline__ void start(int step) {
+    now = scalar(buffer);
+    soff = (uint32_t)__builtin_amdgcn_readfirstlane(step * 128);
+    gap = (uint32_t)__builtin_amdgcn_readfirstlane((int)(32 * bytes));
+    voff = soff + 128 > bytes ? last : off;
+  }
+  __device__ __forceinline__ void copy(int c, uint32_t lds) {
+    copy16(now, voff, soff, lds + c * 4096);
+    soff += gap;
   }
   __device__ __forceinline__ i32x4_t read(const uint8_t* area, int quarter, int f) const {
-    return *(const i32x4_t*)(area + (at ^ (quarter * 32)) + f * 4096);
+    return *(const i32x4_t*)(area + (at ^ (quarter * 32)) + f * (STRIDE * 4096));
   }
 };
 
@@ -109,50 +172,57 @@ struct RowSource {
 // 32-byte chunk c of row k is at c ^ (2 (k % 4) + 8 (k / 8 % 2)), so that the 4
 // rows and the 2 chunks next to each other of 32 lanes lie in different banks.
 // Columns past the last chunk are that chunk again; rows past the last are zero.
-template <int COLS>
+template <int COLS, int STRIDE>
 struct ColSource {
   static constexpr int kCopies = COLS / 32;
   static constexpr int kRow = COLS * 2, kLanes = kRow / 16, kRows = 64 / kLanes;  // a copy's lanes per row, and rows
   static constexpr int kMask = kRow / 32 - 1;
-  const uint8_t* base;
-  uint32_t off[kCopies];
-  int64_t ld;
-  int row, rows;           // this lane's row of copy 0; rows of the contraction
+  static constexpr int kSwaps = COLS == 256 ? 2 : 1;  // places of a lane's chunk: copies of 8 rows differ in k / 8 % 2
+  static_assert(COLS == 256 || COLS == 128, "rows of a copy");
+  const uint8_t* base;     // of the next step
+  uint32_t ld;             // bytes of a row
+  int rows;                // of the contraction, from the next step on
+  i32x4_t buffer;
+  uint32_t soff, gap;      // of the next copy; from one to the next
+  int row;                 // this lane's row of copy 0
+  uint32_t off[kSwaps];    // and its chunk there, and in copy 1
   uint32_t at;             // this lane's row and place in a 32-byte chunk
-  uint32_t swz, first;     // of its row; its chunk in fragment 0
+  uint32_t swz, chunk;     // of its row; its chunk in fragment 0
 
   __device__ static int swizzle(int k) { return ((k & 3) << 1 | (k & 8)) & kMask; }
-  __device__ void init(const void* p, int64_t ld_bytes, int64_t n, int64_t cols, int first_col, int wave, int lane) {
-    base = (const uint8_t*)p;
-    ld = ld_bytes;
-    rows = (int)n;
+  __device__ void lanes(int first, int wave, int lane) {
     row = wave * kRows + lane / kLanes;
-#pragma unroll
-    for (int c = 0; c < kCopies; ++c) {
-      const int k = c * 4 * kRows + row;
-      const int chunk = (lane % kLanes) ^ (swizzle(k) << 1);
-      off[c] = (uint32_t)k * (uint32_t)ld_bytes + (uint32_t)min((int64_t)chunk, cols / 8 - 1) * 16;
-    }
     const int i = lane & 15, q = lane >> 4;
     const int k = 8 * (q >> 1) + (i >> 2);
     at = (uint32_t)k * kRow + (i & 3) * 8;
     swz = (uint32_t)swizzle(k);
-    first = (uint32_t)first_col / 16 + (q & 1);
+    chunk = (uint32_t)first * 2 + (q & 1);
   }
-  __device__ int steps() const { return (rows + 63) / 64; }
-  __device__ bool ragged() const { return rows % 64 != 0; }
-  template <bool TAIL>
-  __device__ __forceinline__ void copy(int step, int c, uint32_t lds) const {
-    const uint8_t* const from = base + (int64_t)step * 64 * ld;
-    if (TAIL) {
-      const bool in = step * 64 + c * 4 * kRows + row < rows;
-      dma16(in ? (const void*)(from + here(off[c])) : (const void*)&zero_chunk, lds + c * 4096);
-    } else {
-      dma16_at(from, off[c], lds + c * 4096);
-    }
+  // n rows of the contraction (0: all zero), from a column on of which the matrix has `cols` to its end
+  __device__ void set(const void* p, int ld_bytes, int n, int cols, int lane) {
+    base = uniform(p);
+    ld = __builtin_amdgcn_readfirstlane(ld_bytes);
+    rows = __builtin_amdgcn_readfirstlane(n);
+#pragma unroll
+    for (int c = 0; c < kSwaps; ++c)
+      off[c] = (uint32_t)row * ld +
+               (uint32_t)min((lane % kLanes) ^ (swizzle(c * 4 * kRows + row) << 1), cols / 8 - 1) * 16;
+  }
+  __device__ void none() { rows = 0; }
+  __device__ __forceinline__ void start(int) {
+    // the last row ends with the matrix's row, which starts before this column
+    buffer = scalar(buffer_of(base, rows > 0 ? (uint32_t)min(rows, 64) * ld : 0u));
+    base += (int64_t)64 * ld;
+    rows -= 64;
+    soff = 0;
+    gap = (uint32_t)__builtin_amdgcn_readfirstlane((int)(4 * kRows * ld));
+  }
+  __device__ __forceinline__ void copy(int c, uint32_t lds) {
+    copy16(buffer, off[c % kSwaps], soff, lds + c * 4096);
+    soff += gap;
   }
   __device__ __forceinline__ i32x4_t read(const uint8_t* area, int quarter, int f) const {
-    const uint32_t a = (uint32_t)(uintptr_t)(const lds_char*)area + at + (((first + 2 * f) ^ swz) & kMask) * 32;
+    const uint32_t a = (uint32_t)(uintptr_t)(const lds_char*)area + at + (((chunk + 2 * STRIDE * f) ^ swz) & kMask) * 32;
     const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)(a + quarter * 16 * kRow));
     const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)(a + quarter * 16 * kRow + 4 * kRow));
     struct Two {
@@ -165,7 +235,8 @@ struct ColSource {
 struct Bf16Op {
   static constexpr int kCopies = 0;
   struct Scales {};
-  __device__ __forceinline__ void copy(int, int) const {}
+  __device__ __forceinline__ void start(int, int) {}
+  __device__ __forceinline__ void copy(int) {}
   __device__ __forceinline__ void read(int, Scales&) const {}
   template <int QUARTER, int F, int T>
   __device__ __forceinline__ f32x16_t mul(const i32x4_t& a, const i32x4_t& b, const f32x16_t& c, const Scales&) const {
@@ -174,14 +245,22 @@ struct Bf16Op {
   }
 };
 
-// acc[f][t] += rows of q (fragment f, the accumulator's acc_row) times rows of
-// p (fragment t, its lane % 32) over `steps` steps, the last of them cut short if
-// `ragged`.  `smem` is the ring of 2 slots of T::kSlot; what op copies with
-// each step (its scales) it keeps itself.
-template <class T, class P, class Q, class Op>
-__device__ __forceinline__ void tile_loop(int steps, bool ragged, const P& p, const Q& q, const Op& op,
-                                          uint8_t* smem, int wave, f32x16_t (&acc)[T::FN][T::FM]) {
-  constexpr int kTiles = T::FN * T::FM, kAll = 2 * kTiles, kOps = T::FM + T::FN, kReads = 2 * kOps;
+// Computes a workgroup's tiles.  `work` has
+//   p, q, op      the tokens' and the weights' source and the instruction, set
+//                 to the tile that is copied;
+//   fetch(i)      sets them to the workgroup's tile i, returns its steps (0:
+//                 there is none);
+//   begin(i)      the tile that is computed: its steps (0: none); sets
+//   active        of T::FM fragments of rows, how many have any (at least 1);
+//   store(acc)    its outputs: acc[f][t] of rows of q (fragment f, the
+//                 accumulator's acc_row) and of p (fragment t, lane % 32).
+// `smem` is the ring of 2 slots of T::kSlot; what op copies it keeps itself.
+template <class T, class Work>
+__device__ __forceinline__ void tile_loop(Work& work, uint8_t* smem, int wave) {
+  using P = decltype(work.p);
+  using Q = decltype(work.q);
+  using Op = decltype(work.op);
+  constexpr int kOps = T::FM + T::FN, kReads = 2 * kOps;
   constexpr int kCopies = P::kCopies + Q::kCopies + Op::kCopies;
   struct Frags {
     i32x4_t m[2][T::FM], n[2][T::FN];  // two quarters
@@ -189,130 +268,159 @@ __device__ __forceinline__ void tile_loop(int steps, bool ragged, const P& p, co
   Frags r0, r1;
   typename Op::Scales sc, sc_next;
   const uint32_t lds = lds_addr(smem) + wave * 1024;
-  auto copy = [&](auto tail, int step, int c) __attribute__((always_inline)) {
-    const uint32_t to = lds + (step & 1) * T::kSlot;
-    if (c < P::kCopies)
-      p.template copy<decltype(tail)::value>(step, c, to);
-    else if (c < P::kCopies + Q::kCopies)
-      q.template copy<decltype(tail)::value>(step, c - P::kCopies, to + T::kM);
-    else
-      op.copy(step, c - P::kCopies - Q::kCopies);
+
+  // What is copied next: a step of a tile of the workgroup's.
+  int tile = 0, step = 0, steps = work.fetch(0);
+  if (steps == 0) return;
+  auto start = [&](int ring) __attribute__((always_inline)) {
+    work.p.start(step);
+    work.q.start(step);
+    work.op.start(step, ring);
   };
-  auto copy_all = [&](int step) __attribute__((always_inline)) {
-    if (ragged && step == steps - 1) {
-#pragma unroll
-      for (int c = 0; c < kCopies; ++c) copy(std::true_type{}, step, c);
-    } else {
-#pragma unroll
-      for (int c = 0; c < kCopies; ++c) copy(std::false_type{}, step, c);
+  auto copy = [&](int ring, int c) __attribute__((always_inline)) {
+    const uint32_t to = lds + ring * T::kSlot;
+    if (c < P::kCopies)
+      work.p.copy(c, to);
+    else if (c < P::kCopies + Q::kCopies)
+      work.q.copy(c - P::kCopies, to + T::kM);
+    else
+      work.op.copy(c - P::kCopies - Q::kCopies);
+  };
+  auto advance = [&]() __attribute__((always_inline)) {
+    if (steps > 0 && ++step == steps) {
+      step = 0;
+      steps = work.fetch(++tile);
+      if (steps == 0) {  // what is copied from here on is not used
+        work.p.none();
+        work.q.none();
+      }
     }
   };
   auto read = [&](Frags& r, const uint8_t* slot, int half, int j) __attribute__((always_inline)) {
     const int part = j / kOps, o = j % kOps;
     if (o < T::FN)
-      r.n[part][o] = q.read(slot + T::kM, 2 * half + part, o);
+      r.n[part][o] = work.q.read(slot + T::kM, 2 * half + part, o);
     else
-      r.m[part][o - T::FN] = p.read(slot, 2 * half + part, o - T::FN);
-  };
-  // One half: its products, with the next half's reads over the first three
-  // quarters of them and a later step's copies between all of them.  The order
-  // is pinned.
-  auto half = [&](auto h, const Frags& now, Frags& next, const uint8_t* slot, int step) __attribute__((always_inline)) {
-    constexpr int H = decltype(h)::value;
-    // uniform: copies, none (past the last step), or those of the step that is cut short
-    const bool whole = step < steps - (int)ragged, cut = step == steps - 1;
-    constexpr int kOver = kAll * 3 / 4 > 0 ? kAll * 3 / 4 : 1;
-    static_for<kAll>([&](auto ic) __attribute__((always_inline)) {
-      constexpr int i = decltype(ic)::value, part = i / kTiles, t = i % kTiles / T::FN, f = i % T::FN;
-      acc[f][t] = op.template mul<2 * H + part, f, t>(now.n[part][f], now.m[part][t], acc[f][t], sc);
-      // A product has no side effect, so nothing else would keep it from moving
-      // behind the reads, the barrier and the copies that it is to run beside.
-      asm volatile("" : "+a"(acc[f][t]));
-      __builtin_amdgcn_sched_barrier(0);
-      // read j comes after product j kOver / kReads
-      constexpr int j0 = i < kOver ? (i * kReads + kOver - 1) / kOver : kReads;
-      constexpr int j1 = i + 1 < kOver ? ((i + 1) * kReads + kOver - 1) / kOver : kReads;
-      static_for<j1 - j0>([&](auto j) __attribute__((always_inline)) { read(next, slot, 1 - H, j0 + decltype(j)::value); });
-      if constexpr (H == 1 && i == 0) op.read(step - 1, sc_next);
-      if constexpr (H == 1) {
-        constexpr int c0 = i * kCopies / kAll, c1 = (i + 1) * kCopies / kAll;
-        if constexpr (c1 > c0) {
-          auto some = [&](auto tail) __attribute__((always_inline)) {
-            static_for<c1 - c0>([&](auto c) __attribute__((always_inline)) { copy(tail, step, c0 + decltype(c)::value); });
-          };
-          if (whole)
-            some(std::false_type{});
-          else if (cut)
-            some(std::true_type{});
-        }
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    });
+      r.m[part][o - T::FN] = work.p.read(slot, 2 * half + part, o - T::FN);
   };
 
-  copy_all(0);
-  if (steps > 1) {
-    copy_all(1);
-    vm_wait<kCopies>();
-  } else {
-    vm_wait<0>();
+#pragma unroll
+  for (int ring = 0; ring < 2; ++ring) {
+    start(ring);
+#pragma unroll
+    for (int c = 0; c < kCopies; ++c) copy(ring, c);
+    advance();
   }
+  vm_wait<kCopies>();
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < kReads; ++j) read(r0, smem, 0, j);
-  op.read(0, sc);
-#pragma unroll 1
-  for (int s = 0; s < steps; ++s) {
-    half(std::integral_constant<int, 0>{}, r0, r1, smem + (s & 1) * T::kSlot, 0);
-    vm_wait<0>();      // this wave's copies for step s + 1 are there
-    __syncthreads();   // everyone's are, and everyone has read slot s
-    half(std::integral_constant<int, 1>{}, r1, r0, smem + ((s + 1) & 1) * T::kSlot, s + 2);
-    sc = sc_next;
-  }
-  // The accumulators stay where they are until each is read: without this the
-  // compiler moves all of them at once, which takes more registers than there are.
-#pragma unroll
-  for (int f = 0; f < T::FN; ++f)
-#pragma unroll
-    for (int t = 0; t < T::FM; ++t) asm volatile("" : "+a"(acc[f][t]));
-}
+  work.op.read(0, sc);
 
-// The wave's outputs as bf16 rows: row m of its part starts at out + m * ld,
-// T::FN * 32 outputs (HALF: half of them) of which
-// the first `cols` (a multiple of 8, may be 0 or less) and rows below `rows`
-// are stored.  They are turned round in the wave's own part of the LDS, so that
-// it stores whole rows; 16-byte chunk c of row r lies at c ^ (r % chunks).
-// value(f, t, i): the output of accumulator i of fragments f, t (HALF: i < 8).
-template <class T, bool HALF, class Value>
-__device__ __forceinline__ void store_rows(uint8_t* smem, int wave, int lane, uint16_t* out, int64_t ld, int64_t rows,
-                                           int64_t cols, Value value) {
-  constexpr int kQuads = HALF ? 2 : 4;  // groups of 8 outputs of a fragment
-  constexpr int kRow = T::FN * kQuads * 16, kPer = kRow / 16;
-  static_assert(4 * T::FM * 32 * kRow <= 2 * T::kSlot, "the waves' parts");
-  uint8_t* const mine = smem + wave * T::FM * 32 * kRow;
-  const int r = lane & 31, h = lane >> 5;
-#pragma unroll
-  for (int t = 0; t < T::FM; ++t) {
-    __builtin_amdgcn_sched_barrier(0);  // a fragment row at a time: its values out of the accumulators, no more
+  int ring = 0;  // slot of the step that is multiplied
+  // A tile with rows in the first A fragments of each wave.
+  auto run = [&](auto active, int n) __attribute__((always_inline)) {
+    constexpr int A = decltype(active)::value, kTiles = T::FN * A, kAll = 2 * kTiles;
+    f32x16_t acc[T::FN][A];
 #pragma unroll
     for (int f = 0; f < T::FN; ++f)
 #pragma unroll
-      for (int q = 0; q < kQuads; ++q) {
-        const int c = f * kQuads + q;
-        *(uint2*)(mine + (32 * t + r) * kRow + (c ^ (r % kPer)) * 16 + h * 8) =
-            make_uint2(pack_bf16(value(f, t, 4 * q), value(f, t, 4 * q + 1)),
-                       pack_bf16(value(f, t, 4 * q + 2), value(f, t, 4 * q + 3)));
-      }
+      for (int t = 0; t < A; ++t) acc[f][t] = f32x16_t{};
+    // One half: its products, with the next half's reads over the first three
+    // quarters of them and, in the second, a later step's copies between all of
+    // them.  The order is pinned.
+    auto half = [&](auto h, const Frags& now, Frags& next, const uint8_t* slot) __attribute__((always_inline)) {
+      constexpr int H = decltype(h)::value;
+      constexpr int kOver = kAll * 3 / 4 > 0 ? kAll * 3 / 4 : 1;
+      static_for<kAll>([&](auto ic) __attribute__((always_inline)) {
+        constexpr int i = decltype(ic)::value, part = i / kTiles, t = i % kTiles / T::FN, f = i % T::FN;
+        acc[f][t] = work.op.template mul<2 * H + part, f, t>(now.n[part][f], now.m[part][t], acc[f][t], sc);
+        // A product has no side effect, so nothing else would keep it from moving
+        // behind the reads, the barrier and the copies that it is to run beside.
+        asm volatile("" : "+a"(acc[f][t]));
+        __builtin_amdgcn_sched_barrier(0);
+        // read j comes after product j kOver / kReads
+        constexpr int j0 = i < kOver ? (i * kReads + kOver - 1) / kOver : kReads;
+        constexpr int j1 = i + 1 < kOver ? ((i + 1) * kReads + kOver - 1) / kOver : kReads;
+        static_for<j1 - j0>([&](auto j) __attribute__((always_inline)) { read(next, slot, 1 - H, j0 + decltype(j)::value); });
+        if constexpr (H == 1) {
+          if constexpr (i == 0) {
+            work.op.read(ring ^ 1, sc_next);
+            start(ring);
+          }
+          constexpr int c0 = i * kCopies / kAll, c1 = (i + 1) * kCopies / kAll;
+          static_for<c1 - c0>([&](auto c) __attribute__((always_inline)) { copy(ring, c0 + decltype(c)::value); });
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    };
+#pragma unroll 1
+    do {
+      half(std::integral_constant<int, 0>{}, r0, r1, smem + ring * T::kSlot);
+      vm_wait<0>();     // this wave's copies for the next step are there
+      __syncthreads();  // everyone's are, and everyone has read this slot
+      half(std::integral_constant<int, 1>{}, r1, r0, smem + (ring ^ 1) * T::kSlot);
+      sc = sc_next;
+      ring ^= 1;
+      advance();
+    } while (--n > 0);
+    work.template store<A>(acc);
+  };
+#pragma unroll 1
+  for (int i = 0;; ++i) {
+    const int n = work.begin(i);
+    if (n == 0) break;
+    if constexpr (T::FM > 2) {
+      if (work.active > 3) run(std::integral_constant<int, 4>{}, n);
+      else if (work.active == 3) run(std::integral_constant<int, 3>{}, n);
+    }
+    if (T::FM <= 2 ? work.active > 1 : work.active == 2) run(std::integral_constant<int, 2>{}, n);
+    else if (work.active == 1) run(std::integral_constant<int, 1>{}, n);
   }
-  wave_sync();
-  constexpr int kAtOnce = 64 / kPer > 0 ? 64 / kPer : 1;
-  lane = here(threadIdx.x) & 63;  // what is derived of it starts here: the accumulators fill the registers above
-  const int c = lane % kPer;
-#pragma unroll 4
-  for (int i = 0; i < T::FM * 32 / kAtOnce; ++i) {
-    const int row = i * kAtOnce + lane / kPer;
-    const uint4 v = *(const uint4*)(mine + row * kRow + (c ^ row % kPer) * 16);
-    if (row < rows && c * 8 < cols) *(uint4*)(out + row * ld + c * 8) = v;
+  vm_wait<0>();  // no copy may land after the workgroup's LDS is released
+}
+
+// A fragment row's accumulators stay where they are up to here: without this the
+// compiler moves all of them at once, which takes more registers than there are.
+template <class T, int A>
+__device__ __forceinline__ void hold(f32x16_t (&acc)[T::FN][A], int t) {
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int f = 0; f < T::FN; ++f) asm volatile("" : "+a"(acc[f][t]));
+}
+
+// A tile's outputs, rows of `ld` bytes from its first on: stores past the last
+// row or the matrix's last column do nothing.
+struct TileOut {
+  __amdgpu_buffer_rsrc_t buffer;
+  uint32_t ld;
+  __device__ TileOut(const void* first, int64_t ld_bytes, int rows) : ld((uint32_t)ld_bytes) {
+    buffer = __builtin_amdgcn_make_buffer_rsrc((void*)uniform(first), 0, (int)((uint32_t)rows * ld), 0x00020000);
+  }
+  __device__ __forceinline__ void put(const u32x4& v, uint32_t off) const {
+    __builtin_amdgcn_raw_buffer_store_b128(v, buffer, off, 0, 0);
+  }
+};
+
+// Stores a fragment of 32 rows x 32 outputs as bf16 (of 16, for 2 `quads`): row
+// r, which is this lane's (lane % 32), at byte `off` of the tile, the first
+// `cols` (a multiple of 8) of its outputs.  A lane has 4 of every 8; the two
+// lanes of a row swap, so that each holds 8 in a row: the lower groups 0 and 2,
+// the upper 1 and 3.
+template <class Value>
+__device__ __forceinline__ void store_fragment(const TileOut& out, uint32_t off, int cols, int quads, Value value) {
+  const int h = (threadIdx.x >> 5) & 1;
+#pragma unroll
+  for (int q = 0; q < 4; q += 2) {
+    if (q >= quads) break;
+    uint32_t v[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) v[i][e] = pack_bf16(value(4 * (q + i) + 2 * e), value(4 * (q + i) + 2 * e + 1));
+    const auto lo = __builtin_amdgcn_permlane32_swap(v[0][0], v[1][0], false, false);
+    const auto hi = __builtin_amdgcn_permlane32_swap(v[0][1], v[1][1], false, false);
+    out.put(u32x4{lo[0], hi[0], lo[1], hi[1]}, 8 * (q + h) < cols ? off + 16 * (q + h) : kOutside);
   }
 }
 
