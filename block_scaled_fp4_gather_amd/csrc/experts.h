@@ -48,7 +48,6 @@ hipError_t launch_fp4_dequantize(const DequantArgs& a, hipStream_t st);
 // ---------------------------------------------------------------- routes
 
 constexpr int kGroupMaxExperts = 4096;
-constexpr int kProductMaxExperts = 2048;  // of the grouped products, whose tables are in LDS
 constexpr int64_t kGroupMaxRoutes = (int64_t)1 << 22;
 
 int64_t group_routes_workspace(int64_t routes, int E);

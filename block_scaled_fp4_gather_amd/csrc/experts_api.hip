@@ -125,7 +125,7 @@ moe_fp4_status grouped_shape(const moe_fp4_grouped_desc* d, int32_t rows) {
       d->out_features % 8 || rows < 0)
     return MOE_FP4_EINVAL;
   if (d->weight_layout != MOE_FP4_WEIGHT_OUT_IN && d->weight_layout != MOE_FP4_WEIGHT_IN_OUT) return MOE_FP4_EINVAL;
-  if (d->num_experts > moe::kProductMaxExperts || d->in_features > kMaxCols || d->out_features > kMaxCols ||
+  if (d->num_experts > moe::kGroupMaxExperts || d->in_features > kMaxCols || d->out_features > kMaxCols ||
       rows > moe::kGroupMaxRoutes)
     return MOE_FP4_EUNSUPPORTED;
   return MOE_FP4_OK;

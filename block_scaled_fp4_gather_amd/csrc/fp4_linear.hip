@@ -309,7 +309,6 @@ struct PackSource {
     buffer = buffer_of(uniform(p + sub0 * kb * 1024 + mine), all > 0 ? (uint32_t)all : 0u);
     stride = __builtin_amdgcn_readfirstlane(2 * kb * 1024);
   }
-  __device__ void none() { buffer[2] = 0; }
   __device__ __forceinline__ void start(int step) {
     now = scalar(buffer);
     soff = (uint32_t)__builtin_amdgcn_readfirstlane(step * 2048);
@@ -385,7 +384,7 @@ struct Fp4Op {
 };
 
 template <class T>
-constexpr int kFp4Lds = 2 * T::kSlot + 2 * Fp4Op<T>::kRing;
+constexpr int kFp4Lds = T::kRing + 2 * Fp4Op<T>::kRing;
 
 struct TileArgs {
   Fp4Shape s;
@@ -401,14 +400,15 @@ struct LinearWork {
   PackSource<T::BM, T::WM> p;
   PackSource<T::BN, 1> q;
   Fp4Op<T> op;
-  int active;
 
   Places places;
   int lane, wave, wm, wn;
   Parked row0, col0;  // of the tile that is computed
 
-  __device__ LinearWork(const Places& tiles, uint8_t* ring, int w)
-      : places(tiles), lane(threadIdx.x & 63), wave(w), wm(w % T::WM), wn(w / T::WM) {
+  enum { kM, kN, kSteps };
+
+  __device__ LinearWork(uint8_t* ring, int w)
+      : lane(threadIdx.x & 63), wave(w), wm(w % T::WM), wn(w / T::WM) {
     p.lanes(wm, wave, lane);
     q.lanes(wn * T::FN, wave, lane);
     op.lanes(ring, wm, wn, wave, lane);
@@ -428,34 +428,44 @@ struct LinearWork {
     m = 4 * band + in_band % bm;
     return true;
   }
-  __device__ int fetch(int i) {
-    int m, n;
-    if (!locate(i, m, n)) {
-      places.put(i, make_int4(0, 0, 0, 0));
-      return 0;
-    }
+  __device__ static Fp4Shape shape() {
     const auto& a = kernel_args<TileArgs>();
-    places.put(i, make_int4(m * T::BM, n * T::BN, min(T::FM, (a.M - m * T::BM + 32 * T::WM - 1) / (32 * T::WM)),
-                            (a.s.K + 255) / 256));
     Fp4Shape s;
     s.K = a.s.K;
     s.N = a.s.N;
     s.gated = GATED;
-    const int kb = s.kblocks(), ns = s.subtiles();
-    const int64_t groups = ((int64_t)a.M + 15) / 16;
-    p.set(a.packed, kb, (int64_t)m * (T::BM / 16), groups);
-    q.set(a.prepared, kb, (int64_t)n * (T::BN / 16), ns);
-    op.set(a.pscales, Fp4Shape::pair_cols(groups), (int64_t)m * (T::BM / 32), a.prepared + s.codes_bytes(ns),
-           Fp4Shape::pair_cols(ns), (int64_t)n * (T::BN / 32), wave);
-    return s.ksteps();
+    return s;
+  }
+  __device__ int steps(int i) const { return places.get(i, kSteps); }
+  __device__ int find(int i) {
+    int m, n;
+    if (!locate(i, m, n)) {
+      places.clear(i);
+      return 0;
+    }
+    places.put(i, kM, m);
+    places.put(i, kN, n);
+    places.put(i, kSteps, shape().ksteps());
+    return shape().ksteps();
+  }
+  __device__ void set_p(int i) {
+    const auto& a = kernel_args<TileArgs>();
+    p.set(a.packed, shape().kblocks(), (int64_t)places.get(i, kM) * (T::BM / 16), ((int64_t)a.M + 15) / 16);
+  }
+  __device__ void set_q(int i) {
+    const auto& a = kernel_args<TileArgs>();
+    const Fp4Shape s = shape();
+    const int ns = s.subtiles(), m = places.get(i, kM), n = places.get(i, kN);
+    q.set(a.prepared, s.kblocks(), (int64_t)n * (T::BN / 16), ns);
+    op.set(a.pscales, Fp4Shape::pair_cols(((int64_t)a.M + 15) / 16), (int64_t)m * (T::BM / 32),
+           a.prepared + s.codes_bytes(ns), Fp4Shape::pair_cols(ns), (int64_t)n * (T::BN / 32), wave);
   }
   __device__ int begin(int i) {
-    const int4 t = places.get(i);
-    row0 = t.x;
-    col0 = t.y;
-    active = t.z;
-    return t.w;
+    row0 = places.get(i, kM) * T::BM;
+    col0 = places.get(i, kN) * T::BN;
+    return min(T::FM, (kernel_args<TileArgs>().M - row0 + 32 * T::WM - 1) / (32 * T::WM));
   }
+  static constexpr int kStores = (GATED ? 1 : 2) * T::FN;
   template <int A>
   __device__ __forceinline__ void store(f32x16_t (&acc)[T::FN][A]) {
     const auto& a = kernel_args<TileArgs>();
@@ -495,8 +505,7 @@ template <class T, bool GATED>
 __global__ void __launch_bounds__(256, T::kPerCu) fp4_tile_kernel(TileArgs) {
   extern __shared__ __align__(16) uint8_t smem[];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  __shared__ int4 tiles[4][4];
-  LinearWork<T, GATED> work(Places{tiles[wave]}, smem + 2 * T::kSlot, wave);
+  LinearWork<T, GATED> work(smem + T::kRing, wave);
   tile_loop<T>(work, smem, wave);
 }
 
@@ -584,8 +593,8 @@ hipError_t launch_fp4_linear(const Fp4Shape& s, const uint8_t* prepared, const u
   auto rounds = [&](int bm, int bn) {
     return ((M + bm - 1) / bm * (int64_t)((s.subtiles() * 16 + bn - 1) / bn) + 255) / 256;
   };
-  if (20 * rounds(256, 256) <= 10 * rounds(128, 128)) return launch_tile<Tile<256, 256, 2, 2>>(s, prepared, t, M, out, st);
-  return launch_tile<Tile<128, 128, 2, 2>>(s, prepared, t, M, out, st);
+  if (20 * rounds(256, 256) <= 10 * rounds(128, 128)) return launch_tile<Tile<256, 256, 2, 2, 2>>(s, prepared, t, M, out, st);
+  return launch_tile<Tile<128, 128, 2, 2, 2>>(s, prepared, t, M, out, st);
 }
 
 }  // namespace moe

@@ -17,52 +17,8 @@ namespace {
 // Rows of expert e, whatever the offsets hold: within [0, rows] and not
 // negative in number.
 __device__ __forceinline__ void expert_rows(const int32_t* offsets, int e, int64_t rows, int& a, int& b) {
-  a = min(max(offsets[e], 0), (int)rows);
-  b = max(a, min(offsets[e + 1], (int)rows));
-}
-
-// In LDS, by the 4 waves: row tiles before expert e in start[e], e up to E, and
-// its first row and rows.
-struct Experts {
-  int* start;
-  int2* rows;
-};
-__device__ __forceinline__ void tile_starts(const int32_t* __restrict__ offsets, int E, int64_t rows, int bm,
-                                            const Experts& x) {
-  __shared__ int sums[4];
-  int* const start = x.start;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int per = (E + 255) / 256, e0 = min(E, (int)threadIdx.x * per), e1 = min(E, e0 + per);
-  int n = 0;
-  for (int e = e0; e < e1; ++e) {
-    int a, b;
-    expert_rows(offsets, e, rows, a, b);
-    start[e] = n;
-    x.rows[e] = make_int2(a, b - a);
-    n += (b - a + bm - 1) / bm;
-  }
-  int in = n;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int up = __shfl_up(in, d);
-    if (lane >= d) in += up;
-  }
-  if (lane == 63) sums[wave] = in;
-  __syncthreads();
-  int before = in - n;
-  for (int w = 0; w < wave; ++w) before += sums[w];
-  for (int e = e0; e < e1; ++e) start[e] += before;
-  if (threadIdx.x == 255) start[E] = before + n;
-  __syncthreads();
-}
-
-// The expert whose row tiles hold tile `at`: the last one that starts at or
-// before it.  Every wave looks by itself, 64 experts at a time.
-__device__ __forceinline__ int tile_expert(const int* start, int E, int at) {
-  const int lane = threadIdx.x & 63, per = (E + 63) / 64;
-  const int seg = __popcll(__ballot(lane * per < E && start[min(lane * per, E)] <= at)) - 1;
-  const int e = seg * per + lane;
-  return seg * per + __popcll(__ballot(lane < per && e < E && start[min(e, E)] <= at)) - 1;
+  a = min(max(constant(offsets + e), 0), (int)rows);
+  b = max(a, min(constant(offsets + e + 1), (int)rows));
 }
 
 // A workgroup's tile i among `total`: each XCD (workgroups are dealt to the 8 in
@@ -85,50 +41,101 @@ struct ForwardWork {
   RowSource<T::BM, T::WM> p;
   std::conditional_t<KN, ColSource<T::BN, 1>, RowSource<T::BN, 1>> q;
   Bf16Op op;
-  int active;
 
-  Experts x;
   Places places;
+  int total;      // tiles
+  int e, before;  // the expert of the tile that was found last, and the tiles before its
   int lane, wave, wm, wn;
   Parked row0, rows, n0;  // of the tile that is computed
+  enum { kRow, kRows, kCol, kExpert };
 
-  __device__ ForwardWork(const Experts& experts, const Places& ring, int w)
-      : x(experts), places(ring), lane(threadIdx.x & 63), wave(w), wm(w % T::WM), wn(w / T::WM) {
+  __device__ explicit ForwardWork(int w) : lane(threadIdx.x & 63), wave(w), wm(w % T::WM), wn(w / T::WM) {
     p.lanes(wm, wave, lane);
     q.lanes(wn * T::FN, wave, lane);
+    // The row tiles of all experts, 64 experts at a time, and the expert where
+    // this XCD's share of the tiles starts.
+    const auto& args = kernel_args<ForwardArgs>();
+    const auto& a = args.g;
+    const int32_t* const offsets = a.offsets;
+    const int E = a.E, R = (int)a.rows, tiles_n = args.tiles_n;
+    total = 0;
+    for (int e0 = 0; e0 < E; e0 += 64) total += __builtin_amdgcn_readlane(tiles_upto(offsets, E, R, e0), 63);
+    total *= tiles_n;
+    const int start = (int)(blockIdx.x % 8) * ((total + 7) / 8);
+    e = before = 0;
+    for (int e0 = 0; e0 < E; e0 += 64) {
+      const int upto = tiles_upto(offsets, E, R, e0), here = before + __builtin_amdgcn_readlane(upto, 63) * tiles_n;
+      if (here > start || e0 + 64 >= E) {  // the last expert that starts at or before it, of these 64
+        const uint64_t past = __ballot(before + upto * tiles_n <= start);
+        const int n = __popcll(past) < 63 ? __popcll(past) : 63;
+        e = min(e0 + n, E - 1);
+        before += n ? __builtin_amdgcn_readlane(upto, n - 1) * tiles_n : 0;
+        break;
+      }
+      before = here;
+    }
   }
-  __device__ int fetch(int i) {
+  // Inclusive sum over the lanes of the row tiles of expert e0 + lane.
+  __device__ static int tiles_upto(const int32_t* offsets, int E, int R, int e0) {
+    const int lane = threadIdx.x & 63, x = e0 + lane;
+    int n = 0;
+    if (x < E) {
+      const int a = min(max(offsets[x], 0), R), b = max(a, min(offsets[x + 1], R));
+      n = (b - a + T::BM - 1) / T::BM;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int up = __shfl_up(n, d);
+      if (lane >= d) n += up;
+    }
+    return n;
+  }
+  __device__ int steps(int i) const { return places.get(i, kRows) > 0 ? (kernel_args<ForwardArgs>().g.K + 63) / 64 : 0; }
+  __device__ int find(int i) {
     const auto& args = kernel_args<ForwardArgs>();
     const auto& a = args.g;
     const int tiles_n = args.tiles_n;
-    const int at = (int)tile_of((int64_t)__builtin_amdgcn_readfirstlane(x.start[a.E]) * tiles_n, i);
+    const int at = (int)tile_of(total, i);
     if (at < 0) {
-      places.put(i, make_int4(0, 0, 0, 0));
+      places.clear(i);
       return 0;
     }
-    const int e = tile_expert(x.start, a.E, at / tiles_n);
-    const int first = __builtin_amdgcn_readfirstlane(x.start[e]) * tiles_n;
-    const int r0 = __builtin_amdgcn_readfirstlane(x.rows[e].x), n = __builtin_amdgcn_readfirstlane(x.rows[e].y);
-    const int nt = (n + T::BM - 1) / T::BM;
-    const int tn = (at - first) / nt, tm = (at - first) - tn * nt;
-    const int row = r0 + tm * T::BM, count = min(T::BM, n - tm * T::BM), col = tn * T::BN;
-    places.put(i, make_int4(row, count, col, 0));
-    p.set(a.x + (int64_t)row * a.K, count, a.K);
-    const uint16_t* const w = a.w + (int64_t)e * a.N * a.K;
+    // tiles are found in order: from the last one's expert on
+    int r0, r1, nt;
+    for (;; ++e) {
+      expert_rows(a.offsets, e, a.rows, r0, r1);
+      nt = (r1 - r0 + T::BM - 1) / T::BM;
+      if (e + 1 >= a.E || before + nt * tiles_n > at) break;
+      before += nt * tiles_n;
+    }
+    const int tn = (at - before) / max(nt, 1), tm = (at - before) - tn * nt;
+    const int row = r0 + tm * T::BM;
+    places.put(i, kRow, row);
+    places.put(i, kRows, max(min(T::BM, r1 - row), 0));
+    places.put(i, kCol, tn * T::BN);
+    places.put(i, kExpert, e);
+    return steps(i);
+  }
+  __device__ void set_p(int i) {
+    const auto& a = kernel_args<ForwardArgs>().g;
+    p.set(a.x + (int64_t)places.get(i, kRow) * a.K, places.get(i, kRows), a.K);
+  }
+  __device__ void set_q(int i) {
+    const auto& a = kernel_args<ForwardArgs>().g;
+    const int col = places.get(i, kCol);
+    const uint16_t* const w = a.w + (int64_t)places.get(i, kExpert) * a.N * a.K;
     if constexpr (KN)
       q.set(w + col, 2 * a.N, a.K, a.N - col, lane);
     else
       q.set(w + (int64_t)col * a.K, a.N - col, a.K);
-    return p.steps();
   }
   __device__ int begin(int i) {
-    const int4 t = places.get(i);
-    row0 = t.x;
-    rows = t.y;
-    n0 = t.z;
-    active = (t.y + 32 * T::WM - 1) / (32 * T::WM);
-    return t.y > 0 ? p.steps() : 0;  // the same for every tile
+    row0 = places.get(i, kRow);
+    rows = places.get(i, kRows);
+    n0 = places.get(i, kCol);
+    return (rows + 32 * T::WM - 1) / (32 * T::WM);
   }
+  static constexpr int kStores = 2 * T::FN;
   template <int A>
   __device__ __forceinline__ void store(f32x16_t (&acc)[T::FN][A]) {
     const auto& a = kernel_args<ForwardArgs>().g;
@@ -146,13 +153,10 @@ struct ForwardWork {
 };
 
 template <class T, bool KN>
-__global__ void __launch_bounds__(256, T::kPerCu) grouped_tile_kernel(ForwardArgs args) {
+__global__ void __launch_bounds__(256, T::kPerCu) grouped_tile_kernel(ForwardArgs) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int4 ring[4][4];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Experts x{(int*)(smem + 2 * T::kSlot) + 2 * args.g.E, (int2*)(smem + 2 * T::kSlot)};
-  tile_starts(args.g.offsets, args.g.E, args.g.rows, T::BM, x);
-  ForwardWork<T, KN> work(x, Places{ring[wave]}, wave);
+  ForwardWork<T, KN> work(wave);
   tile_loop<T>(work, smem, wave);
   const auto& a = kernel_args<ForwardArgs>().g;
   // rows of no expert: before the first expert's and after the last one's
@@ -176,47 +180,57 @@ struct GradWork {
   ColSource<T::BM, T::WM> p;
   ColSource<T::BN, 1> q;
   Bf16Op op;
-  int active;
 
   Places places;
   int lane, wave, wm, wn;
   Parked e, n0, k0;  // of the tile that is computed
+  enum { kExpert, kN, kK, kSteps, kRow, kRows };
 
-  __device__ GradWork(const Places& ring, int w)
-      : places(ring), lane(threadIdx.x & 63), wave(w), wm(w % T::WM), wn(w / T::WM) {
+  __device__ explicit GradWork(int w) : lane(threadIdx.x & 63), wave(w), wm(w % T::WM), wn(w / T::WM) {
     p.lanes(wm, wave, lane);
     q.lanes(wn * T::FN, wave, lane);
   }
-  __device__ int fetch(int i) {
+  __device__ int steps(int i) const { return places.get(i, kSteps); }
+  __device__ int find(int i) {
     const auto& args = kernel_args<GradArgs>();
     const auto& a = args.g;
     const int tiles_n = args.tiles_n, tiles_k = args.tiles_k;
     const int64_t each = (int64_t)tiles_n * tiles_k, at = tile_of(each * a.E, i);
     if (at < 0) {
-      places.put(i, make_int4(0, 0, 0, 0));
+      places.clear(i);
       return 0;
     }
     const int expert = (int)(at / each);
     const int local = (int)(at - expert * each);
     const int band = local / (4 * tiles_k), in_band = local - band * 4 * tiles_k;
     const int bm = min(4, tiles_n - 4 * band);
-    const int n = (4 * band + in_band % bm) * T::BM, k = in_band / bm * T::BN;
     int r0, r1;
     expert_rows(a.offsets, expert, a.rows, r0, r1);
-    const int steps = r1 > r0 ? (r1 - r0 + 63) / 64 : 1;
-    places.put(i, make_int4(expert, n, k, steps));
-    p.set(a.dy + (int64_t)r0 * a.N + n, 2 * a.N, r1 - r0, a.N - n, lane);
-    q.set(a.x + (int64_t)r0 * a.K + k, 2 * a.K, r1 - r0, a.K - k, lane);
-    return steps;
+    places.put(i, kExpert, expert);
+    places.put(i, kN, (4 * band + in_band % bm) * T::BM);
+    places.put(i, kK, in_band / bm * T::BN);
+    places.put(i, kSteps, r1 > r0 ? (r1 - r0 + 63) / 64 : 1);
+    places.put(i, kRow, r0);
+    places.put(i, kRows, r1 - r0);
+    return steps(i);
+  }
+  __device__ void set_p(int i) {
+    const auto& a = kernel_args<GradArgs>().g;
+    const int n = places.get(i, kN);
+    p.set(a.dy + (int64_t)places.get(i, kRow) * a.N + n, 2 * a.N, places.get(i, kRows), a.N - n, lane);
+  }
+  __device__ void set_q(int i) {
+    const auto& a = kernel_args<GradArgs>().g;
+    const int k = places.get(i, kK);
+    q.set(a.x + (int64_t)places.get(i, kRow) * a.K + k, 2 * a.K, places.get(i, kRows), a.K - k, lane);
   }
   __device__ int begin(int i) {
-    const int4 t = places.get(i);
-    e = t.x;
-    n0 = t.y;
-    k0 = t.z;
-    active = min(T::FM, (kernel_args<GradArgs>().g.N - t.y + 32 * T::WM - 1) / (32 * T::WM));
-    return t.w;
+    e = places.get(i, kExpert);
+    n0 = places.get(i, kN);
+    k0 = places.get(i, kK);
+    return min(T::FM, (kernel_args<GradArgs>().g.N - n0 + 32 * T::WM - 1) / (32 * T::WM));
   }
+  static constexpr int kStores = (F32 ? 4 : 2) * T::FN;
   template <int A>
   __device__ __forceinline__ void store(f32x16_t (&acc)[T::FN][A]) {
     const auto& a = kernel_args<GradArgs>().g;
@@ -249,8 +263,7 @@ template <class T, bool F32>
 __global__ void __launch_bounds__(256, T::kPerCu) grouped_grad_kernel(GradArgs) {
   extern __shared__ __align__(16) uint8_t smem[];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  __shared__ int4 ring[4][4];
-  GradWork<T, F32> work(Places{ring[wave]}, wave);
+  GradWork<T, F32> work(wave);
   tile_loop<T>(work, smem, wave);
 }
 
@@ -266,11 +279,10 @@ hipError_t tiles(const GroupedArgs& a, hipStream_t st) {
   const int tn = (int)ceil_div(a.N, T::BN);
   // at most one partial row tile per expert beyond the whole ones; one workgroup for the rows of no expert
   const dim3 grid(grid_of<T>((a.rows / T::BM + (a.E < a.rows ? a.E : a.rows)) * tn + 1));
-  const unsigned lds = 2 * T::kSlot + 12 * a.E + 4;
   if (a.w_kn)
-    hipLaunchKernelGGL((grouped_tile_kernel<T, true>), grid, dim3(256), lds, st, ForwardArgs{a, tn});
+    hipLaunchKernelGGL((grouped_tile_kernel<T, true>), grid, dim3(256), T::kRing, st, ForwardArgs{a, tn});
   else
-    hipLaunchKernelGGL((grouped_tile_kernel<T, false>), grid, dim3(256), lds, st, ForwardArgs{a, tn});
+    hipLaunchKernelGGL((grouped_tile_kernel<T, false>), grid, dim3(256), T::kRing, st, ForwardArgs{a, tn});
   return hipGetLastError();
 }
 
@@ -279,14 +291,14 @@ hipError_t grads(const GroupedGradArgs& a, hipStream_t st) {
   const int tn = (int)ceil_div(a.N, T::BM), tk = (int)ceil_div(a.K, T::BN);
   const dim3 grid(grid_of<T>((int64_t)a.E * tn * tk));
   if (a.f32)
-    hipLaunchKernelGGL((grouped_grad_kernel<T, true>), grid, dim3(256), 2 * T::kSlot, st, GradArgs{a, tn, tk});
+    hipLaunchKernelGGL((grouped_grad_kernel<T, true>), grid, dim3(256), T::kRing, st, GradArgs{a, tn, tk});
   else
-    hipLaunchKernelGGL((grouped_grad_kernel<T, false>), grid, dim3(256), 2 * T::kSlot, st, GradArgs{a, tn, tk});
+    hipLaunchKernelGGL((grouped_grad_kernel<T, false>), grid, dim3(256), T::kRing, st, GradArgs{a, tn, tk});
   return hipGetLastError();
 }
 
-using Large = Tile<256, 256, 2, 2>;
-using Small = Tile<128, 128, 2, 2>;
+using Large = Tile<256, 256, 2, 2, 3>;
+using Small = Tile<128, 128, 2, 2, 3>;
 
 }  // namespace
 

@@ -4,17 +4,19 @@
 // operands are 32 bytes of a row: 16 bf16 or 64 E2M1 values, 16 bytes a lane.  A
 // step is 128 bytes of the contraction, two halves of two such quarters.
 //
-// Both operands come to LDS by direct copies, in a ring of two slots, and from
-// there to registers half a step before they are multiplied:
+// Both operands come to LDS by direct copies, in rings of two slots and of QS,
+// and from there to registers half a step before they are multiplied:
 //   half 0 of step s   multiply half 0; read half 1
-//   barrier            slot s is read, and the copies for step s + 1 are there
-//   half 1             multiply half 1; copy step s + 2 over slot s; read half
-//                      0 of step s + 1
-// so that a copy has a whole step (2048 cycles of the matrix cores at 256 x
-// 256) and an LDS read half of one to arrive, with one barrier a step.  The
-// steps of a tile and those of the next follow each other without a gap: what
-// is copied runs two steps ahead of what is multiplied, across tiles, and the
-// outputs go from the accumulators to memory beside it.
+//   barrier            the slots of step s are read, and step s + 1 is there
+//   half 1             multiply half 1; copy steps s + 2 and s + QS over those of
+//                      step s; read half 0 of step s + 1
+// so that a copy has a step (2048 cycles of the matrix cores at 256 x 256) to
+// arrive, or with three slots two: enough for the way from HBM, which an operand
+// takes that few tiles share (weights); the other one comes from the L2 mostly.
+// An LDS read has half a step, and there is one barrier a step.  The steps of a
+// tile and those of the next follow each other without a gap: what is copied
+// runs ahead of what is multiplied across tiles, and the outputs go from the
+// accumulators to memory beside it.
 // One wave per SIMD keeps its matrix core busy by itself; a wave's 128 x 128
 // outputs, which halve the LDS reads of 128 x 64, need 256 accumulators.
 // One wave issues a 16 x 16 instruction every 30 cycles or so, though bf16 and
@@ -49,13 +51,15 @@ __device__ __forceinline__ void static_for(F&& f) {
   static_for(std::make_integer_sequence<int, N>{}, f);
 }
 
-template <int BM_, int BN_, int WM_, int WN_>
+template <int BM_, int BN_, int WM_, int WN_, int QS_>
 struct Tile {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+  static constexpr int QS = QS_;  // slots of the second operand
   static constexpr int FM = BM / 32 / WM, FN = BN / 32 / WN;  // a wave's fragments of 32 rows
-  static constexpr int kM = BM * 128, kSlot = (BM + BN) * 128;
+  static constexpr int kM = BM * 128, kN = BN * 128;  // bytes of a slot
+  static constexpr int kRing = 2 * kM + QS * kN;
   // workgroups of a launch: as many as run at once on the 256 CUs, and of them on an XCD
-  static constexpr int kPerCu = kSlot <= 32768 ? 2 : 1, kGrid = 256 * kPerCu, kPerXcd = kGrid / 8;
+  static constexpr int kPerCu = kRing <= 81920 ? 2 : 1, kGrid = 256 * kPerCu;
   static_assert(WM * WN == 4 && BM % 32 == 0 && BN % 32 == 0 && FM > 0 && FN > 0, "4 waves, whole copies");
 };
 
@@ -99,19 +103,24 @@ struct Parked {
 };
 
 // What a workgroup's tiles are, from when they are first copied until they are
-// multiplied (up to 3 tiles later): each wave keeps them for itself in LDS.
+// multiplied (up to 4 tiles later): 8 numbers each, in the lanes of a register.
 struct Places {
-  int4* at;  // of the wave's: 4
-  __device__ __forceinline__ void put(int i, int4 v) const {
-    if ((threadIdx.x & 63) == 0) at[i & 3] = v;
-    wave_sync();
+  int lanes;
+  __device__ __forceinline__ void put(int i, int field, int v) {
+    lanes = (int)(threadIdx.x & 63) == i % 8 * 8 + field ? v : lanes;
   }
-  __device__ __forceinline__ int4 get(int i) const {
-    const int4 v = at[i & 3];
-    return make_int4(__builtin_amdgcn_readfirstlane(v.x), __builtin_amdgcn_readfirstlane(v.y),
-                     __builtin_amdgcn_readfirstlane(v.z), __builtin_amdgcn_readfirstlane(v.w));
+  __device__ __forceinline__ void clear(int i) { lanes = (int)(threadIdx.x & 63) / 8 == i % 8 ? 0 : lanes; }
+  __device__ __forceinline__ int get(int i, int field) const {
+    return __builtin_amdgcn_readlane(lanes, __builtin_amdgcn_readfirstlane(i % 8 * 8 + field));
   }
 };
+
+// Memory that no one writes while the kernel runs, read through the scalar
+// cache: a load among the copies would wait for all of those before it.
+template <class V>
+__device__ __forceinline__ V constant(const V* p) {
+  return *(const __attribute__((address_space(4))) V*)(uint64_t)p;
+}
 
 // A kernel's arguments (one struct) where they are used: read again each time, so
 // that the loop's scalar registers do not hold what a tile needs once.
@@ -149,8 +158,7 @@ struct RowSource {
     off = (uint32_t)row * bytes + chunk;
     last = (bytes & ~127u) + chunk < bytes ? off : kOutside;
   }
-  __device__ int steps() const { return (bytes + 127) / 128; }
-  __device__ void none() { buffer[2] = 0; }
+  __device__ static int steps_of(int k) { return (k + 63) / 64; }
   __device__ __forceinline__ void start(int step) {
     now = scalar(buffer);
     soff = (uint32_t)__builtin_amdgcn_readfirstlane(step * 128);
@@ -179,9 +187,9 @@ struct ColSource {
   static constexpr int kMask = kRow / 32 - 1;
   static constexpr int kSwaps = COLS == 256 ? 2 : 1;  // places of a lane's chunk: copies of 8 rows differ in k / 8 % 2
   static_assert(COLS == 256 || COLS == 128, "rows of a copy");
-  const uint8_t* base;     // of the next step
+  const uint8_t* base;
   uint32_t ld;             // bytes of a row
-  int rows;                // of the contraction, from the next step on
+  int rows;                // of the contraction
   i32x4_t buffer;
   uint32_t soff, gap;      // of the next copy; from one to the next
   int row;                 // this lane's row of copy 0
@@ -208,12 +216,9 @@ struct ColSource {
       off[c] = (uint32_t)row * ld +
                (uint32_t)min((lane % kLanes) ^ (swizzle(c * 4 * kRows + row) << 1), cols / 8 - 1) * 16;
   }
-  __device__ void none() { rows = 0; }
-  __device__ __forceinline__ void start(int) {
-    // the last row ends with the matrix's row, which starts before this column
-    buffer = scalar(buffer_of(base, rows > 0 ? (uint32_t)min(rows, 64) * ld : 0u));
-    base += (int64_t)64 * ld;
-    rows -= 64;
+  __device__ __forceinline__ void start(int step) {
+    const int left = rows - 64 * step;
+    buffer = scalar(buffer_of(base + (uint64_t)(uint32_t)(64 * step) * ld, left > 0 ? (uint32_t)min(left, 64) * ld : 0u));
     soff = 0;
     gap = (uint32_t)__builtin_amdgcn_readfirstlane((int)(4 * kRows * ld));
   }
@@ -246,22 +251,32 @@ struct Bf16Op {
 };
 
 // Computes a workgroup's tiles.  `work` has
-//   p, q, op      the tokens' and the weights' source and the instruction, set
-//                 to the tile that is copied;
-//   fetch(i)      sets them to the workgroup's tile i, returns its steps (0:
-//                 there is none);
-//   begin(i)      the tile that is computed: its steps (0: none); sets
-//   active        of T::FM fragments of rows, how many have any (at least 1);
+//   p, q, op      the sources of the first and the second operand, and the
+//                 instruction;
+//   find(i)       what the workgroup's tile i is, kept for the calls below; its
+//                 steps (0: there is none, and tile 0 of all is copied where one
+//                 has to be, and not used);
+//   steps(i)      the same;
+//   set_p(i), set_q(i)  sets p, and q with op, to tile i;
+//   begin(i)      tile i is computed; of T::FM fragments of p's rows, how many
+//                 have any (at least 1);
+//   kStores       stores of a fragment row, in
 //   store(acc)    its outputs: acc[f][t] of rows of q (fragment f, the
 //                 accumulator's acc_row) and of p (fragment t, lane % 32).
-// `smem` is the ring of 2 slots of T::kSlot; what op copies it keeps itself.
+// `smem` is the ring, T::kRing bytes; what op copies it keeps itself.
 template <class T, class Work>
 __device__ __forceinline__ void tile_loop(Work& work, uint8_t* smem, int wave) {
   using P = decltype(work.p);
   using Q = decltype(work.q);
   using Op = decltype(work.op);
+  static_assert(T::QS == 2 || (T::QS == 3 && Op::kCopies == 0), "two or three steps");
   constexpr int kOps = T::FM + T::FN, kReads = 2 * kOps;
   constexpr int kCopies = P::kCopies + Q::kCopies + Op::kCopies;
+  // Copies that may be on their way when a step's have to be there: with three
+  // slots those of the second operand for a later one, which come last.
+  constexpr int kLater = T::QS == 3 ? Q::kCopies : 0;
+  // Stores of a whole tile that may be too: a wave counts 63 operations.
+  constexpr int kFullStores = T::FM * Work::kStores + kLater < 60 ? T::FM * Work::kStores + kLater : 60;
   struct Frags {
     i32x4_t m[2][T::FM], n[2][T::FN];  // two quarters
   };
@@ -269,55 +284,65 @@ __device__ __forceinline__ void tile_loop(Work& work, uint8_t* smem, int wave) {
   typename Op::Scales sc, sc_next;
   const uint32_t lds = lds_addr(smem) + wave * 1024;
 
-  // What is copied next: a step of a tile of the workgroup's.
-  int tile = 0, step = 0, steps = work.fetch(0);
-  if (steps == 0) return;
-  auto start = [&](int ring) __attribute__((always_inline)) {
-    work.p.start(step);
-    work.q.start(step);
-    work.op.start(step, ring);
+  // What is copied next of each operand: a step of a tile of the workgroup's.
+  struct Cursor {
+    int tile, step, steps;
   };
-  auto copy = [&](int ring, int c) __attribute__((always_inline)) {
-    const uint32_t to = lds + ring * T::kSlot;
+  Cursor cp{0, 0, 0}, cq{0, 0, 0};
+  if ((cp.steps = cq.steps = work.find(0)) == 0) return;
+  work.set_p(0);
+  work.set_q(0);
+  auto advance_q = [&]() __attribute__((always_inline)) {
+    if (cq.steps > 0 && ++cq.step == cq.steps) {
+      cq.step = 0;
+      cq.steps = work.find(++cq.tile);
+      work.set_q(cq.tile);
+    }
+  };
+  auto advance_p = [&]() __attribute__((always_inline)) {
+    if (cp.steps > 0 && ++cp.step == cp.steps) {
+      cp.step = 0;
+      cp.steps = work.steps(++cp.tile);
+      work.set_p(cp.tile);
+    }
+  };
+  // Slots: of the step that is multiplied and the next, which is read.
+  int slot = 0, qslot = 0, qnext = 1;
+  auto area_p = [&](int s) __attribute__((always_inline)) { return smem + s * T::kM; };
+  auto area_q = [&](int s) __attribute__((always_inline)) { return smem + 2 * T::kM + s * T::kN; };
+  // Copy c into slots s and t, the first operand's copies first.
+  auto copy = [&](int s, int t, int c) __attribute__((always_inline)) {
     if (c < P::kCopies)
-      work.p.copy(c, to);
+      work.p.copy(c, lds + s * T::kM);
     else if (c < P::kCopies + Q::kCopies)
-      work.q.copy(c - P::kCopies, to + T::kM);
+      work.q.copy(c - P::kCopies, lds + 2 * T::kM + t * T::kN);
     else
       work.op.copy(c - P::kCopies - Q::kCopies);
   };
-  auto advance = [&]() __attribute__((always_inline)) {
-    if (steps > 0 && ++step == steps) {
-      step = 0;
-      steps = work.fetch(++tile);
-      if (steps == 0) {  // what is copied from here on is not used
-        work.p.none();
-        work.q.none();
-      }
-    }
-  };
-  auto read = [&](Frags& r, const uint8_t* slot, int half, int j) __attribute__((always_inline)) {
+  auto read = [&](Frags& r, const uint8_t* ap, const uint8_t* aq, int half, int j) __attribute__((always_inline)) {
     const int part = j / kOps, o = j % kOps;
     if (o < T::FN)
-      r.n[part][o] = work.q.read(slot + T::kM, 2 * half + part, o);
+      r.n[part][o] = work.q.read(aq, 2 * half + part, o);
     else
-      r.m[part][o - T::FN] = work.p.read(slot, 2 * half + part, o - T::FN);
+      r.m[part][o - T::FN] = work.p.read(ap, 2 * half + part, o - T::FN);
   };
 
-#pragma unroll
-  for (int ring = 0; ring < 2; ++ring) {
-    start(ring);
-#pragma unroll
-    for (int c = 0; c < kCopies; ++c) copy(ring, c);
-    advance();
-  }
-  vm_wait<kCopies>();
+  static_for<T::QS>([&](auto sc) __attribute__((always_inline)) {
+    constexpr int s = decltype(sc)::value, c0 = s < 2 ? 0 : P::kCopies;
+    if constexpr (s < 2) work.p.start(cp.step);
+    work.q.start(cq.step);
+    work.op.start(cq.step, s);
+    static_for<kCopies - c0>([&](auto c) __attribute__((always_inline)) { copy(s, s, c0 + decltype(c)::value); });
+    advance_q();
+    if constexpr (s < 2) advance_p();
+  });
+  vm_wait<kCopies + kLater>();
   __syncthreads();
 #pragma unroll
-  for (int j = 0; j < kReads; ++j) read(r0, smem, 0, j);
+  for (int j = 0; j < kReads; ++j) read(r0, area_p(0), area_q(0), 0, j);
   work.op.read(0, sc);
 
-  int ring = 0;  // slot of the step that is multiplied
+  int stored = 0;  // fragment rows that the tile before stored
   // A tile with rows in the first A fragments of each wave.
   auto run = [&](auto active, int n) __attribute__((always_inline)) {
     constexpr int A = decltype(active)::value, kTiles = T::FN * A, kAll = 2 * kTiles;
@@ -329,7 +354,8 @@ __device__ __forceinline__ void tile_loop(Work& work, uint8_t* smem, int wave) {
     // One half: its products, with the next half's reads over the first three
     // quarters of them and, in the second, a later step's copies between all of
     // them.  The order is pinned.
-    auto half = [&](auto h, const Frags& now, Frags& next, const uint8_t* slot) __attribute__((always_inline)) {
+    auto half = [&](auto h, const Frags& now, Frags& next, const uint8_t* ap, const uint8_t* aq)
+                    __attribute__((always_inline)) {
       constexpr int H = decltype(h)::value;
       constexpr int kOver = kAll * 3 / 4 > 0 ? kAll * 3 / 4 : 1;
       static_for<kAll>([&](auto ic) __attribute__((always_inline)) {
@@ -342,40 +368,57 @@ __device__ __forceinline__ void tile_loop(Work& work, uint8_t* smem, int wave) {
         // read j comes after product j kOver / kReads
         constexpr int j0 = i < kOver ? (i * kReads + kOver - 1) / kOver : kReads;
         constexpr int j1 = i + 1 < kOver ? ((i + 1) * kReads + kOver - 1) / kOver : kReads;
-        static_for<j1 - j0>([&](auto j) __attribute__((always_inline)) { read(next, slot, 1 - H, j0 + decltype(j)::value); });
+        static_for<j1 - j0>([&](auto j) __attribute__((always_inline)) {
+          read(next, ap, aq, 1 - H, j0 + decltype(j)::value);
+        });
         if constexpr (H == 1) {
           if constexpr (i == 0) {
-            work.op.read(ring ^ 1, sc_next);
-            start(ring);
+            work.op.read(slot ^ 1, sc_next);
+            work.p.start(cp.step);
+            work.q.start(cq.step);
+            work.op.start(cq.step, slot);
           }
           constexpr int c0 = i * kCopies / kAll, c1 = (i + 1) * kCopies / kAll;
-          static_for<c1 - c0>([&](auto c) __attribute__((always_inline)) { copy(ring, c0 + decltype(c)::value); });
+          static_for<c1 - c0>([&](auto c) __attribute__((always_inline)) { copy(slot, qslot, c0 + decltype(c)::value); });
         }
         __builtin_amdgcn_sched_barrier(0);
       });
     };
 #pragma unroll 1
     do {
-      half(std::integral_constant<int, 0>{}, r0, r1, smem + ring * T::kSlot);
-      vm_wait<0>();     // this wave's copies for the next step are there
-      __syncthreads();  // everyone's are, and everyone has read this slot
-      half(std::integral_constant<int, 1>{}, r1, r0, smem + (ring ^ 1) * T::kSlot);
+      half(std::integral_constant<int, 0>{}, r0, r1, area_p(slot), area_q(qslot));
+      // This wave's copies for the next step are there; in a tile's first step the
+      // stores of the one before, which came after them, may not be.
+      if (stored == T::FM)
+        vm_wait<kFullStores>();
+      else if (stored > 0)
+        vm_wait<Work::kStores + kLater>();
+      else
+        vm_wait<kLater>();
+      stored = 0;
+      __syncthreads();  // everyone's are, and everyone has read these slots
+      half(std::integral_constant<int, 1>{}, r1, r0, area_p(slot ^ 1), area_q(qnext));
       sc = sc_next;
-      ring ^= 1;
-      advance();
+      slot ^= 1;
+      qslot = qnext;
+      qnext = qnext + 1 == T::QS ? 0 : qnext + 1;
+      advance_q();
+      advance_p();
     } while (--n > 0);
     work.template store<A>(acc);
+    stored = A;
   };
 #pragma unroll 1
   for (int i = 0;; ++i) {
-    const int n = work.begin(i);
+    const int n = work.steps(i);
     if (n == 0) break;
+    const int active = work.begin(i);
     if constexpr (T::FM > 2) {
-      if (work.active > 3) run(std::integral_constant<int, 4>{}, n);
-      else if (work.active == 3) run(std::integral_constant<int, 3>{}, n);
+      if (active > 3) run(std::integral_constant<int, 4>{}, n);
+      else if (active == 3) run(std::integral_constant<int, 3>{}, n);
     }
-    if (T::FM <= 2 ? work.active > 1 : work.active == 2) run(std::integral_constant<int, 2>{}, n);
-    else if (work.active == 1) run(std::integral_constant<int, 1>{}, n);
+    if (T::FM <= 2 ? active > 1 : active == 2) run(std::integral_constant<int, 2>{}, n);
+    else if (active == 1) run(std::integral_constant<int, 1>{}, n);
   }
   vm_wait<0>();  // no copy may land after the workgroup's LDS is released
 }

@@ -604,7 +604,7 @@ typedef enum {
  * rows but no access out of range.  Rows of no expert (before offsets[0], from
  * offsets[E] on) are set to zeros. */
 typedef struct {
-  int32_t num_experts;   /* E, at most 2048 */
+  int32_t num_experts;   /* E, at most 4096 */
   int32_t in_features;   /* K, a multiple of 8, at most 2^20 */
   int32_t out_features;  /* N, a multiple of 8, at most 2^20 */
   int32_t weight_layout; /* moe_fp4_weight_layout */

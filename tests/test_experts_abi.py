@@ -145,7 +145,7 @@ def test_grouped_rejects_before_launch(L):
                dict(rows=-1), dict(x=None), dict(w=None), dict(offsets=None), dict(y=None), dict(x=A + 8),
                dict(offsets=C + 2), dict(y=A), dict(y=B), dict(y=C), dict(w=B + 8)):
         assert call(**kw) == EINVAL, kw
-    assert call(d=desc(E=2049)) == EUNSUPPORTED and call(rows=(1 << 22) + 1) == EUNSUPPORTED
+    assert call(d=desc(E=4097)) == EUNSUPPORTED and call(rows=(1 << 22) + 1) == EUNSUPPORTED
     assert call(d=desc(K=(1 << 20) + 8)) == EUNSUPPORTED and call(d=desc(N=(1 << 20) + 8)) == EUNSUPPORTED
     call = caller(L.moe_fp4_grouped_weight_grad, dict(d=desc(), type=0, dy=A, x=B, rows=10, offsets=C, dw=D))
     for kw in (dict(type=2), dict(d=desc(layout=1)), dict(dy=None), dict(x=None), dict(offsets=None), dict(dw=None),
