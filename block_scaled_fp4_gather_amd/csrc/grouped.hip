@@ -168,6 +168,156 @@ __global__ void __launch_bounds__(256, T::kPerCu) grouped_tile_kernel(ForwardArg
   }
 }
 
+// ---- few rows per expert: what bounds it is the weights, read once
+
+// Row tile `at` of BM rows: its expert, first row and rows (0: there is none).
+// Each wave looks by itself: lane l sums the tiles of `per` consecutive experts.
+struct RowTile {
+  int e, row0, rows;
+};
+__device__ __forceinline__ RowTile row_tile(const int32_t* __restrict__ offsets, int E, int R, int bm, int at) {
+  const int lane = threadIdx.x & 63;
+  const int per = (E + 63) / 64, e0 = min(E, lane * per), e1 = min(E, e0 + per);
+  int n = 0;
+  for (int e = e0; e < e1; ++e) {
+    const int a = min(max(offsets[e], 0), R), b = max(a, min(offsets[e + 1], R));
+    n += (b - a + bm - 1) / bm;
+  }
+  int in = n;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int up = __shfl_up(in, d);
+    if (lane >= d) in += up;
+  }
+  const uint64_t past = __ballot(in > at);
+  if (past == 0) return RowTile{0, 0, 0};
+  RowTile t{0, 0, 0};
+  int before = in - n;
+  for (int e = e0; e < e1; ++e) {
+    const int a = min(max(offsets[e], 0), R), b = max(a, min(offsets[e + 1], R));
+    const int nt = (b - a + bm - 1) / bm;
+    if (before <= at && at < before + nt) {
+      t.e = e;
+      t.row0 = a + (at - before) * bm;
+      t.rows = min(bm, b - t.row0);
+    }
+    before += nt;
+  }
+  const int owner = __builtin_ctzll(past);
+  return RowTile{__builtin_amdgcn_readlane(t.e, owner), __builtin_amdgcn_readlane(t.row0, owner),
+                 __builtin_amdgcn_readlane(t.rows, owner)};
+}
+
+// 16 FS features x 16 TT rows per workgroup, whose NW waves share K in runs of
+// blocks of 64 and join their sums in LDS in wave order; a wave has U blocks in
+// flight.  Weights are read as they lie: a lane takes chunk g and then chunk 4 +
+// g of its row's 128 bytes of a block, so that two loads take whole lines, and
+// the rows of x the same, which is all that the instruction asks for: their
+// contraction in the same order.  The workgroups of the last row tile clear the
+// rows of no expert.
+template <int FS, int TT, int NW, int U>
+__global__ void __launch_bounds__(NW * 64) grouped_few_kernel(GroupedArgs a) {
+  __shared__ f32x4_t part[NW][FS * TT][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4, R = (int)a.rows, n0 = blockIdx.x * (16 * FS);
+  const RowTile t = row_tile(a.offsets, a.E, R, 16 * TT, blockIdx.y);
+  if (blockIdx.y + 1 == gridDim.y) {
+    const int d0 = min(max(a.offsets[0], 0), R), d1 = max(d0, min(a.offsets[a.E], R));
+    for (int i = threadIdx.x; i < (d0 + R - d1) * 2 * FS; i += NW * 64) {
+      const int d = i / (2 * FS), row = d < d0 ? d : d1 + (d - d0), n = n0 + i % (2 * FS) * 8;
+      if (n < a.N) *(uint4*)(a.y + (int64_t)row * a.N + n) = make_uint4(0, 0, 0, 0);
+    }
+  }
+  if (t.rows <= 0) return;
+  const int blocks = (a.K + 63) / 64, per = (blocks + NW - 1) / NW, b0 = wave * per, b1 = min(blocks, b0 + per);
+  const uint16_t* w[FS];
+  const uint16_t* x[TT];
+#pragma unroll
+  for (int f = 0; f < FS; ++f) w[f] = a.w + ((int64_t)t.e * a.N + min(n0 + 16 * f + r, a.N - 1)) * a.K;
+#pragma unroll
+  for (int i = 0; i < TT; ++i) x[i] = a.x + (int64_t)(t.row0 + min(16 * i + r, t.rows - 1)) * a.K;
+  struct Operands {
+    i32x4_t w[U][FS][2], x[U][TT][2];
+  };
+  auto load = [&](int b, Operands& o) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        // blocks past the run and chunks past K are read in their place, and not multiplied or zero
+        const int k = min(min(b + u, blocks - 1) * 64 + 32 * h + 8 * g, a.K - 8);
+#pragma unroll
+        for (int f = 0; f < FS; ++f) o.w[u][f][h] = __builtin_nontemporal_load((const i32x4_t*)(w[f] + k));
+#pragma unroll
+        for (int i = 0; i < TT; ++i) o.x[u][i][h] = *(const i32x4_t*)(x[i] + k);
+      }
+  };
+  f32x4_t acc[FS][TT];
+#pragma unroll
+  for (int f = 0; f < FS; ++f)
+#pragma unroll
+    for (int i = 0; i < TT; ++i) acc[f][i] = f32x4_t{};
+  auto multiply = [&](int b, Operands& o) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (b + u >= b1) break;  // uniform
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if ((b + u) * 64 + 32 * h + 32 > a.K) {  // uniform: the last chunks
+          const bool in = (b + u) * 64 + 32 * h + 8 * g < a.K;
+#pragma unroll
+          for (int f = 0; f < FS; ++f) o.w[u][f][h] = in ? o.w[u][f][h] : i32x4_t{};
+#pragma unroll
+          for (int i = 0; i < TT; ++i) o.x[u][i][h] = in ? o.x[u][i][h] : i32x4_t{};
+        }
+#pragma unroll
+        for (int f = 0; f < FS; ++f)
+#pragma unroll
+          for (int i = 0; i < TT; ++i)
+            acc[f][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, o.w[u][f][h]),
+                                                                __builtin_bit_cast(bf16x8_t, o.x[u][i][h]), acc[f][i], 0, 0, 0);
+      }
+    }
+  };
+  // two sets of U blocks take turns
+  Operands o[2];
+  load(b0, o[0]);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll 1
+  for (int b = b0; b < b1; b += 2 * U) {
+    load(b + U, o[1]);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(b, o[0]);
+    __builtin_amdgcn_sched_barrier(0);
+    load(b + 2 * U, o[0]);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(b + U, o[1]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+#pragma unroll
+  for (int f = 0; f < FS; ++f)
+#pragma unroll
+    for (int i = 0; i < TT; ++i) part[wave][f * TT + i][lane] = acc[f][i];
+  __syncthreads();
+  for (int j = wave; j < FS * TT; j += NW) {
+    const int f = j / TT, i = j % TT;
+    f32x4_t v{};
+#pragma unroll
+    for (int q = 0; q < NW; ++q) v += part[q][j][lane];
+    const int n = n0 + 16 * f + 4 * g, row = 16 * i + r;
+    if (n < a.N && row < t.rows)  // N % 8 == 0: the lane's four outputs are all in or all out
+      *(uint2*)(a.y + (int64_t)(t.row0 + row) * a.N + n) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+  }
+}
+
+template <int FS, int TT, int NW, int U>
+hipError_t few(const GroupedArgs& a, hipStream_t st) {
+  const int64_t tm = a.rows / (16 * TT) + (a.E < a.rows ? a.E : a.rows);
+  hipLaunchKernelGGL((grouped_few_kernel<FS, TT, NW, U>), dim3((unsigned)((a.N + 16 * FS - 1) / (16 * FS)), (unsigned)tm),
+                     dim3(NW * 64), 0, st, a);
+  return hipGetLastError();
+}
+
 struct GradArgs {
   GroupedGradArgs g;
   int tiles_n, tiles_k;
@@ -303,6 +453,10 @@ using Small = Tile<128, 128, 2, 2, 3>;
 }  // namespace
 
 hipError_t launch_grouped(const GroupedArgs& a, hipStream_t st) {
+  if (!a.w_kn && a.rows <= 16ll * a.E && a.rows <= 32768) {
+    if (a.rows <= 8ll * a.E) return few<1, 1, 8, 4>(a, st);
+    return few<2, 2, 8, 2>(a, st);
+  }
   return a.rows >= 64ll * a.E ? tiles<Large>(a, st) : tiles<Small>(a, st);
 }
 
