@@ -208,36 +208,33 @@ __device__ __forceinline__ RowTile row_tile(const int32_t* __restrict__ offsets,
                  __builtin_amdgcn_readlane(t.rows, owner)};
 }
 
-// 16 FS features x 16 TT rows per workgroup, whose NW waves share K in runs of
-// blocks of 64 and join their sums in LDS in wave order; a wave has U blocks in
-// flight.  Weights are read as they lie: a lane takes chunk g and then chunk 4 +
-// g of its row's 128 bytes of a block, so that two loads take whole lines, and
-// the rows of x the same, which is all that the instruction asks for: their
-// contraction in the same order.  The workgroups of the last row tile clear the
-// rows of no expert.
-template <int FS, int TT, int NW, int U>
+// 16 rows x 16 features per S waves, NW / S such features' groups a workgroup.
+// The S waves share K in runs of blocks of 64 and join their sums in LDS in wave
+// order; a wave has 2 U blocks in flight.  Weights are read as they lie: a lane
+// takes chunk g and then chunk 4 + g of its row's 128 bytes of a block, so that
+// two loads take whole lines, and the rows of x the same, which is all that the
+// instruction asks for: their contraction in the same order.  The workgroups of
+// the last row tile clear the rows of no expert.
+template <int S, int NW, int U>
 __global__ void __launch_bounds__(NW * 64) grouped_few_kernel(GroupedArgs a) {
-  __shared__ f32x4_t part[NW][FS * TT][64];
+  __shared__ f32x4_t part[S > 1 ? NW : 1][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = lane & 15, g = lane >> 4, R = (int)a.rows, n0 = blockIdx.x * (16 * FS);
-  const RowTile t = row_tile(a.offsets, a.E, R, 16 * TT, blockIdx.y);
+  const int r = lane & 15, g = lane >> 4, R = (int)a.rows, n0 = (blockIdx.x * (NW / S) + wave / S) * 16;
+  const RowTile t = row_tile(a.offsets, a.E, R, 16, blockIdx.y);
   if (blockIdx.y + 1 == gridDim.y) {
+    constexpr int kChunks = NW / S * 2;  // of 8 outputs, of a workgroup
     const int d0 = min(max(a.offsets[0], 0), R), d1 = max(d0, min(a.offsets[a.E], R));
-    for (int i = threadIdx.x; i < (d0 + R - d1) * 2 * FS; i += NW * 64) {
-      const int d = i / (2 * FS), row = d < d0 ? d : d1 + (d - d0), n = n0 + i % (2 * FS) * 8;
+    for (int i = threadIdx.x; i < (d0 + R - d1) * kChunks; i += NW * 64) {
+      const int d = i / kChunks, row = d < d0 ? d : d1 + (d - d0), n = (blockIdx.x * kChunks + i % kChunks) * 8;
       if (n < a.N) *(uint4*)(a.y + (int64_t)row * a.N + n) = make_uint4(0, 0, 0, 0);
     }
   }
   if (t.rows <= 0) return;
-  const int blocks = (a.K + 63) / 64, per = (blocks + NW - 1) / NW, b0 = wave * per, b1 = min(blocks, b0 + per);
-  const uint16_t* w[FS];
-  const uint16_t* x[TT];
-#pragma unroll
-  for (int f = 0; f < FS; ++f) w[f] = a.w + ((int64_t)t.e * a.N + min(n0 + 16 * f + r, a.N - 1)) * a.K;
-#pragma unroll
-  for (int i = 0; i < TT; ++i) x[i] = a.x + (int64_t)(t.row0 + min(16 * i + r, t.rows - 1)) * a.K;
+  const int blocks = (a.K + 63) / 64, per = (blocks + S - 1) / S, b0 = wave % S * per, b1 = min(blocks, b0 + per);
+  const uint16_t* const w = a.w + ((int64_t)t.e * a.N + min(n0 + r, a.N - 1)) * a.K;
+  const uint16_t* const x = a.x + (int64_t)(t.row0 + min(r, t.rows - 1)) * a.K;
   struct Operands {
-    i32x4_t w[U][FS][2], x[U][TT][2];
+    i32x4_t w[U][2], x[U][2];
   };
   auto load = [&](int b, Operands& o) __attribute__((always_inline)) {
 #pragma unroll
@@ -246,17 +243,11 @@ __global__ void __launch_bounds__(NW * 64) grouped_few_kernel(GroupedArgs a) {
       for (int h = 0; h < 2; ++h) {
         // blocks past the run and chunks past K are read in their place, and not multiplied or zero
         const int k = min(min(b + u, blocks - 1) * 64 + 32 * h + 8 * g, a.K - 8);
-#pragma unroll
-        for (int f = 0; f < FS; ++f) o.w[u][f][h] = __builtin_nontemporal_load((const i32x4_t*)(w[f] + k));
-#pragma unroll
-        for (int i = 0; i < TT; ++i) o.x[u][i][h] = *(const i32x4_t*)(x[i] + k);
+        o.w[u][h] = __builtin_nontemporal_load((const i32x4_t*)(w + k));
+        o.x[u][h] = *(const i32x4_t*)(x + k);
       }
   };
-  f32x4_t acc[FS][TT];
-#pragma unroll
-  for (int f = 0; f < FS; ++f)
-#pragma unroll
-    for (int i = 0; i < TT; ++i) acc[f][i] = f32x4_t{};
+  f32x4_t acc{};
   auto multiply = [&](int b, Operands& o) __attribute__((always_inline)) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -265,55 +256,52 @@ __global__ void __launch_bounds__(NW * 64) grouped_few_kernel(GroupedArgs a) {
       for (int h = 0; h < 2; ++h) {
         if ((b + u) * 64 + 32 * h + 32 > a.K) {  // uniform: the last chunks
           const bool in = (b + u) * 64 + 32 * h + 8 * g < a.K;
-#pragma unroll
-          for (int f = 0; f < FS; ++f) o.w[u][f][h] = in ? o.w[u][f][h] : i32x4_t{};
-#pragma unroll
-          for (int i = 0; i < TT; ++i) o.x[u][i][h] = in ? o.x[u][i][h] : i32x4_t{};
+          o.w[u][h] = in ? o.w[u][h] : i32x4_t{};
+          o.x[u][h] = in ? o.x[u][h] : i32x4_t{};
         }
-#pragma unroll
-        for (int f = 0; f < FS; ++f)
-#pragma unroll
-          for (int i = 0; i < TT; ++i)
-            acc[f][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, o.w[u][f][h]),
-                                                                __builtin_bit_cast(bf16x8_t, o.x[u][i][h]), acc[f][i], 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, o.w[u][h]),
+                                                      __builtin_bit_cast(bf16x8_t, o.x[u][h]), acc, 0, 0, 0);
       }
     }
   };
-  // two sets of U blocks take turns
+  // Two sets of U blocks take turns; the last of a run loads no more.
   Operands o[2];
-  load(b0, o[0]);
-  __builtin_amdgcn_sched_barrier(0);
+  auto turn = [&](int b, Operands& now, Operands& next) __attribute__((always_inline)) {
+    if (b + U >= b1) {
+      multiply(b, now);
+      return false;
+    }
+    load(b + U, next);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(b, now);
+    __builtin_amdgcn_sched_barrier(0);
+    return true;
+  };
+  if (b0 < b1) {
+    load(b0, o[0]);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll 1
-  for (int b = b0; b < b1; b += 2 * U) {
-    load(b + U, o[1]);
-    __builtin_amdgcn_sched_barrier(0);
-    multiply(b, o[0]);
-    __builtin_amdgcn_sched_barrier(0);
-    load(b + 2 * U, o[0]);
-    __builtin_amdgcn_sched_barrier(0);
-    multiply(b + U, o[1]);
-    __builtin_amdgcn_sched_barrier(0);
+    for (int b = b0; turn(b, o[0], o[1]) && turn(b + U, o[1], o[0]); b += 2 * U) {}
   }
+  if constexpr (S > 1) {
+    part[wave][lane] = acc;
+    __syncthreads();
+    if (wave % S) return;
 #pragma unroll
-  for (int f = 0; f < FS; ++f)
-#pragma unroll
-    for (int i = 0; i < TT; ++i) part[wave][f * TT + i][lane] = acc[f][i];
-  __syncthreads();
-  for (int j = wave; j < FS * TT; j += NW) {
-    const int f = j / TT, i = j % TT;
-    f32x4_t v{};
-#pragma unroll
-    for (int q = 0; q < NW; ++q) v += part[q][j][lane];
-    const int n = n0 + 16 * f + 4 * g, row = 16 * i + r;
-    if (n < a.N && row < t.rows)  // N % 8 == 0: the lane's four outputs are all in or all out
-      *(uint2*)(a.y + (int64_t)(t.row0 + row) * a.N + n) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+    for (int q = 1; q < S; ++q) acc += part[wave + q][lane];
   }
+  const int n = n0 + 4 * g;
+  if (n < a.N && r < t.rows)  // N % 8 == 0: the lane's four outputs are all in or all out
+    *(uint2*)(a.y + (int64_t)(t.row0 + r) * a.N + n) = make_uint2(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]));
 }
 
-template <int FS, int TT, int NW, int U>
+// Row tiles that a launch has at most: one partial tile per expert beyond the whole ones.
+int64_t row_tiles(const GroupedArgs& a, int bm) { return a.rows / bm + (a.E < a.rows ? a.E : a.rows); }
+
+template <int S, int NW>
 hipError_t few(const GroupedArgs& a, hipStream_t st) {
-  const int64_t tm = a.rows / (16 * TT) + (a.E < a.rows ? a.E : a.rows);
-  hipLaunchKernelGGL((grouped_few_kernel<FS, TT, NW, U>), dim3((unsigned)((a.N + 16 * FS - 1) / (16 * FS)), (unsigned)tm),
+  constexpr int kFeatures = NW / S * 16;
+  hipLaunchKernelGGL((grouped_few_kernel<S, NW, 4>), dim3((unsigned)((a.N + kFeatures - 1) / kFeatures), (unsigned)row_tiles(a, 16)),
                      dim3(NW * 64), 0, st, a);
   return hipGetLastError();
 }
@@ -330,13 +318,15 @@ struct GradWork {
   ColSource<T::BM, T::WM> p;
   ColSource<T::BN, 1> q;
   Bf16Op op;
+  static constexpr int kRow = 64 * T::FN, kTurn = 32 * kRow;  // bytes that a wave turns at a time
+  uint8_t* turn;
 
   Places places;
   int lane, wave, wm, wn;
   Parked e, n0, k0;  // of the tile that is computed
-  enum { kExpert, kN, kK, kSteps, kRow, kRows };
+  enum { kExpert, kN, kK, kSteps, kFirst, kRows };
 
-  __device__ explicit GradWork(int w) : lane(threadIdx.x & 63), wave(w), wm(w % T::WM), wn(w / T::WM) {
+  __device__ GradWork(uint8_t* smem, int w) : turn(smem + T::kRing + w * kTurn), lane(threadIdx.x & 63), wave(w), wm(w % T::WM), wn(w / T::WM) {
     p.lanes(wm, wave, lane);
     q.lanes(wn * T::FN, wave, lane);
   }
@@ -360,19 +350,19 @@ struct GradWork {
     places.put(i, kN, (4 * band + in_band % bm) * T::BM);
     places.put(i, kK, in_band / bm * T::BN);
     places.put(i, kSteps, r1 > r0 ? (r1 - r0 + 63) / 64 : 1);
-    places.put(i, kRow, r0);
+    places.put(i, kFirst, r0);
     places.put(i, kRows, r1 - r0);
     return steps(i);
   }
   __device__ void set_p(int i) {
     const auto& a = kernel_args<GradArgs>().g;
     const int n = places.get(i, kN);
-    p.set(a.dy + (int64_t)places.get(i, kRow) * a.N + n, 2 * a.N, places.get(i, kRows), a.N - n, lane);
+    p.set(a.dy + (int64_t)places.get(i, kFirst) * a.N + n, 2 * a.N, places.get(i, kRows), a.N - n, lane);
   }
   __device__ void set_q(int i) {
     const auto& a = kernel_args<GradArgs>().g;
     const int k = places.get(i, kK);
-    q.set(a.x + (int64_t)places.get(i, kRow) * a.K + k, 2 * a.K, places.get(i, kRows), a.K - k, lane);
+    q.set(a.x + (int64_t)places.get(i, kFirst) * a.K + k, 2 * a.K, places.get(i, kRows), a.K - k, lane);
   }
   __device__ int begin(int i) {
     e = places.get(i, kExpert);
@@ -385,25 +375,32 @@ struct GradWork {
   __device__ __forceinline__ void store(f32x16_t (&acc)[T::FN][A]) {
     const auto& a = kernel_args<GradArgs>().g;
     constexpr int kSize = F32 ? 4 : 2;
-    const int h = (threadIdx.x >> 5) & 1, n = n0, col = k0 + wn * T::FN * 32;
+    [[maybe_unused]] const int h = (threadIdx.x >> 5) & 1;
+    const int n = n0, col = k0 + wn * T::FN * 32;
     const int64_t first = ((int64_t)(int)e * a.N + n) * a.K + col;
     const TileOut out((const uint8_t*)a.dw + first * kSize, (int64_t)kSize * a.K, min(T::BM, a.N - n));
 #pragma unroll
     for (int t = 0; t < A; ++t) {
       hold<T>(acc, t);
-      const uint32_t row = ((t * T::WM + wm) * 32 + (threadIdx.x & 31)) * out.ld;
+      const int row = (t * T::WM + wm) * 32;
+      if constexpr (F32) {
 #pragma unroll
-      for (int f = 0; f < T::FN; ++f) {
-        if constexpr (F32) {
+        for (int f0 = 0; f0 < T::FN; f0 += T::FN / 2) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const f32x4_t v = {acc[f][t][4 * q], acc[f][t][4 * q + 1], acc[f][t][4 * q + 2], acc[f][t][4 * q + 3]};
-            const int c = 32 * f + 8 * q + 4 * h;
-            out.put(__builtin_bit_cast(u32x4, v), c < a.K - col ? row + 4 * c : kOutside);
-          }
-        } else {
-          store_fragment(out, row + 64 * f, a.K - col - 32 * f, 4, [&](int i) { return acc[f][t][i]; });
+          for (int f = f0; f < f0 + T::FN / 2; ++f)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const f32x4_t v = {acc[f][t][4 * q], acc[f][t][4 * q + 1], acc[f][t][4 * q + 2], acc[f][t][4 * q + 3]};
+              Turn<kRow>{turn}.put(__builtin_bit_cast(u32x4, v), 8 * (f - f0) + 2 * q + h);
+            }
+          Turn<kRow>{turn}.store(out, row, 128 * f0, 4 * (a.K - col) - 128 * f0);
         }
+      } else {
+#pragma unroll
+        for (int f = 0; f < T::FN; ++f)
+          row_chunks(4, [&](int i) { return acc[f][t][i]; },
+                     [&](const u32x4& v, int c) { Turn<kRow>{turn}.put(v, 4 * f + c); });
+        Turn<kRow>{turn}.store(out, row, 0, 2 * (a.K - col));
       }
     }
   }
@@ -413,7 +410,7 @@ template <class T, bool F32>
 __global__ void __launch_bounds__(256, T::kPerCu) grouped_grad_kernel(GradArgs) {
   extern __shared__ __align__(16) uint8_t smem[];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  GradWork<T, F32> work(wave);
+  GradWork<T, F32> work(smem, wave);
   tile_loop<T>(work, smem, wave);
 }
 
@@ -427,8 +424,8 @@ unsigned grid_of(int64_t tiles) {
 template <class T>
 hipError_t tiles(const GroupedArgs& a, hipStream_t st) {
   const int tn = (int)ceil_div(a.N, T::BN);
-  // at most one partial row tile per expert beyond the whole ones; one workgroup for the rows of no expert
-  const dim3 grid(grid_of<T>((a.rows / T::BM + (a.E < a.rows ? a.E : a.rows)) * tn + 1));
+  // one workgroup more for the rows of no expert
+  const dim3 grid(grid_of<T>(row_tiles(a, T::BM) * tn + 1));
   if (a.w_kn)
     hipLaunchKernelGGL((grouped_tile_kernel<T, true>), grid, dim3(256), T::kRing, st, ForwardArgs{a, tn});
   else
@@ -440,28 +437,46 @@ template <class T>
 hipError_t grads(const GroupedGradArgs& a, hipStream_t st) {
   const int tn = (int)ceil_div(a.N, T::BM), tk = (int)ceil_div(a.K, T::BN);
   const dim3 grid(grid_of<T>((int64_t)a.E * tn * tk));
+  constexpr int lds = T::kRing + 4 * GradWork<T, false>::kTurn;
   if (a.f32)
-    hipLaunchKernelGGL((grouped_grad_kernel<T, true>), grid, dim3(256), T::kRing, st, GradArgs{a, tn, tk});
+    hipLaunchKernelGGL((grouped_grad_kernel<T, true>), grid, dim3(256), lds, st, GradArgs{a, tn, tk});
   else
-    hipLaunchKernelGGL((grouped_grad_kernel<T, false>), grid, dim3(256), T::kRing, st, GradArgs{a, tn, tk});
+    hipLaunchKernelGGL((grouped_grad_kernel<T, false>), grid, dim3(256), lds, st, GradArgs{a, tn, tk});
   return hipGetLastError();
 }
 
-using Large = Tile<256, 256, 2, 2, 3>;
-using Small = Tile<128, 128, 2, 2, 3>;
+// The outputs of the gradient take the LDS of the third slots.
+template <int QS>
+using Large = Tile<256, 256, 2, 2, QS>;
+template <int QS>
+using Small = Tile<128, 128, 2, 2, QS>;
 
 }  // namespace
 
+// The kernel of few rows where 128 x 128 tiles of the most 16-row tiles would not
+// give each CU one: a tile's workgroup has its weights' latency to itself then
+// (us, few rows / 128 x 128; E rows K N: 256 8 7168 512 17 / 60, 256 32 7168 512
+// 57 / 71, 8 1 4096 4096 9 / 34, 32 64 512 512 6.2 / 8.9; above the bound 256 64
+// 7168 512 107 / 99, 128 8 1536 4096 29 / 22, 8 16 4096 4096 63 / 39).  K is
+// shared by 4 waves where units of 16 x 16 outputs are few (17 us of the first;
+// by one wave 42, by 8 21) and long enough for two sets of loads each.
+// 256 x 256 tiles where there is one per CU (128 4096 1536 4096: 316, 128 x 128
+// 323; 64 4096 1024 2048: 55, 58), the small ones below that (32 2060 2560 640:
+// 29, 47; 16 300 2048 1024: 21, 28).
 hipError_t launch_grouped(const GroupedArgs& a, hipStream_t st) {
-  if (!a.w_kn && a.rows <= 16ll * a.E && a.rows <= 32768) {
-    if (a.rows <= 8ll * a.E) return few<1, 1, 8, 4>(a, st);
-    return few<2, 2, 8, 2>(a, st);
+  const int64_t tiny = row_tiles(a, 16);
+  if (!a.w_kn && tiny * ceil_div(a.N, 128) < 256) {
+    const int64_t waves = tiny * ceil_div(a.N, 16);
+    return waves >= 1024 || a.K < 512 ? few<1, 4>(a, st) : waves >= 512 || a.K < 1024 ? few<2, 4>(a, st) : few<4, 4>(a, st);
   }
-  return a.rows >= 64ll * a.E ? tiles<Large>(a, st) : tiles<Small>(a, st);
+  return row_tiles(a, 256) * ceil_div(a.N, 256) >= 256 ? tiles<Large<3>>(a, st) : tiles<Small<3>>(a, st);
 }
 
+// The same bound as above (us, 256 x 256 / 128 x 128; E rows K N: 128 32768 1536
+// 4096 731 / 959, 128 4096 1536 4096 335 / 458, 16 300 2048 1024 19.7 / 19.9;
+// below it 8 200 512 264 9.4 / 5.2).
 hipError_t launch_grouped_weight_grad(const GroupedGradArgs& a, hipStream_t st) {
-  return a.N > 128 && a.K > 128 ? grads<Large>(a, st) : grads<Small>(a, st);
+  return a.E * ceil_div(a.N, 256) * ceil_div(a.K, 256) >= 256 ? grads<Large<2>>(a, st) : grads<Small<2>>(a, st);
 }
 
 }  // namespace moe

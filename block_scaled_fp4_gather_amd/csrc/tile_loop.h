@@ -445,13 +445,39 @@ struct TileOut {
   }
 };
 
-// Stores a fragment of 32 rows x 32 outputs as bf16 (of 16, for 2 `quads`): row
-// r, which is this lane's (lane % 32), at byte `off` of the tile, the first
-// `cols` (a multiple of 8) of its outputs.  A lane has 4 of every 8; the two
-// lanes of a row swap, so that each holds 8 in a row: the lower groups 0 and 2,
-// the upper 1 and 3.
-template <class Value>
-__device__ __forceinline__ void store_fragment(const TileOut& out, uint32_t off, int cols, int quads, Value value) {
+// Rows of 32 that a wave turns in LDS, so that its stores are of whole rows of
+// ROW bytes: a lane has parts of one row, and 16 bytes of 32 rows at a time are
+// no whole lines.  16-byte chunk c of row r at position c ^ r.
+template <int ROW>
+struct Turn {
+  static constexpr int kChunks = ROW / 16;
+  uint8_t* area;  // of the wave, 32 ROW bytes
+  __device__ __forceinline__ void put(const u32x4& v, int c) const {
+    const int r = threadIdx.x & 31;
+    *(u32x4*)(area + r * ROW + ((c ^ r) % kChunks) * 16) = v;
+  }
+  // Rows row .. row + 31 of the tile, their first `bytes` (a multiple of 16) from byte `off` on.
+  __device__ __forceinline__ void store(const TileOut& out, int row, uint32_t off, int bytes) const {
+    const int lane = threadIdx.x & 63, c = lane % kChunks, r0 = lane / kChunks;
+    __builtin_amdgcn_wave_barrier();  // the wave's own LDS operations are in order
+    u32x4 v[kChunks / 2];
+#pragma unroll
+    for (int i = 0; i < kChunks / 2; ++i) {
+      const int r = r0 + i * (64 / kChunks);
+      v[i] = *(const u32x4*)(area + r * ROW + ((c ^ r) % kChunks) * 16);
+    }
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int i = 0; i < kChunks / 2; ++i)
+      out.put(v[i], 16 * c < bytes ? (uint32_t)(row + r0 + i * (64 / kChunks)) * out.ld + off + 16 * c : kOutside);
+  }
+};
+
+// put(v, c) for the 16-byte chunks c of a row's 32 outputs as bf16 (of 16, for 2
+// `quads`) that this lane gets: it has 4 of every 8 of row lane % 32, and the two
+// lanes of a row swap, so that the lower has chunks 0 and 2, the upper 1 and 3.
+template <class Value, class Put>
+__device__ __forceinline__ void row_chunks(int quads, Value value, Put put) {
   const int h = (threadIdx.x >> 5) & 1;
 #pragma unroll
   for (int q = 0; q < 4; q += 2) {
@@ -463,8 +489,14 @@ __device__ __forceinline__ void store_fragment(const TileOut& out, uint32_t off,
       for (int e = 0; e < 2; ++e) v[i][e] = pack_bf16(value(4 * (q + i) + 2 * e), value(4 * (q + i) + 2 * e + 1));
     const auto lo = __builtin_amdgcn_permlane32_swap(v[0][0], v[1][0], false, false);
     const auto hi = __builtin_amdgcn_permlane32_swap(v[0][1], v[1][1], false, false);
-    out.put(u32x4{lo[0], hi[0], lo[1], hi[1]}, 8 * (q + h) < cols ? off + 16 * (q + h) : kOutside);
+    put(u32x4{lo[0], hi[0], lo[1], hi[1]}, q + h);
   }
+}
+
+// Stores such a row's first `cols` (a multiple of 8) outputs at byte `off` of the tile.
+template <class Value>
+__device__ __forceinline__ void store_fragment(const TileOut& out, uint32_t off, int cols, int quads, Value value) {
+  row_chunks(quads, value, [&](const u32x4& v, int c) { out.put(v, 8 * c < cols ? off + 16 * c : kOutside); });
 }
 
 }  // namespace moe
