@@ -1,15 +1,22 @@
 // Linear map with MXFP4 weights and MXFP4 activations:
 //   y[m][n] = sum over blocks b of 32:  sw[n][b] sx[m][b] sum_{k in b} c[n][k] q[m][k]
-// with E2M1 codes c and q and UE8M0 scales, on v_mfma_scale_f32_16x16x128_
-// f8f6f4, which takes codes and scales as they are stored: both operands E2M1,
-// at twice the rate of its FP8 forms.  Sums are fp32; a product of two codes
-// has at most 4 significant bits.  An activation of the framework follows where
-// asked for, and one rounding to bf16.
+// with E2M1 codes c and q and UE8M0 scales, on v_mfma_scale_f32_*_f8f6f4, which
+// takes codes and scales as they are stored: both operands E2M1, at twice the
+// rate of its FP8 forms.  Few tokens take its 16x16x128 form, which wastes least
+// of them, tiles the 32x32x64 one (tile_loop.h).  Sums are fp32; a product of two
+// codes has at most 4 significant bits.  An activation of the framework follows
+// where asked for, and one rounding to bf16.
 //
 // Tokens are quantised as fp4_quant.hip does, and kept in the operand order of
 // the prepared weights (Fp4Shape), so that a wave's load or copy is 1 KiB in a
-// row.  Operands: A = weights (16 rows), B = tokens (16): a lane's four
-// accumulators are consecutive outputs of one token.
+// row.  Operands: A = weights, B = tokens: four of a lane's accumulators are
+// consecutive outputs of one token.
+//
+// Measured (M tokens, K, N; without the tokens' own quantisation): 8192 7168
+// 2 x 2048 118 us, 4.1 PFLOP/s, what its matrix instructions reach beside the LDS
+// reads and copies at the clock that the power leaves; 37 320 2560 3.8 us and 512
+// 4096 4096 15 us, latency of few steps; 1 7168 2 x 2048 5.2 us with it, 3.0 TB/s
+// of weights.
 #include <hip/hip_runtime.h>
 
 #include "act.h"
@@ -584,17 +591,24 @@ hipError_t launch_fp4_linear(const Fp4Shape& s, const uint8_t* prepared, const u
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  // Few tokens: the waves of a workgroup share K, and workgroups of more outputs
+  // read the tokens less often (us with the tokens' quantisation, 32 x 64 / 64 x
+  // 64 outputs / tiles; M K N: 64 4096 4096 8.9 / 10.0 / 16.5, 192 4096 4096 11.9 /
+  // 10.8 / 18.6, 512 4096 4096 19.8 / 18.4 / 19.8, 512 7168 2 x 2048 25 / 23 / 30,
+  // 768 4096 4096 27 / 25 / 21.7, 384 2048 7168 16 / 17 / 14.3).
   if (M <= 16) return ks > 8 ? MOE_FEW(1, 1, 16, 1, false) : MOE_FEW(1, 1, 4, 1, false);
   if (M <= 32) return MOE_FEW(2, 2, 8, 1, false);
   const int64_t wide = (M + 63) / 64;
   if (wide * ((s.subtiles() + 1) / 2) <= 256) return MOE_FEW(2, 4, 8, 1, false);
   if (wide * ((s.subtiles() + 3) / 4) <= 512) return MOE_FEW(4, 4, 8, 1, false);
 #undef MOE_FEW
-  auto rounds = [&](int bm, int bn) {
-    return ((M + bm - 1) / bm * (int64_t)((s.subtiles() * 16 + bn - 1) / bn) + 255) / 256;
-  };
-  if (20 * rounds(256, 256) <= 10 * rounds(128, 128)) return launch_tile<Tile<256, 256, 2, 2, 2>>(s, prepared, t, M, out, st);
-  return launch_tile<Tile<128, 128, 2, 2, 2>>(s, prepared, t, M, out, st);
+  // 256 x 256 tiles move half the bytes into LDS, 128 x 128 ones fill the chip
+  // sooner, two a CU (us, 128 / 256; M K N: 2048 4096 4096, 512 tiles of 128, 33 /
+  // 40; 1536 2048 7168, 672, 27 / 29; 2048 2048 7168, 896, 33 / 31; 4096 4096 4096,
+  // 1024, 55 / 49; 8192 7168 2 x 2048, 2048, 174 / 141).
+  if ((M + 127) / 128 * (int64_t)((s.subtiles() + 7) / 8) <= 3 * 256)
+    return launch_tile<Tile<128, 128, 2, 2, 2>>(s, prepared, t, M, out, st);
+  return launch_tile<Tile<256, 256, 2, 2, 2>>(s, prepared, t, M, out, st);
 }
 
 }  // namespace moe

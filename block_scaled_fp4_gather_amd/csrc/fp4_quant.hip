@@ -80,21 +80,14 @@ __device__ __forceinline__ uint32_t raw_amax(const Raw<F32>& r) {
 
 __device__ __forceinline__ bool finite_bits(uint32_t b) { return b < 0x7F800000u; }
 
-// The value of E2M1 code c and the midpoint above it.
-__device__ __forceinline__ double e2m1_middle(int c) {
-  return c < 4 ? 0.5 * c + 0.25 : c == 4 ? 2.5 : c == 5 ? 3.5 : 5.0;
-}
-
-// Code of v with |v| / unit rounded exactly, unit > 0: the midpoints that lie
-// below it are counted, one that it equals where the code below is odd.
+// Code of v with |v| / unit rounded exactly, unit > 0: of the midpoints between
+// the values 0 0.5 1 1.5 2 3 4 6, those that lie below it are counted, and one
+// that it equals where the code below is odd.  (Their products with the unit are
+// made from each other, exactly: as constants they would fill scalar registers.)
 __device__ __forceinline__ uint32_t e2m1_exact(float v, double unit) {
-  const double a = fabs((double)v);
-  int c = 0;
-#pragma unroll
-  for (int i = 0; i < 7; ++i) {
-    const double t = e2m1_middle(i) * unit;
-    c += (i & 1) ? a >= t : a > t;
-  }
+  const double a = fabs((double)v), h = 0.5 * unit;
+  const double t0 = 0.5 * h, t1 = t0 + h, t2 = t1 + h, t3 = t2 + h, t4 = 2.0 * t2, t5 = 2.0 * t3, t6 = 2.0 * t4;
+  const int c = (a > t0) + (a >= t1) + (a > t2) + (a >= t3) + (a > t4) + (a >= t5) + (a > t6);
   return (uint32_t)c | (__float_as_uint(v) >> 31 << 3);
 }
 
