@@ -58,9 +58,10 @@ struct ForwardWork {
     const auto& a = args.g;
     const int32_t* const offsets = a.offsets;
     const int E = a.E, R = (int)a.rows, tiles_n = args.tiles_n;
-    total = 0;
-    for (int e0 = 0; e0 < E; e0 += 64) total += __builtin_amdgcn_readlane(tiles_upto(offsets, E, R, e0), 63);
-    total *= tiles_n;
+    int64_t all = 0;
+    for (int e0 = 0; e0 < E; e0 += 64) all += __builtin_amdgcn_readlane(tiles_upto(offsets, E, R, e0), 63);
+    all *= tiles_n;
+    total = all <= 0x7FFFFFFF ? (int)all : 0;  // more only where offsets decrease: no tiles then
     const int start = (int)(blockIdx.x % 8) * ((total + 7) / 8);
     e = before = 0;
     for (int e0 = 0; e0 < E; e0 += 64) {

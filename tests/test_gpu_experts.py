@@ -218,6 +218,20 @@ def test_linear(M, K, N, fn):
     assert torch.equal(lin(x.cuda()), y)
 
 
+# 256 x 256 tiles: above 768 of 128 x 128.
+@pytest.mark.parametrize("M,K,N,fn", [(2100, 320, 6200, "none"), (3100, 96, 4000, "relu2"), (1100, 544, 8200, "swigluoai"),
+                                      (1030, 64, 5800, "gelu_tanh")])
+def test_linear_large_tiles(M, K, N, fn):
+    lin, codes, scales = make_linear(M, K, N, fn)
+    x = (rand(3, M, K) * torch.exp(0.4 * rand(4, K))).bfloat16()
+    rows = torch.cat([torch.arange(0, M, 67), torch.tensor([1, 31, 32, 63, 64, 255, 256, 1023, 1024, M - 2, M - 1])])
+    y = check_linear(lin, codes, scales, x, rows)
+    x[1, 40], x[0, 5] = NAN, INF
+    z = lin(x.cuda())
+    assert bool(torch.isnan(z[:2]).all() if fn in ("none", "relu2") else torch.isnan(z[:2]).any())
+    assert torch.equal(z[2:], y[2:])
+
+
 @pytest.mark.parametrize("M", [1, 4, 37, 600])
 def test_linear_given_codes(M):
     lin, codes, scales = make_linear(M, 1312, 1056, "silu")
@@ -461,6 +475,154 @@ def test_grouped_nan_stays_in_its_row_and_expert():
     assert bool(torch.isnan(dw[1, :, 5]).all())
     dw[1, :, 5] = cw[1, :, 5]
     assert torch.equal(dw, cw)
+
+
+# Ragged groups at the borders of the launches' variants: 256 x 256 tiles (many
+# experts, or many rows), one-step contractions, tails of every row fragment, and
+# few rows with K shared by 1, 2 and 4 waves.
+SOME = [0, 1, 2, 5, 0, 3]
+VARIANTS = [
+    # counts, rows before and after them, K, N
+    (SOME * 40 + [600, 257, 64, 33, 96, 161, 225, 31, 255, 256], 3, 7, 72, 264), (SOME * 11 + [400, 200], 0, 2, 328, 1032),
+    ([70, 0, 1] * 23, 0, 0, 64, 1288), ([1] * 130, 5, 0, 24, 520), ([9000, 0, 11000], 1, 40, 72, 1000),
+    ([0] * 258 + [3], 0, 0, 520, 264), ([2, 0, 0, 31, 16], 5, 3, 2056, 40), ([1], 0, 0, 4104, 8), ([5] * 20, 1, 0, 520, 72),
+    ([1, 0, 1, 17], 0, 300, 1032, 136), ([0, 2] * 150, 0, 0, 1096, 16), ([16, 15], 0, 0, 8, 2056),
+]
+
+
+@pytest.mark.parametrize("counts,before,after,K,N", VARIANTS)
+def test_grouped_variants(counts, before, after, K, N):
+    test_grouped_linear_and_gradients(counts, before, after, K, N)
+
+
+@pytest.mark.parametrize("E,T,K,N", [(4, 96, 64, 72), (300, 700, 72, 264), (6, 9, 1032, 72), (3, 700, 64, 1032)])
+def test_grouped_wild_offsets_in_every_variant(E, T, K, N):
+    x, w, dy = rand(1, T, K).bfloat16().cuda(), rand(2, E, N, K).bfloat16().cuda(), rand(3, T, N).bfloat16().cuda()
+    g = torch.Generator().manual_seed(E)
+    for low, high in ((-50, T + 50), (-2 ** 31, 2 ** 31 - 1)):
+        off = torch.randint(low, high, (E + 1,), generator=g).int().cuda()
+        for a, b, layout in ((x, N, 0), (dy, K, 1)):
+            big = torch.full((T + 32, b), 7.0, dtype=torch.bfloat16, device="cuda")
+            experts._grouped(a, w, off, layout, big[16:T + 16])
+            assert bool((big[:16] == 7).all()) and bool((big[T + 16:] == 7).all())
+        big = torch.full((E + 2, N, K), 7.0, device="cuda")
+        experts.grouped_weight_grad(dy, x, off, torch.float32, out=big[1:E + 1])
+        assert bool((big[0] == 7).all()) and bool((big[E + 1] == 7).all())
+
+
+@pytest.mark.parametrize("T", [5, 600])
+def test_grouped_weights_past_32_bits(T):
+    """300 experts of 2048 x 4096: 5 GB of weights and of their gradient."""
+    E, N, K = 300, 2048, 4096
+    w = torch.empty(E, N, K, dtype=torch.bfloat16, device="cuda")
+    w[0], w[-1] = rand(1, N, K).bfloat16(), rand(2, N, K).bfloat16()
+    x, dy = rand(3, T, K).bfloat16(), rand(4, T, N).bfloat16()
+    off = make_offsets([2] + [0] * (E - 2) + [T - 2])
+    small = torch.tensor([0, 2, T], dtype=torch.int32)
+    both = w[[0, E - 1]].cpu()
+    y = experts.grouped_linear(x.cuda(), w, off.cuda())
+    ey, sy = ref.grouped(x, both, small)
+    assert bool(((y.cpu().double() - ey).abs() <= dot_bound(sy, K) + BF16 * ey.abs()).all())
+    dx = experts._grouped(dy.cuda(), w, off.cuda(), experts.WEIGHT_IN_OUT)
+    ex, sx = ref.grouped(dy, both.transpose(1, 2), small)
+    assert bool(((dx.cpu().double() - ex).abs() <= dot_bound(sx, N) + BF16 * ex.abs()).all())
+    w.fill_(7.0)
+    dw = experts.grouped_weight_grad(dy.cuda(), x.cuda(), off.cuda(), out=w)
+    assert not bool(dw[1:-1].any())
+    ew, sw = ref.grouped_grad(dy, x, small)
+    assert bool(((dw[[0, E - 1]].cpu().double() - ew).abs() <= dot_bound(sw, T) + BF16 * ew.abs()).all())
+
+
+def test_grouped_rows_past_32_bits():
+    """600000 rows of 4096 values, of which the last 300 are not zero."""
+    T, K, N, n = 600000, 4096, 8, 300
+    x = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda")
+    dy = torch.zeros(T, N, dtype=torch.bfloat16, device="cuda")
+    tail, dtail = rand(1, n, K).bfloat16(), rand(2, n, N).bfloat16()
+    x[-n:], dy[-n:] = tail, dtail
+    w = (rand(3, 2, N, K) / 64).bfloat16()
+    off = torch.tensor([0, T - 100, T], dtype=torch.int32)
+    small = torch.tensor([0, n - 100, n], dtype=torch.int32)
+    y = experts.grouped_linear(x, w.cuda(), off.cuda())
+    ey, sy = ref.grouped(tail, w, small)
+    assert bool(((y[-n:].cpu().double() - ey).abs() <= dot_bound(sy, K) + BF16 * ey.abs()).all()) and not bool(y[:-n].any())
+    dx = experts._grouped(dy, w.cuda(), off.cuda(), experts.WEIGHT_IN_OUT)
+    ex, sx = ref.grouped(dtail, w.transpose(1, 2), small)
+    assert bool(((dx[-n:].cpu().double() - ex).abs() <= dot_bound(sx, N) + BF16 * ex.abs()).all()) and not bool(dx[:-n].any())
+    dw = experts.grouped_weight_grad(dy, x, off.cuda())
+    ew, sw = ref.grouped_grad(dtail, tail, small)
+    # zeros add nothing: 300 products that are not
+    assert bool(((dw.cpu().double() - ew).abs() <= dot_bound(sw, n) + BF16 * ew.abs()).all())
+
+
+def test_grouped_gradients_one_at_a_time():
+    """Only x or only w asks for a gradient; the output's may be strided or broadcast."""
+    off = make_offsets([20, 0, 45], 2).cuda()
+    x, w = rand(1, 70, 64).bfloat16().cuda(), rand(2, 3, 40, 64).bfloat16().cuda()
+    dy = rand(3, 40, 70).bfloat16().cuda().t()
+    xr, wr = x.clone().requires_grad_(), w.clone().requires_grad_()
+    dx, dw = torch.autograd.grad(experts.grouped_linear(xr, wr, off), (xr, wr), dy)
+    assert torch.equal(torch.autograd.grad(experts.grouped_linear(xr, w, off), xr, dy)[0], dx)
+    assert torch.equal(torch.autograd.grad(experts.grouped_linear(x, wr, off), wr, dy)[0], dw)
+    assert torch.equal(dw, experts.grouped_weight_grad(dy.contiguous(), x, off))
+    (ones,) = torch.autograd.grad(experts.grouped_linear(x, wr, off).sum(), wr)
+    assert torch.equal(ones, experts.grouped_weight_grad(torch.ones_like(dy).contiguous(), x, off))
+
+
+# ---------------------------------------------------------------- long arrays
+
+def test_quantize_past_32_bits():
+    x = torch.zeros(40000, 65536, dtype=torch.bfloat16, device="cuda")
+    tail = spread(1, 7, 65536).bfloat16()
+    x[-7:] = tail
+    codes, scales, _ = ref.quantize(tail[None], "mxfp4")
+    q = experts.fp4_quantize(x)
+    assert torch.equal(q.codes[-7:].cpu(), codes[0]) and torch.equal(q.scales[-7:].cpu(), scales[0])
+    back = experts.fp4_dequantize(q)
+    assert torch.equal(back[-7:].cpu(), ref.dequantize(codes[0], scales[0], "mxfp4").bfloat16())
+    del back, q
+    codes, scales, g = ref.quantize(tail[None], "nvfp4")
+    q = experts.fp4_quantize(x, "nvfp4")
+    assert torch.equal(q.global_scale.cpu(), g)
+    assert torch.equal(q.codes[-7:].cpu(), codes[0]) and torch.equal(q.scales[-7:].cpu(), scales[0])
+
+
+def test_linear_past_32_bits():
+    """The last features of 2^31 weights, and the last tokens of 2^31 values."""
+    K, N = 65536, 32768
+    g = torch.Generator(device="cuda").manual_seed(1)
+    codes = torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8, device="cuda")
+    scales = torch.randint(112, 118, (N, K // 32), generator=g, dtype=torch.uint8, device="cuda")
+    x = torch.zeros(34000, K, dtype=torch.bfloat16, device="cuda")
+    x[-3:] = rand(2, 3, K).bfloat16()
+    for M, rows in ((3, slice(N - 40, N)), (300, slice(N - 24, N)), (34000, slice(0, 8))):
+        part = experts.Fp4Desc(K, N if M < 1000 else 8, M)
+        lin = experts.Fp4Linear(part, codes[:part.N], scales[:part.N])
+        q = experts.fp4_quantize(x[-3:])
+        y = lin(x[-M:])
+        exact, s = ref.linear(q.codes.cpu(), q.scales.cpu(), codes[rows].cpu(), scales[rows].cpu())
+        want, tol = linear_bound(exact, s, 0, "none", K)
+        assert bool(((y[-3:, rows].cpu().double() - want).abs() <= tol).all())
+        assert not bool(y[:-3].any())
+
+
+def test_routes_past_32_bits():
+    M, k, H, E = 300000, 4, 2048, 64
+    ids = make_ids(M, k, E)
+    groups = experts.group_routes(ids.cuda(), E)
+    x = torch.randn(M, H, device="cuda").bfloat16()
+    xg = experts.gather_routes(x, groups)
+    pick = torch.tensor([0, 1, M * k // 2, int(groups.offsets[-1]) - 1, M * k - 1])
+    for p in pick.tolist():
+        r = int(groups.order[p])
+        assert torch.equal(xg[p], x[r // k] if r >= 0 else torch.zeros_like(x[0]))
+    w = rand(3, M, k).cuda()
+    out = experts.combine_routes(xg, groups, w)
+    f = torch.where(groups.place >= 0, w, torch.zeros_like(w)).double()
+    for t in (0, 7, M - 2, M - 1):  # rows of a token are its own x again
+        terms = f[t].sum() * x[t].double()
+        tol = BF16 * terms.abs() + (k + 1) * FP32 * f[t].abs().sum() * x[t].double().abs()
+        assert bool(((out[t].double() - terms).abs() <= tol).all())
 
 
 # ---------------------------------------------------------------- together
