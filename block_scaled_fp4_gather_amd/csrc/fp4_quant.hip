@@ -177,7 +177,10 @@ __device__ __forceinline__ uint32_t nvfp4_codes(const Raw<F32>& r, uint32_t byte
 template <bool NV, bool F32, bool STRIDED>
 __global__ void __launch_bounds__(256) fp4_quantize_kernel(QuantArgs a, Rows rows, int64_t items, int parts) {
   const int64_t step = (int64_t)gridDim.x * 256;
-  for (int64_t e = blockIdx.y; e < a.experts; e += gridDim.y) {
+  // From the last expert back: the one that fp4_amax_kernel read last may still be
+  // in the cache before HBM (64 x 640 x 2560 of fp32: 85 -> 78 us, and the inverse,
+  // which starts at the first, 120 -> 112).
+  for (int64_t e = a.experts - 1 - blockIdx.y; e >= 0; e -= gridDim.y) {
     const uint8_t* const x = (const uint8_t*)a.x + e * a.rows * a.ld * (F32 ? 4 : 2);
     uint32_t* const codes = (uint32_t*)(a.codes + e * a.rows * (a.K / 2));
     uint8_t* const scales = a.scales + e * a.rows * (a.K / (NV ? 16 : 32));
