@@ -446,11 +446,14 @@ hipError_t grads(const GroupedGradArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-// The outputs of the gradient take the LDS of the third slots.
+// Slots of the second operand, and with Deep of both.  The outputs of the gradient
+// take the LDS of one more.
 template <int QS>
 using Large = Tile<256, 256, 2, 2, QS>;
 template <int QS>
 using Small = Tile<128, 128, 2, 2, QS>;
+template <int S>
+using Deep = Tile<128, 128, 2, 2, S, S>;
 
 }  // namespace
 
@@ -463,21 +466,27 @@ using Small = Tile<128, 128, 2, 2, QS>;
 // by one wave 42, by 8 21) and long enough for two sets of loads each.
 // 256 x 256 tiles where there is one per CU (128 4096 1536 4096: 316, 128 x 128
 // 323; 64 4096 1024 2048: 55, 58), the small ones below that (32 2060 2560 640:
-// 29, 47; 16 300 2048 1024: 21, 28).
+// 29, 47; 16 300 2048 1024: 21, 28).  Small ones that have a CU to themselves take
+// all of its LDS (five slots / 3 and 2 and two a CU: 256 64 7168 512 86 / 97, 8 64
+// 4096 4096 44 / 48, 8 2000 512 264 9.9 / 9.4; where there are more, 4 8000 1024
+// 1024 39 / 31).
 hipError_t launch_grouped(const GroupedArgs& a, hipStream_t st) {
   const int64_t tiny = row_tiles(a, 16);
   if (!a.w_kn && tiny * ceil_div(a.N, 128) < 256) {
     const int64_t waves = tiny * ceil_div(a.N, 16);
     return waves >= 1024 || a.K < 512 ? few<1, 4>(a, st) : waves >= 512 || a.K < 1024 ? few<2, 4>(a, st) : few<4, 4>(a, st);
   }
-  return row_tiles(a, 256) * ceil_div(a.N, 256) >= 256 ? tiles<Large<3>>(a, st) : tiles<Small<3>>(a, st);
+  if (row_tiles(a, 256) * ceil_div(a.N, 256) >= 256) return tiles<Large<3>>(a, st);
+  return row_tiles(a, 128) * ceil_div(a.N, 128) <= 256 ? tiles<Deep<5>>(a, st) : tiles<Small<3>>(a, st);
 }
 
 // The same bound as above (us, 256 x 256 / 128 x 128; E rows K N: 128 32768 1536
 // 4096 731 / 959, 128 4096 1536 4096 335 / 458, 16 300 2048 1024 19.7 / 19.9;
-// below it 8 200 512 264 9.4 / 5.2).
+// below it 8 200 512 264 9.4 / 5.2); the small ones with four slots or two as there
+// (3 20000 1000 72: 71 / 86; 8 2000 512 264: 8.4 / 7.9).
 hipError_t launch_grouped_weight_grad(const GroupedGradArgs& a, hipStream_t st) {
-  return a.E * ceil_div(a.N, 256) * ceil_div(a.K, 256) >= 256 ? grads<Large<2>>(a, st) : grads<Small<2>>(a, st);
+  if (a.E * ceil_div(a.N, 256) * ceil_div(a.K, 256) >= 256) return grads<Large<2>>(a, st);
+  return a.E * ceil_div(a.N, 128) * ceil_div(a.K, 128) <= 256 ? grads<Deep<4>>(a, st) : grads<Small<2>>(a, st);
 }
 
 }  // namespace moe

@@ -4,15 +4,17 @@
 // operands are 32 bytes of a row: 16 bf16 or 64 E2M1 values, 16 bytes a lane.  A
 // step is 128 bytes of the contraction, two halves of two such quarters.
 //
-// Both operands come to LDS by direct copies, in rings of two slots and of QS,
+// Both operands come to LDS by direct copies, in rings of PS and of QS slots,
 // and from there to registers half a step before they are multiplied:
 //   half 0 of step s   multiply half 0; read half 1
 //   barrier            the slots of step s are read, and step s + 1 is there
-//   half 1             multiply half 1; copy steps s + 2 and s + QS over those of
+//   half 1             multiply half 1; copy steps s + PS and s + QS over those of
 //                      step s; read half 0 of step s + 1
 // so that a copy has a step (2048 cycles of the matrix cores at 256 x 256) to
-// arrive, or with three slots two: enough for the way from HBM, which an operand
-// takes that few tiles share (weights); the other one comes from the L2 mostly.
+// arrive with two slots, and with three two: enough for the way from HBM, which
+// an operand takes that few tiles share (weights); the other one comes from the
+// L2 mostly.  Where a CU has one small tile, of 512 cycles a step, all of its LDS
+// is slots.
 // An LDS read has half a step, and there is one barrier a step.  The steps of a
 // tile and those of the next follow each other without a gap: what is copied
 // runs ahead of what is multiplied across tiles, and the outputs go from the
@@ -51,13 +53,13 @@ __device__ __forceinline__ void static_for(F&& f) {
   static_for(std::make_integer_sequence<int, N>{}, f);
 }
 
-template <int BM_, int BN_, int WM_, int WN_, int QS_>
+template <int BM_, int BN_, int WM_, int WN_, int QS_, int PS_ = 2>
 struct Tile {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
-  static constexpr int QS = QS_;  // slots of the second operand
+  static constexpr int QS = QS_, PS = PS_;  // slots of the second operand, and of the first
   static constexpr int FM = BM / 32 / WM, FN = BN / 32 / WN;  // a wave's fragments of 32 rows
   static constexpr int kM = BM * 128, kN = BN * 128;  // bytes of a slot
-  static constexpr int kRing = 2 * kM + QS * kN;
+  static constexpr int kRing = PS * kM + QS * kN;
   // workgroups of a launch: as many as run at once on the 256 CUs, and of them on an XCD
   static constexpr int kPerCu = kRing <= 81920 ? 2 : 1, kGrid = 256 * kPerCu;
   static_assert(WM * WN == 4 && BM % 32 == 0 && BN % 32 == 0 && FM > 0 && FN > 0, "4 waves, whole copies");
@@ -103,7 +105,7 @@ struct Parked {
 };
 
 // What a workgroup's tiles are, from when they are first copied until they are
-// multiplied (up to 4 tiles later): 8 numbers each, in the lanes of a register.
+// multiplied (up to QS + 1 tiles later): 8 numbers each, in the lanes of a register.
 struct Places {
   int lanes;
   __device__ __forceinline__ void put(int i, int field, int v) {
@@ -269,12 +271,13 @@ __device__ __forceinline__ void tile_loop(Work& work, uint8_t* smem, int wave) {
   using P = decltype(work.p);
   using Q = decltype(work.q);
   using Op = decltype(work.op);
-  static_assert(T::QS == 2 || (T::QS == 3 && Op::kCopies == 0), "two or three steps");
+  static_assert(T::PS == T::QS || (T::PS == 2 && T::QS == 3), "what kLater counts");
+  static_assert(Op::kCopies == 0 || T::QS == 2, "the instruction's own copies have two slots");
   constexpr int kOps = T::FM + T::FN, kReads = 2 * kOps;
   constexpr int kCopies = P::kCopies + Q::kCopies + Op::kCopies;
-  // Copies that may be on their way when a step's have to be there: with three
-  // slots those of the second operand for a later one, which come last.
-  constexpr int kLater = T::QS == 3 ? Q::kCopies : 0;
+  // Copies that may be on their way when a step's have to be there: those for
+  // later ones, which came after them.
+  constexpr int kLater = (T::PS - 2) * P::kCopies + (T::QS - 2) * Q::kCopies;
   // Stores of a whole tile that may be too: a wave counts 63 operations.
   constexpr int kFullStores = T::FM * Work::kStores + kLater < 60 ? T::FM * Work::kStores + kLater : 60;
   struct Frags {
@@ -307,15 +310,15 @@ __device__ __forceinline__ void tile_loop(Work& work, uint8_t* smem, int wave) {
     }
   };
   // Slots: of the step that is multiplied and the next, which is read.
-  int slot = 0, qslot = 0, qnext = 1;
+  int slot = 0, snext = 1, qslot = 0, qnext = 1;
   auto area_p = [&](int s) __attribute__((always_inline)) { return smem + s * T::kM; };
-  auto area_q = [&](int s) __attribute__((always_inline)) { return smem + 2 * T::kM + s * T::kN; };
+  auto area_q = [&](int s) __attribute__((always_inline)) { return smem + T::PS * T::kM + s * T::kN; };
   // Copy c into slots s and t, the first operand's copies first.
   auto copy = [&](int s, int t, int c) __attribute__((always_inline)) {
     if (c < P::kCopies)
       work.p.copy(c, lds + s * T::kM);
     else if (c < P::kCopies + Q::kCopies)
-      work.q.copy(c - P::kCopies, lds + 2 * T::kM + t * T::kN);
+      work.q.copy(c - P::kCopies, lds + T::PS * T::kM + t * T::kN);
     else
       work.op.copy(c - P::kCopies - Q::kCopies);
   };
@@ -328,13 +331,13 @@ __device__ __forceinline__ void tile_loop(Work& work, uint8_t* smem, int wave) {
   };
 
   static_for<T::QS>([&](auto sc) __attribute__((always_inline)) {
-    constexpr int s = decltype(sc)::value, c0 = s < 2 ? 0 : P::kCopies;
-    if constexpr (s < 2) work.p.start(cp.step);
+    constexpr int s = decltype(sc)::value, c0 = s < T::PS ? 0 : P::kCopies;
+    if constexpr (s < T::PS) work.p.start(cp.step);
     work.q.start(cq.step);
     work.op.start(cq.step, s);
     static_for<kCopies - c0>([&](auto c) __attribute__((always_inline)) { copy(s, s, c0 + decltype(c)::value); });
     advance_q();
-    if constexpr (s < 2) advance_p();
+    if constexpr (s < T::PS) advance_p();
   });
   vm_wait<kCopies + kLater>();
   __syncthreads();
@@ -397,9 +400,14 @@ __device__ __forceinline__ void tile_loop(Work& work, uint8_t* smem, int wave) {
         vm_wait<kLater>();
       stored = 0;
       __syncthreads();  // everyone's are, and everyone has read these slots
-      half(std::integral_constant<int, 1>{}, r1, r0, area_p(slot ^ 1), area_q(qnext));
+      half(std::integral_constant<int, 1>{}, r1, r0, area_p(T::PS == 2 ? slot ^ 1 : snext), area_q(qnext));
       sc = sc_next;
-      slot ^= 1;
+      if constexpr (T::PS == 2) {
+        slot ^= 1;
+      } else {
+        slot = snext;
+        snext = snext + 1 == T::PS ? 0 : snext + 1;
+      }
       qslot = qnext;
       qnext = qnext + 1 == T::QS ? 0 : qnext + 1;
       advance_q();
