@@ -215,11 +215,13 @@ class Fp4Linear:
 
     @classmethod
     def from_float(cls, desc: Fp4Desc, weight: torch.Tensor, device="cuda", stream=None):
-        """The map of a bf16 or fp32 weight [rows][K], quantised here."""
-        if stream is not None:
-            return _on(stream, lambda: cls.from_float(desc, weight, device), weight)
-        q = fp4_quantize(weight.to(_device(device)), "mxfp4")
-        return cls(desc, q.codes, q.scales, device)
+        """The map of a bf16 or fp32 weight [rows][K], quantised on the GPU."""
+        dev = _device(device)
+        with moe.preparing(moe.as_stream(stream, dev), dev, weight) as made:
+            q = fp4_quantize(weight.to(dev).contiguous(), "mxfp4")
+            linear = cls(desc, q.codes, q.scales, dev)
+            made += linear.prepared, linear.workspace
+        return linear
 
     def __call__(self, x=None, out=None, stream=None, quantized=None):
         """bf16 [M][N] of x bf16 [M][K], or of `quantized`, the Fp4Tensor (or its

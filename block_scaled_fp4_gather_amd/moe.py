@@ -302,16 +302,14 @@ class Fp4MoE:
         """The layer of bf16 or fp32 experts, w13 [E][2 I][H] (relu2: [E][I][H]) and
         w2 [E][H][I], quantised on the GPU (experts.fp4_quantize); NVFP4 with a
         global scale per expert and matrix."""
-        from . import experts
+        from . import block, experts
 
-        if stream is not None:
-            stream = as_stream(stream, w13.device)
-            for t in (w13, w2):
-                t.record_stream(stream)
-            with torch.cuda.stream(stream):
-                return cls.from_float(desc, w13, w2, device)
-        q13, q2 = (experts.fp4_quantize(t.to(device).contiguous(), desc.fmt) for t in (w13, w2))
-        return cls(desc, q13.codes, q13.scales, q2.codes, q2.scales, q13.global_scale, q2.global_scale, device)
+        dev = block._device(device)
+        with preparing(as_stream(stream, dev), dev, w13, w2) as made:
+            q13, q2 = (experts.fp4_quantize(t.to(dev).contiguous(), desc.fmt) for t in (w13, w2))
+            layer = cls(desc, q13.codes, q13.scales, q2.codes, q2.scales, q13.global_scale, q2.global_scale, dev)
+            made += layer.prepared, layer.workspace
+        return layer
 
     def __call__(self, x, ids, w, out=None, stream=None, tuning=None, phases=None):
         if out is None:

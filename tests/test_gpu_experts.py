@@ -746,6 +746,32 @@ def test_calls_on_a_given_stream():
     assert torch.equal(y.grad, (groups.place >= 0).sum(1, keepdim=True).expand(50, 128).bfloat16())
 
 
+@pytest.mark.parametrize("where", ["cpu", "cuda"])
+def test_made_from_floats_on_a_given_stream(where):
+    """In order with the current stream before and after: the weights are still
+    on their way when the objects are made, which are used at once."""
+    M, H, I, E, k = 20, 128, 64, 8, 3
+    x, ids, w, w13, w2 = layer_inputs(M, H, I, E, k, seed=61)
+    x = x.detach()
+    desc, up = moe.Desc("nvfp4", E, H, I, k, M), experts.Fp4Desc(H, I, M, fn="silu")
+    want = moe.Fp4MoE.from_float(desc, w13, w2)(x, ids, w), experts.Fp4Linear.from_float(up, w13[0])(x)
+    side = torch.cuda.Stream()
+    given = [t.detach().to(where) for t in (w13, w2)]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(10_000_000)
+    if where == "cuda":
+        late = [torch.zeros_like(t) for t in given]
+        for a, b in zip(late, given):
+            a.copy_(b)
+        given = late
+    layer = moe.Fp4MoE.from_float(desc, *given, stream=side)
+    linear = experts.Fp4Linear.from_float(up, given[0][0], stream=side.cuda_stream)
+    del given
+    got = layer(x, ids, w), linear(x)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_captured_and_replayed():
     """A forward and backward pass in a graph, replayed on new inputs with eager
     work in between, against eager calls."""
