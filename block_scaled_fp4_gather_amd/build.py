@@ -8,9 +8,11 @@ know the feature, which is harmless.
 """
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -22,22 +24,30 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 
-def command(out: str) -> list[str]:
-    return [HIPCC, f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
-            "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-            "-Wall", "-Wno-unused-command-line-argument",
-            "-o", out] + [os.path.join(CSRC, s) for s in SOURCES]
+FLAGS = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
+         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+         "-Wall", "-Wno-unused-command-line-argument"]
 
 
-def build(verbose: bool = False) -> str:
-    tmp = LIB + ".tmp"
-    cmd = command(tmp)
+def _run(cmd: list[str], verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError("hipcc failed building libmoe_fp4.so")
+        raise RuntimeError(f"hipcc failed building {os.path.basename(cmd[-1])}")
+
+
+def build(verbose: bool = False) -> str:
+    """Compiles the sources side by side, up to 8 (or MAX_JOBS) at a time, and links them."""
+    tmp = LIB + ".tmp"
+    jobs = max(1, min(8, int(os.environ.get("MAX_JOBS") or os.cpu_count() or 1)))
+    with tempfile.TemporaryDirectory() as d:
+        objects = [os.path.join(d, s + ".o") for s in SOURCES]
+        with concurrent.futures.ThreadPoolExecutor(jobs) as pool:
+            list(pool.map(lambda s, o: _run([HIPCC, *FLAGS, "-c", "-o", o, os.path.join(CSRC, s)], verbose),
+                          SOURCES, objects))
+        _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-o", tmp, *objects], verbose)
     os.replace(tmp, LIB)
     return LIB
 

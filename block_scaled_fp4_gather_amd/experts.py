@@ -19,7 +19,9 @@ so that a layer of bf16 experts is
 and ``moe.Fp4MoE.from_float`` makes the FP4 layer of the same weights.
 
 Argument marshalling only, as in ``moe``; every step runs in the HIP library.
-Calls run on the current stream of the tensors' device unless given one.
+Calls run on the current stream of the tensors' device unless given one.  A
+graph that captures a backward pass takes its leaves' gradients by
+``torch.autograd.grad``, or of leaves that no eager graph holds any more.
 """
 from __future__ import annotations
 
