@@ -14,6 +14,8 @@
 
 namespace moe {
 
+constexpr int kMaxCols = 1 << 20;  // values of a row that is quantised or multiplied
+
 // ---------------------------------------------------------------- quantisation
 
 struct QuantArgs {

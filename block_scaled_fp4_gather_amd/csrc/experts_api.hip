@@ -39,7 +39,6 @@ bool overlapping(std::initializer_list<Range> in, std::initializer_list<Range> o
 bool format_ok(int32_t f) { return f == MOE_FP4_MXFP4 || f == MOE_FP4_NVFP4; }
 bool type_ok(int32_t t) { return t == MOE_FP4_TYPE_BF16 || t == MOE_FP4_TYPE_F32; }
 
-constexpr int kMaxCols = 1 << 20;
 constexpr int64_t kMaxValues = (int64_t)1 << 40;  // of a quantised tensor
 
 // experts * rows * stride without overflow, or -1 where it passes kMaxValues.
@@ -60,7 +59,7 @@ moe_fp4_status linear_shape(const moe_fp4_linear_desc* d, moe::Fp4Shape* s) {
   if (d->act_fn == MOE_FP4_FN_SWIGLUOAI &&
       (!std::isfinite(d->act_alpha) || !std::isfinite(d->act_beta) || !(d->act_limit > 0.0f)))
     return MOE_FP4_EINVAL;
-  if (d->in_features > kMaxCols || d->out_features > kMaxOutFeatures ||
+  if (d->in_features > moe::kMaxCols || d->out_features > kMaxOutFeatures ||
       (int64_t)d->in_features * d->out_features > (int64_t)1 << 31 || d->max_tokens > kMaxTokens)
     return MOE_FP4_EUNSUPPORTED;
   const bool act = d->act_fn != MOE_FP4_FN_NONE;
@@ -125,7 +124,7 @@ moe_fp4_status grouped_shape(const moe_fp4_grouped_desc* d, int32_t rows) {
       d->out_features % 8 || rows < 0)
     return MOE_FP4_EINVAL;
   if (d->weight_layout != MOE_FP4_WEIGHT_OUT_IN && d->weight_layout != MOE_FP4_WEIGHT_IN_OUT) return MOE_FP4_EINVAL;
-  if (d->num_experts > moe::kGroupMaxExperts || d->in_features > kMaxCols || d->out_features > kMaxCols ||
+  if (d->num_experts > moe::kGroupMaxExperts || d->in_features > moe::kMaxCols || d->out_features > moe::kMaxCols ||
       rows > moe::kGroupMaxRoutes)
     return MOE_FP4_EUNSUPPORTED;
   return MOE_FP4_OK;
@@ -152,7 +151,7 @@ moe_fp4_status moe_fp4_quantize(int32_t format, int32_t type, const void* x, int
   if (cols % G || row_stride < cols || row_stride % (16 / size)) return MOE_FP4_EINVAL;
   if (nv ? (global_scale != nullptr) == (global_out != nullptr) : global_scale || global_out) return MOE_FP4_EINVAL;
   const int64_t n = values(experts, rows, row_stride);
-  if (cols > kMaxCols || n < 0) return MOE_FP4_EUNSUPPORTED;
+  if (cols > moe::kMaxCols || n < 0) return MOE_FP4_EUNSUPPORTED;
   if (n == 0) return MOE_FP4_OK;
   if (!x || !codes || !scales || !aligned(x, 16) || !aligned(codes, 16) || !aligned(global_scale, 4) ||
       !aligned(global_out, 4))
@@ -188,7 +187,7 @@ moe_fp4_status moe_fp4_dequantize(int32_t format, int32_t type, const uint8_t* c
   const int G = nv ? 16 : 32;
   if (cols % G || nv != (global_scale != nullptr)) return MOE_FP4_EINVAL;
   const int64_t n = values(experts, rows, cols);
-  if (cols > kMaxCols || n < 0) return MOE_FP4_EUNSUPPORTED;
+  if (cols > moe::kMaxCols || n < 0) return MOE_FP4_EUNSUPPORTED;
   if (n == 0) return MOE_FP4_OK;
   if (!codes || !scales || !out || !aligned(codes, 16) || !aligned(out, 16) || !aligned(global_scale, 4))
     return MOE_FP4_EINVAL;

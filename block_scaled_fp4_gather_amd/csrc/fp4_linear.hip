@@ -393,6 +393,9 @@ struct Fp4Op {
 template <class T>
 constexpr int kFp4Lds = T::kRing + 2 * Fp4Op<T>::kRing;
 
+// Outputs of a token, at most, of which a fragment's 32 rows are one buffer (TileOut).
+constexpr int kTileMaxN = kOutside / (32 * 2);
+
 struct TileArgs {
   Fp4Shape s;
   const uint8_t* prepared;
@@ -479,13 +482,16 @@ struct LinearWork {
     const ActParams act = {a.s.act.kind, a.s.act.alpha, a.s.act.beta, a.s.act.limit};
     constexpr int kCols = GATED ? 16 : 32;  // outputs of a fragment
     const int m0 = row0, N = a.s.N, n1 = (int)col0 / (GATED ? 2 : 1) + wn * T::FN * kCols;
-    const TileOut o(a.out + (int64_t)m0 * N + n1, 2ll * N, min(T::BM, a.M - m0));
     auto put = [&](auto kind) __attribute__((always_inline)) {
       constexpr int kKind = decltype(kind)::value;
 #pragma unroll
       for (int t = 0; t < A; ++t) {
         hold<T>(acc, t);
-        const uint32_t row = ((t * T::WM + wm) * 32 + (threadIdx.x & 31)) * o.ld;
+        // a buffer for each fragment: a whole tile's rows of a wide map pass 32 bits
+        // (8192 7168 2 x 2048: 145 us, 143 with one for the tile)
+        const int m = m0 + (t * T::WM + wm) * 32;
+        const TileOut o(a.out + (int64_t)m * N + n1, 2ll * N, max(min(32, a.M - m), 0));
+        const uint32_t row = (threadIdx.x & 31) * o.ld;
 #pragma unroll
         for (int f = 0; f < T::FN; ++f) {
           store_fragment(o, row + 2 * kCols * f, N - n1 - kCols * f, kCols / 8, [&](int i) __attribute__((always_inline)) {
@@ -595,12 +601,14 @@ hipError_t launch_fp4_linear(const Fp4Shape& s, const uint8_t* prepared, const u
   // read the tokens less often (us with the tokens' quantisation, 32 x 64 / 64 x
   // 64 outputs / tiles; M K N: 64 4096 4096 8.9 / 10.0 / 16.5, 192 4096 4096 11.9 /
   // 10.8 / 18.6, 512 4096 4096 19.8 / 18.4 / 19.8, 512 7168 2 x 2048 25 / 23 / 30,
-  // 768 4096 4096 27 / 25 / 21.7, 384 2048 7168 16 / 17 / 14.3).
+  // 768 4096 4096 27 / 25 / 21.7, 384 2048 7168 16 / 17 / 14.3).  More features than
+  // a tile can store go the same way, with 64-bit addresses, whatever it takes (256
+  // 64 2^25: 31.8 ms / 10.5 in tiles).
   if (M <= 16) return ks > 8 ? MOE_FEW(1, 1, 16, 1, false) : MOE_FEW(1, 1, 4, 1, false);
   if (M <= 32) return MOE_FEW(2, 2, 8, 1, false);
   const int64_t wide = (M + 63) / 64;
   if (wide * ((s.subtiles() + 1) / 2) <= 256) return MOE_FEW(2, 4, 8, 1, false);
-  if (wide * ((s.subtiles() + 3) / 4) <= 512) return MOE_FEW(4, 4, 8, 1, false);
+  if (wide * ((s.subtiles() + 3) / 4) <= 512 || s.N > kTileMaxN) return MOE_FEW(4, 4, 8, 1, false);
 #undef MOE_FEW
   // 256 x 256 tiles move half the bytes into LDS, 128 x 128 ones fill the chip
   // sooner, two a CU (us, 128 / 256; M K N: 2048 4096 4096, 512 tiles of 128, 33 /

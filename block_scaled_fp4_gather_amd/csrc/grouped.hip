@@ -23,6 +23,8 @@
 namespace moe {
 namespace {
 
+static_assert(256ll * 4 * kMaxCols <= kOutside, "a tile's rows, of operands and of fp32 outputs, are one buffer");
+
 // Rows of expert e, whatever the offsets hold: within [0, rows] and not
 // negative in number.
 __device__ __forceinline__ void expert_rows(const int32_t* offsets, int e, int64_t rows, int& a, int& b) {

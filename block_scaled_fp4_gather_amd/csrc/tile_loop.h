@@ -82,7 +82,9 @@ __device__ __forceinline__ i32x4_t scalar(const i32x4_t& b) {
   return i32x4_t{__builtin_amdgcn_readfirstlane(b[0]), __builtin_amdgcn_readfirstlane(b[1]),
                  __builtin_amdgcn_readfirstlane(b[2]), __builtin_amdgcn_readfirstlane(b[3])};
 }
-constexpr uint32_t kOutside = 0x80000000u;  // an offset past every buffer's end (2^30 bytes at most)
+// Offsets into a buffer are 32 bits wide, and kOutside has to be past its end:
+// whoever makes one keeps it within that many bytes.
+constexpr uint32_t kOutside = 0x80000000u;
 
 // Direct copy as in gemm_util.h from a buffer: lane l's 16 bytes at off + scalar
 // land at LDS byte lds + 16 l.  One wave of a SIMD has to issue all of its own
@@ -440,8 +442,8 @@ __device__ __forceinline__ void hold(f32x16_t (&acc)[T::FN][A], int t) {
   for (int f = 0; f < T::FN; ++f) asm volatile("" : "+a"(acc[f][t]));
 }
 
-// A tile's outputs, rows of `ld` bytes from its first on: stores past the last
-// row or the matrix's last column do nothing.
+// A tile's outputs, rows of `ld` bytes from its first on (rows * ld: kOutside at
+// most): stores past the last row or the matrix's last column do nothing.
 struct TileOut {
   __amdgpu_buffer_rsrc_t buffer;
   uint32_t ld;

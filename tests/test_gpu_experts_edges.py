@@ -1,0 +1,90 @@
+"""Ends of the ranges that include/moe_fp4.h gives for FP4 quantisation, the
+MXFP4 linear map, grouped products and the routes' calls."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import experts_ref as ref
+from block_scaled_fp4_gather_amd import experts
+from gpu_util import say
+from test_gpu_experts import linear_bound, rand
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _announce(request):
+    say(f"\n[gpu] {request.node.nodeid}")
+    yield
+
+
+# ---------------------------------------------------------------- very wide maps
+
+def wide_map(M, N, fn="none", K=32):
+    """A map whose outputs are exact: one block of 32, so that an output is a sum
+    of 32 quarters of whole numbers below 36, times a power of two."""
+    g = torch.Generator(device="cuda").manual_seed(N)
+    desc = experts.Fp4Desc(K, N, M, fn)
+    codes = torch.empty(desc.rows, K // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(desc.rows, K // 32, dtype=torch.uint8, device="cuda")
+    for a in range(0, desc.rows, 1 << 24):
+        codes[a:a + (1 << 24)].random_(0, 256, generator=g)
+        scales[a:a + (1 << 24)].random_(120, 126, generator=g)
+    return experts.Fp4Linear(desc, codes, scales), codes, scales
+
+
+def values(codes, scales):
+    return experts.fp4_dequantize((codes, scales), "mxfp4", torch.float32)
+
+
+def check_wide(lin, codes, scales, x, rows):
+    """Every output of the given rows, those that the call did not write
+    among them; nothing around the outputs is touched."""
+    M, N = x.shape[0], lin.desc.N
+    big = torch.full((M * N + 2048,), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = big[1024:-1024].view(M, N)
+    out.fill_(float("nan"))
+    lin(x, out=out)
+    assert bool((big[:1024] == 7).all()) and bool((big[-1024:] == 7).all())
+    q = experts.fp4_quantize(x[rows].contiguous())
+    xv = values(q.codes, q.scales)
+    for a in range(0, N, 1 << 20):
+        want = (xv @ values(codes[a:a + (1 << 20)], scales[a:a + (1 << 20)]).t()).bfloat16()
+        assert torch.equal(out[rows, a:a + (1 << 20)], want), a
+    last = slice(N - 24, N)
+    exact, _ = ref.linear(q.codes.cpu(), q.scales.cpu(), codes[last].cpu(), scales[last].cpu())
+    assert torch.equal(out[rows, last].cpu(), exact.bfloat16())
+
+
+# Outputs of 256 tokens that are 2^30 bytes, and past them: 2^31 and 2^32, with a
+# last tile that is cut; of 32 tokens that are 2^31 bytes, and past them.
+@pytest.mark.parametrize("M,N", [(257, 1 << 21), (257, (1 << 21) + 8), (300, 4194312), (256, 1 << 23), (70, 1 << 25),
+                                 (70, (1 << 25) + 8), (33, 1 << 26)])
+def test_linear_of_very_many_features(M, N):
+    lin, codes, scales = wide_map(M, N)
+    rows = torch.tensor(sorted({0, 1, 31, 32, M // 2, M - 2, M - 1}), device="cuda")
+    check_wide(lin, codes, scales, rand(2, M, 32).bfloat16().cuda(), rows)
+
+
+def test_linear_of_very_many_features_and_tokens():
+    """2^35 outputs, in more than 2^32 threads."""
+    M, N = 513, 1 << 26
+    lin, codes, scales = wide_map(M, N)
+    check_wide(lin, codes, scales, rand(2, M, 32).bfloat16().cuda(), torch.tensor([0, 63, 64, 511, 512], device="cuda"))
+
+
+# Gated: outputs past 2^31 bytes in a tile.
+@pytest.mark.parametrize("M,N", [(300, (1 << 22) + 8)])
+def test_gated_linear_of_very_many_features(M, N):
+    lin, codes, scales = wide_map(M, N, "silu")
+    x = rand(2, M, 32).bfloat16().cuda()
+    out = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lin(x, out=out)
+    assert not any(bool(torch.isnan(row).any()) for row in out)
+    q = experts.fp4_quantize(x)
+    some = torch.cat([torch.arange(40), torch.arange(N // 2 - 20, N // 2 + 20), torch.arange(N - 40, N)])
+    both = torch.cat([some, N + some]).cuda()
+    exact, s = ref.linear(q.codes.cpu(), q.scales.cpu(), codes[both].cpu(), scales[both].cpu())
+    want, tol = linear_bound(exact, s, len(some), "silu", 32)
+    assert bool(((out[:, some.cuda()].cpu().double() - want).abs() <= tol).all())
