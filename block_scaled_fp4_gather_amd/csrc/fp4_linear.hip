@@ -583,7 +583,8 @@ hipError_t launch_fp4_linear(const Fp4Shape& s, const uint8_t* prepared, const u
   const Tokens t{packed, pscales, x};
   const int ks = s.ksteps();
 #define MOE_FEW(...) launch_few<__VA_ARGS__>(s, prepared, t, M, out, st)
-  if (x && M <= 4 && M * ks * 8 <= kFusedUnits<16>) {
+  // (a launch has fewer than 2^32 threads along x)
+  if (x && M <= 4 && M * ks * 8 <= kFusedUnits<16> && s.subtiles() < 1 << 23) {
     if (M * ks * 8 <= kFusedUnits<8>) return ks > 8 ? MOE_FEW(1, 1, 8, 4, true) : MOE_FEW(1, 1, 8, 1, true);
     return s.gated ? MOE_FEW(2, 1, 16, 2, true) : MOE_FEW(1, 1, 16, 2, true);
   }
