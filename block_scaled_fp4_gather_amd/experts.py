@@ -22,6 +22,8 @@ Argument marshalling only, as in ``moe``; every step runs in the HIP library.
 Calls run on the current stream of the tensors' device unless given one.  A
 graph that captures a backward pass takes its leaves' gradients by
 ``torch.autograd.grad``, or of leaves that no eager graph holds any more.
+Gradients are those of reverse mode: tensors with a forward-mode tangent are
+refused.
 """
 from __future__ import annotations
 
@@ -31,6 +33,7 @@ import functools
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd import forward_ad
 
 from . import moe
 from .block import _TORCH_TYPES, FNS, _device, _empty, _launch, _need, _sized
@@ -83,6 +86,13 @@ def _on(stream, call, *tensors):
 def _check_gpu(t, what):
     if not t.is_cuda:
         raise ValueError(f"{what} is on {t.device}, not on a GPU")
+
+
+def _no_tangents(name, *tensors):
+    """Refuses dual tensors, whose derivative would get lost: they require no gradient."""
+    if forward_ad._current_level >= 0 and any(
+            t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise NotImplementedError(f"{name} has no forward-mode derivative")
 
 
 # ---------------------------------------------------------------- quantisation
@@ -355,6 +365,7 @@ def gather_routes(x, groups: RouteGroups, stream=None):
     in the rows of no route.  Differentiable in x."""
     if stream is not None:
         return _on(stream, lambda: gather_routes(x, groups), x, *groups)
+    _no_tangents("gather_routes", x)
     _check_gpu(x, "x")
     if x.dim() != 2 or groups.place.shape[0] != x.shape[0]:
         raise ValueError(f"x: want [{groups.place.shape[0]}][H], got {list(x.shape)}")
@@ -368,6 +379,7 @@ def combine_routes(y, groups: RouteGroups, w=None, stream=None):
     fp32 [M][k] (ones if left out).  Differentiable in y and w."""
     if stream is not None:
         return _on(stream, lambda: combine_routes(y, groups, w), y, w, *groups)
+    _no_tangents("combine_routes", y, w)
     _check_gpu(y, "y")
     if torch.is_grad_enabled() and (y.requires_grad or (w is not None and w.requires_grad)):
         return _CombineRoutes.apply(y, groups.order, groups.place, w)
@@ -418,6 +430,7 @@ def grouped_linear(x, w, offsets, out=None, stream=None):
     `out`)."""
     if stream is not None:
         return _on(stream, lambda: grouped_linear(x, w, offsets, out), x, w, offsets, out)
+    _no_tangents("grouped_linear", x, w)
     _check_gpu(x, "x")
     if w.dim() != 3 or x.dim() != 2:
         raise ValueError(f"want x [T][K] and w [E][N][K], got {list(x.shape)} and {list(w.shape)}")
@@ -433,6 +446,7 @@ def grouped_weight_grad(dy, x, offsets, dtype=torch.bfloat16, out=None, stream=N
     bf16 [T][N] and x bf16 [T][K]; zeros for an expert without rows."""
     if stream is not None:
         return _on(stream, lambda: grouped_weight_grad(dy, x, offsets, dtype, out), dy, x, offsets, out)
+    _no_tangents("grouped_weight_grad", dy, x)
     _check_gpu(dy, "dy")
     if dtype not in _TORCH_TYPES or dy.dim() != 2 or x.dim() != 2:
         raise ValueError(f"want bf16 or fp32 of dy [T][N] and x [T][K], got {dtype} of {list(dy.shape)} and {list(x.shape)}")

@@ -7,6 +7,7 @@ import ctypes
 
 import pytest
 import torch
+from torch.autograd import forward_ad
 
 from block_scaled_fp4_gather_amd import experts, moe
 
@@ -161,3 +162,26 @@ def test_python_refusals():
               lambda: experts.fp4_quantize(cpu[0]), lambda: experts.group_routes(torch.zeros(4, 2), 8)):
         with pytest.raises(ValueError):
             f()
+
+
+def test_forward_mode_derivatives_are_refused():
+    """A dual tensor requires no gradient, so nothing else keeps its tangent from
+    getting lost; with or without one that does beside it, and where gradients
+    are switched off."""
+    bf = torch.zeros(4, 64, dtype=torch.bfloat16)
+    w3, off = torch.zeros(2, 8, 64, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)
+    groups = experts.RouteGroups(off, torch.zeros(4, dtype=torch.int32), torch.zeros(4, 1, dtype=torch.int32))
+    cases = [(experts.gather_routes, (bf, groups), (0,)), (experts.combine_routes, (bf, groups, torch.zeros(4, 1)), (0, 2)),
+             (experts.grouped_linear, (bf, w3, off), (0, 1)), (experts.grouped_weight_grad, (bf, bf, off), (0, 1))]
+    for f, args, inputs in cases:
+        for i in inputs:
+            for other in (False, True):
+                given = [a.clone().requires_grad_() if other and isinstance(a, torch.Tensor) and a.is_floating_point() else a
+                         for a in args]
+                with forward_ad.dual_level():
+                    given[i] = forward_ad.make_dual(args[i].clone(), torch.ones_like(args[i]))
+                    for grad in (False, True):
+                        with torch.set_grad_enabled(grad), pytest.raises(NotImplementedError, match="forward-mode"):
+                            f(*given)
+        with forward_ad.dual_level(), pytest.raises(ValueError, match="not on a GPU"):  # no tangent: the checks as ever
+            f(*args)
