@@ -27,8 +27,8 @@ template <int KIND>
 __device__ __forceinline__ float act_of(const ActParams& p, float g, float u) {
   if constexpr (KIND == kActGeluTanh) {
     const float z = 0.7978845608028654f * (g + 0.044715f * g * g * g);
-    const float th = 1.0f - 2.0f / (1.0f + __expf(2.0f * z));  // tanh(z), saturating to +-1
-    return 0.5f * g * (1.0f + th) * u;
+    // (1 + tanh z) / 2 = 1 / (1 + e^-2z), where 1 + tanh would cancel below -4 or so
+    return g / (1.0f + __expf(-2.0f * z)) * u;
   } else if constexpr (KIND == kActSwigluOai) {
     const float gc = g > p.limit ? p.limit : g;
     const float uc = u > p.limit ? p.limit : (u < -p.limit ? -p.limit : u);

@@ -121,7 +121,7 @@ template <int KIND>
 __device__ __forceinline__ float quick_act(const ActParams& p, float g, float u) {
   if constexpr (KIND == kActGeluTanh) {
     const float z = 0.7978845608028654f * (g + 0.044715f * g * g * g);
-    return g * (1.0f - __builtin_amdgcn_rcpf(1.0f + __expf(2.0f * z))) * u;  // 0.5 (1 + tanh z)
+    return g * __builtin_amdgcn_rcpf(1.0f + __expf(-2.0f * z)) * u;
   } else if constexpr (KIND == kActSwigluOai) {
     const float gc = g > p.limit ? p.limit : g;
     const float uc = u > p.limit ? p.limit : (u < -p.limit ? -p.limit : u);

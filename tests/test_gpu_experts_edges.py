@@ -6,9 +6,9 @@ import pytest
 import torch
 
 import experts_ref as ref
-from block_scaled_fp4_gather_amd import experts
+from block_scaled_fp4_gather_amd import block, experts
 from gpu_util import say
-from test_gpu_experts import linear_bound, rand
+from test_gpu_experts import BF16, linear_bound, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -89,3 +89,36 @@ def test_gated_linear_of_very_many_features(M, N):
     exact, s = ref.linear(q.codes.cpu(), q.scales.cpu(), codes[both].cpu(), scales[both].cpu())
     want, tol = linear_bound(exact, s, len(some), "silu", 32)
     assert bool(((out[:, some.cuda()].cpu().double() - want).abs() <= tol).all())
+
+
+# ---------------------------------------------------------------- activations
+
+@pytest.mark.parametrize("M", [1, 3, 20, 100, 600, 2100])
+@pytest.mark.parametrize("kind", ["fp4", "fp8"])
+def test_gelu_of_negative_gates(kind, M):
+    """GELU keeps its digits where it is nearly zero.  The gates -(a + c / 2 + b / 8)
+    are exact, 4 to 9.75; z = sqrt(2 / pi) (g + 0.044715 g^3) goes through seven
+    roundings of 2^-24 and the exponential's argument through two more, and
+    |2 z| is below 81: 81 * 9 * 2^-24 < 2^-14 of the value."""
+    K, N = 128, 2048
+    x = torch.zeros(M, K)
+    x[:, 0], x[:, 1], x[:, 2] = 1.0, 0.125, 0.5
+    g = torch.Generator().manual_seed(M)
+    pick = torch.randint(0, 8, (N, 3), generator=g)
+    pick[:, 0] = torch.randint(6, 8, (N,), generator=g)  # 4 or 6
+    w = torch.zeros(2 * N, K)
+    w[:N, :3] = -ref.E2M1[pick].float()
+    w[N:, 0] = 1.0
+    if kind == "fp4":
+        lin = experts.Fp4Linear.from_float(experts.Fp4Desc(K, N, M, "gelu_tanh"), w.cuda())
+        q = experts.fp4_quantize(w.cuda())
+        assert torch.equal(values(q.codes, q.scales).cpu(), w)
+    else:
+        lin = block.Fp8Linear(block.Fp8Desc(K, N, M, "gelu_tanh"), w.to(torch.float8_e4m3fn).cuda(),
+                              torch.ones(2 * (N // 128), K // 128, device="cuda"))
+    y = lin(x.bfloat16().cuda()).cpu().double()
+    gate = (x.double() @ w.double().t())[:, :N]
+    z = 0.7978845608028654 * (gate + 0.044715 * gate ** 3)
+    want = gate / (1 + torch.exp(-2 * z))
+    err = (y - want).abs() / want.abs()
+    assert float(err.max()) <= BF16 + 2.0 ** -14
