@@ -148,10 +148,18 @@ def _ptr(t: torch.Tensor | None):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _call(name: str, device, stream, *args) -> None:
+    """Entry point `name` with `device` current, which launches go by, on its
+    current stream unless given one."""
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        stream = torch.cuda.current_stream(device)
+    args += ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)),
+    fn = getattr(lib(), name)
+    if device.index is None or device.index == torch.cuda.current_device():
+        check(name, fn(*args))
+    else:
+        with torch.cuda.device(device):
+            check(name, fn(*args))
 
 
 def as_stream(stream, device):
@@ -202,15 +210,15 @@ def workspace_bytes(desc: Desc, M: int) -> int:
 
 
 def prepare(desc: Desc, w13_codes, w13_scales, w2_codes, w2_scales, g13, g2, prepared, stream=None):
-    check("moe_fp4_prepare", lib().moe_fp4_prepare(
-        ctypes.byref(desc.c()), _ptr(w13_codes), _ptr(w13_scales), _ptr(w2_codes), _ptr(w2_scales),
-        _ptr(g13), _ptr(g2), _ptr(prepared), prepared.numel() * prepared.element_size(), _stream(stream)))
+    _call("moe_fp4_prepare", prepared.device, stream,
+          ctypes.byref(desc.c()), _ptr(w13_codes), _ptr(w13_scales), _ptr(w2_codes), _ptr(w2_scales),
+          _ptr(g13), _ptr(g2), _ptr(prepared), prepared.numel() * prepared.element_size())
 
 
 def unprepare(desc: Desc, prepared, w13_codes, w13_scales, w2_codes, w2_scales, g13, g2, stream=None):
-    check("moe_fp4_unprepare", lib().moe_fp4_unprepare(
-        ctypes.byref(desc.c()), _ptr(prepared), _ptr(w13_codes), _ptr(w13_scales), _ptr(w2_codes),
-        _ptr(w2_scales), _ptr(g13), _ptr(g2), _stream(stream)))
+    _call("moe_fp4_unprepare", prepared.device, stream,
+          ctypes.byref(desc.c()), _ptr(prepared), _ptr(w13_codes), _ptr(w13_scales), _ptr(w2_codes),
+          _ptr(w2_scales), _ptr(g13), _ptr(g2))
 
 
 def forward(desc: Desc, prepared, x, ids, w, out, workspace, stream=None, tuning: Tuning | None = None,
@@ -224,22 +232,20 @@ def forward(desc: Desc, prepared, x, ids, w, out, workspace, stream=None, tuning
     if tuning is not None or phases is not None:
         assert ids.dtype == torch.int32
         tp = ctypes.byref(tuning) if tuning is not None else None
-        check("moe_fp4_forward_ex", lib().moe_fp4_forward_ex(*args, tp, 3 if phases is None else phases,
-                                                               _stream(stream)))
+        _call("moe_fp4_forward_ex", x.device, stream, *args, tp, 3 if phases is None else phases)
     elif ids.dtype == torch.int64:
-        check("moe_fp4_forward_i64", lib().moe_fp4_forward_i64(*args, _stream(stream)))
+        _call("moe_fp4_forward_i64", x.device, stream, *args)
     else:
         assert ids.dtype == torch.int32
-        check("moe_fp4_forward", lib().moe_fp4_forward(*args, _stream(stream)))
+        _call("moe_fp4_forward", x.device, stream, *args)
 
 
 def forward_noalloc(desc: Desc, prepared, x, ids, w, out, stream=None):
     """moe_fp4_forward with the library's own 64 MiB workspace (int32 ids):
     the entry point for callers that cannot allocate."""
     assert ids.dtype == torch.int32
-    check("moe_fp4_forward_noalloc", lib().moe_fp4_forward_noalloc(
-        ctypes.byref(desc.c()), _ptr(prepared), _ptr(x), x.shape[0], _ptr(ids), _ptr(w), _ptr(out),
-        _stream(stream)))
+    _call("moe_fp4_forward_noalloc", x.device, stream,
+          ctypes.byref(desc.c()), _ptr(prepared), _ptr(x), x.shape[0], _ptr(ids), _ptr(w), _ptr(out))
 
 
 def plan(desc: Desc, M: int, tuning: Tuning | None = None) -> Tuning:
@@ -253,8 +259,8 @@ def plan(desc: Desc, M: int, tuning: Tuning | None = None) -> Tuning:
 
 
 def dequant_export(desc: Desc, prepared, expert: int, which: int, out, stream=None):
-    check("moe_fp4_dequant_export", lib().moe_fp4_dequant_export(
-        ctypes.byref(desc.c()), _ptr(prepared), expert, which, _ptr(out), _stream(stream)))
+    _call("moe_fp4_dequant_export", prepared.device, stream,
+          ctypes.byref(desc.c()), _ptr(prepared), expert, which, _ptr(out))
 
 
 def mxfp8_quantize(x, codes=None, scales=None, stream=None):
@@ -264,8 +270,7 @@ def mxfp8_quantize(x, codes=None, scales=None, stream=None):
         codes = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
     if scales is None:
         scales = torch.empty((rows, cols // 32), dtype=torch.uint8, device=x.device)
-    check("moe_fp4_mxfp8_quantize", lib().moe_fp4_mxfp8_quantize(
-        _ptr(x), rows, cols, _ptr(codes), _ptr(scales), _stream(stream)))
+    _call("moe_fp4_mxfp8_quantize", x.device, stream, _ptr(x), rows, cols, _ptr(codes), _ptr(scales))
     return codes, scales
 
 

@@ -3,7 +3,9 @@ products and the routes' calls: bad arguments are rejected before any HIP
 call (so these run without a GPU)."""
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import types
 
 import pytest
 import torch
@@ -185,3 +187,55 @@ def test_forward_mode_derivatives_are_refused():
                             f(*given)
         with forward_ad.dual_level(), pytest.raises(ValueError, match="not on a GPU"):  # no tangent: the checks as ever
             f(*args)
+
+
+class _OnSecond:
+    """Stands for a dense tensor on the second of two GPUs."""
+    device = torch.device("cuda:1")
+    shape = (4, 64)
+
+    def __init__(self, dtype=torch.uint8):
+        self.dtype = dtype
+
+    data_ptr = lambda self: A
+    is_contiguous = lambda self: True
+    numel = lambda self: 256
+    element_size = lambda self: 1
+
+
+def test_layer_calls_follow_their_tensors_to_another_device(monkeypatch):
+    """What Fp4MoE and its from_float call on another device than the current one
+    runs there, on that device's current stream, or on the stream that is given."""
+    current, seen = [0], []
+
+    @contextlib.contextmanager
+    def device(d):
+        before, current[0] = current[0], torch.device(d).index
+        yield
+        current[0] = before
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *args: seen.append((name, current[0], args[-1].value)) or 0
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "current_stream",
+                        lambda d=None: types.SimpleNamespace(cuda_stream=1000 + (current[0] if d is None else torch.device(d).index)))
+    monkeypatch.setattr(moe, "lib", lambda: Library())
+    t, desc = _OnSecond(), moe.Desc("mxfp4", 2, 64, 32, 1, 4)
+    i32, i64 = _OnSecond(torch.int32), _OnSecond(torch.int64)
+    calls = {
+        "moe_fp4_prepare": lambda s: moe.prepare(desc, t, t, t, t, None, None, t, s),
+        "moe_fp4_unprepare": lambda s: moe.unprepare(desc, t, t, t, t, t, None, None, s),
+        "moe_fp4_forward": lambda s: moe.forward(desc, t, t, i32, t, t, t, s),
+        "moe_fp4_forward_i64": lambda s: moe.forward(desc, t, t, i64, t, t, t, s),
+        "moe_fp4_forward_ex": lambda s: moe.forward(desc, t, t, i32, t, t, t, s, moe.Tuning()),
+        "moe_fp4_forward_noalloc": lambda s: moe.forward_noalloc(desc, t, t, i32, t, t, s),
+        "moe_fp4_dequant_export": lambda s: moe.dequant_export(desc, t, 0, 0, t, s),
+        "moe_fp4_mxfp8_quantize": lambda s: moe.mxfp8_quantize(t, t, t, s),
+    }
+    for name, call in calls.items():
+        for stream, address in ((None, 1001), (77, 77), (types.SimpleNamespace(cuda_stream=78), 78)):
+            call(stream)
+            assert seen.pop() == (name, 1, address) and current == [0]
