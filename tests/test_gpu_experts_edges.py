@@ -91,6 +91,44 @@ def test_gated_linear_of_very_many_features(M, N):
     assert bool(((out[:, some.cuda()].cpu().double() - want).abs() <= tol).all())
 
 
+# ---------------------------------------------------------------- every bf16 value
+
+def test_quantize_every_bf16_value():
+    """All finite bf16 values under every scale that a block can give them: next
+    to largest magnitudes 2^e and 1.9921875 2^e of the same exponent and of larger
+    ones.  A linear map whose weights are a one in each row gives the values back,
+    whichever kernel quantises its tokens; it may take those below 2^-126 as zeros."""
+    bits = torch.arange(65536, dtype=torch.int32)
+    every = bits.to(torch.int16).view(torch.bfloat16)
+    every = every[torch.isfinite(every)]
+    rows = []
+    mag = every.abs().float()
+    exponent = torch.where(mag > 0, torch.frexp(mag)[1] - 1, torch.full_like(bits[: len(every)], -133)).clamp(min=-133)
+    for up in (0, 1, 2, 3, 4, 9):
+        for m in (1.0, 1.9921875):
+            top = torch.ldexp(torch.full_like(mag, m), (exponent + up).clamp(max=127)).bfloat16()
+            keep = mag <= top.float()
+            block_ = torch.zeros(len(every), 32, dtype=torch.bfloat16)
+            block_[:, 0], block_[:, 1], block_[:, 31] = top, every, -every
+            rows.append(block_[keep])
+    x = torch.cat(rows)
+    x = x[: len(x) // 8 * 8].view(-1, 256)
+    q = experts.fp4_quantize(x.cuda())
+    codes, scales, _ = ref.quantize(x[None], "mxfp4")
+    assert torch.equal(q.scales.cpu(), scales[0]) and torch.equal(q.codes.cpu(), codes[0])
+    assert bool((scales == 0).any()) and int(scales.max()) == 252
+    f32 = experts.fp4_quantize(x.float().cuda())
+    assert torch.equal(f32.codes, q.codes) and torch.equal(f32.scales, q.scales)
+    ones = experts.Fp4Linear.from_float(experts.Fp4Desc(256, 256, len(x)), torch.eye(256))
+    v, xd = values(q.codes, q.scales), x.cuda()
+    tiny = v.abs() < 2.0 ** -126
+    for M, most in ((len(x), 1), (16, 200), (3, 400)):  # tiles, and one launch for up to 4 tokens
+        step = max(len(x) // most, M)
+        for a in range(0, len(x) - M + 1, step):
+            y = ones(xd[a:a + M]).float()
+            assert bool(((y == v[a:a + M]) | (tiny[a:a + M] & (y.abs() < 2.0 ** -126))).all()), (M, a)
+
+
 # ---------------------------------------------------------------- activations
 
 @pytest.mark.parametrize("M", [1, 3, 20, 100, 600, 2100])
