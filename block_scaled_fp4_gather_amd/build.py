@@ -29,13 +29,13 @@ FLAGS = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
          "-Wall", "-Wno-unused-command-line-argument"]
 
 
-def _run(cmd: list[str], verbose: bool) -> None:
+def _run(cmd: list[str], made: str, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError(f"hipcc failed building {os.path.basename(cmd[-1])}")
+        raise RuntimeError(f"hipcc failed building {made}")
 
 
 def build(verbose: bool = False) -> str:
@@ -45,9 +45,9 @@ def build(verbose: bool = False) -> str:
     with tempfile.TemporaryDirectory() as d:
         objects = [os.path.join(d, s + ".o") for s in SOURCES]
         with concurrent.futures.ThreadPoolExecutor(jobs) as pool:
-            list(pool.map(lambda s, o: _run([HIPCC, *FLAGS, "-c", "-o", o, os.path.join(CSRC, s)], verbose),
+            list(pool.map(lambda s, o: _run([HIPCC, *FLAGS, "-c", "-o", o, os.path.join(CSRC, s)], s, verbose),
                           SOURCES, objects))
-        _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-o", tmp, *objects], verbose)
+        _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-o", tmp, *objects], os.path.basename(LIB), verbose)
     os.replace(tmp, LIB)
     return LIB
 

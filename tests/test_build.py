@@ -42,3 +42,15 @@ def test_no_kernel_uses_scratch(tmp_path):
                 bad.append(f"{src}: {name}: {m.group(1)} = {m.group(2)}")
     assert kernels >= 10
     assert not bad, "\n".join(bad)
+
+
+@pytest.mark.parametrize("step,name", [("-c", "router.hip"), ("-shared", "libmoe_fp4.so")])
+def test_a_failed_step_is_named(tmp_path, monkeypatch, step, name):
+    """By the source that did not compile, or by the library that did not link."""
+    compiler = tmp_path / "compiler"
+    compiler.write_text(f"#!/bin/sh\ncase \"$*\" in *{step}*{'router.hip' if step == '-c' else ''}*) exit 1;; esac\n")
+    compiler.chmod(0o755)
+    monkeypatch.setattr(build, "HIPCC", str(compiler))
+    with pytest.raises(RuntimeError, match=f"building {name}"):
+        build.build()
+    assert not os.path.exists(build.LIB + ".tmp")
