@@ -311,8 +311,6 @@ moe_fp4_status moe_fp4_grouped_linear(const moe_fp4_grouped_desc* desc, const ui
   const int E = desc->num_experts, K = desc->in_features, N = desc->out_features;
   if (overlapping({{x, 2ll * rows * K}, {weight, 2ll * E * N * K}, {offsets, 4ll * (E + 1)}}, {{y, 2ll * rows * N}}))
     return MOE_FP4_EINVAL;
-  // row tiles times column tiles are counted in 32 bits
-  if (((int64_t)rows / 128 + E) * ((N + 127) / 128) > 0x7FFFFFFF) return MOE_FP4_EUNSUPPORTED;
   const moe::GroupedArgs a{x, weight, offsets, y, rows, E, K, N, desc->weight_layout == MOE_FP4_WEIGHT_IN_OUT};
   return from_hip(moe::launch_grouped(a, (hipStream_t)stream));
 }

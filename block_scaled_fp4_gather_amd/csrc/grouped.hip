@@ -24,6 +24,7 @@ namespace moe {
 namespace {
 
 static_assert(256ll * 4 * kMaxCols <= kOutside, "a tile's rows, of operands and of fp32 outputs, are one buffer");
+static_assert((kGroupMaxRoutes / 128 + kGroupMaxExperts) * (kMaxCols / 128) <= 0x7FFFFFFF, "tiles are counted in 32 bits");
 
 // Rows of expert e, whatever the offsets hold: within [0, rows] and not
 // negative in number.

@@ -162,7 +162,6 @@ struct RowSource {
     off = (uint32_t)row * bytes + chunk;
     last = (bytes & ~127u) + chunk < bytes ? off : kOutside;
   }
-  __device__ static int steps_of(int k) { return (k + 63) / 64; }
   __device__ __forceinline__ void start(int step) {
     now = scalar(buffer);
     soff = (uint32_t)__builtin_amdgcn_readfirstlane(step * 128);
