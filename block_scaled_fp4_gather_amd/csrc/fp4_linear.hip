@@ -586,7 +586,7 @@ hipError_t launch_fp4_linear(const Fp4Shape& s, const uint8_t* prepared, const u
   // (a launch has fewer than 2^32 threads along x)
   if (x && M <= 4 && M * ks * 8 <= kFusedUnits<16> && s.subtiles() < 1 << 23) {
     if (M * ks * 8 <= kFusedUnits<8>) return ks > 8 ? MOE_FEW(1, 1, 8, 4, true) : MOE_FEW(1, 1, 8, 1, true);
-    return s.gated ? MOE_FEW(2, 1, 16, 2, true) : MOE_FEW(1, 1, 16, 2, true);
+    return MOE_FEW(1, 1, 16, 2, true);
   }
   if (x) {
     hipLaunchKernelGGL(fp4_tokens_kernel, dim3((unsigned)groups, (unsigned)((s.K + 511) / 512)), dim3(256), 0, st, x, M, s.K,
