@@ -13,10 +13,13 @@
 // consecutive outputs of one token.
 //
 // Measured (M tokens, K, N; without the tokens' own quantisation): 8192 7168
-// 2 x 2048 118 us, 4.1 PFLOP/s, what its matrix instructions reach beside the LDS
-// reads and copies at the clock that the power leaves; 37 320 2560 3.8 us and 512
-// 4096 4096 15 us, latency of few steps; 1 7168 2 x 2048 5.2 us with it, 3.0 TB/s
-// of weights.
+// 2 x 2048 118 us, 4.1 PFLOP/s.  By K, 3584 7168 14336, it takes 66 116 216 (and 67
+// 116 215 without the activation, N 4096): 17 us beside the steps, and the steps at
+// 4.9 PFLOP/s, where the instruction alone reaches 6.6 on such data.  The matrix
+// cores are busy 55% of the waves' cycles, and 18% are waits; what the rest is has
+// not been found (LDS moves 192 KB a step, 1536 of 2048 cycles).  37 320 2560 3.8 us
+// and 512 4096 4096 15 us, latency of few steps; 1 7168 2 x 2048 5.2 us with it,
+// 3.0 TB/s of weights.
 #include <hip/hip_runtime.h>
 
 #include "act.h"
@@ -115,7 +118,7 @@ __global__ void __launch_bounds__(256)
 __device__ __forceinline__ i32x8_t wide(const i32x4_t& v) { return i32x8_t{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
 
 // The gated activations of act.h with the hardware's reciprocal (off by a unit
-// in the last place) for their quotients: a tile of 256 x 256 has 128 of them a
+// in the last place; few tokens get the exact one) for their quotients: a tile of 256 x 256 has 128 of them a
 // lane, and nothing beside them.
 template <int KIND>
 __device__ __forceinline__ float quick_act(const ActParams& p, float g, float u) {
@@ -583,7 +586,12 @@ hipError_t launch_fp4_linear(const Fp4Shape& s, const uint8_t* prepared, const u
   const Tokens t{packed, pscales, x};
   const int ks = s.ksteps();
 #define MOE_FEW(...) launch_few<__VA_ARGS__>(s, prepared, t, M, out, st)
-  // (a launch has fewer than 2^32 threads along x)
+  // Up to 4 tokens in one launch, as far as their blocks fit (us, one / two; M K N:
+  // 1 7168 2 x 2048 5.2 / 7.7, 4 4096 4096 5.0 / 6.5, 4 320 2560 4.2 / 5.5), and a
+  // launch has fewer than 2^32 threads along x.  8 waves where they hold the
+  // blocks (8 / 16: 1 7168 2 x 2048 5.2 / 6.2, 1 2048 7168 5.0 / 6.9), with four
+  // steps of each in flight where it has more than one (4 / 1: 1 7168 2 x 2048 5.2
+  // / 5.5, 1 4096 4096 4.5 / 4.6; where it has one 1 2048 7168 5.3 / 5.0).
   if (x && M <= 4 && M * ks * 8 <= kFusedUnits<16> && s.subtiles() < 1 << 23) {
     if (M * ks * 8 <= kFusedUnits<8>) return ks > 8 ? MOE_FEW(1, 1, 8, 4, true) : MOE_FEW(1, 1, 8, 1, true);
     return MOE_FEW(1, 1, 16, 2, true);
@@ -598,7 +606,12 @@ hipError_t launch_fp4_linear(const Fp4Shape& s, const uint8_t* prepared, const u
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  // Few tokens: the waves of a workgroup share K, and workgroups of more outputs
+  // Up to 16 tokens: 16 waves where there are steps for them (us, 16 / 4; M K N: 16
+  // 4096 4096 6.6 / 7.0, 16 7168 2 x 2048 7.9 / 8.3, 16 2048 7168 6.7 / 6.3, 16 320
+  // 2560 5.8 / 5.5), 16 x 16 outputs (the form for 32: 7.4, 8.6, 6.5, 5.8).  Up to
+  // 32: 32 x 32 outputs (as up to 16, and as from 33 on: 32 7168 2 x 2048 8.9 / 10.8
+  // / 10.0, 32 2048 7168 6.7 / 7.0 / 7.1, but 32 320 2560 6.3 / 5.7 / 6.3).
+  // More tokens: the waves of a workgroup share K, and workgroups of more outputs
   // read the tokens less often (us with the tokens' quantisation, 32 x 64 / 64 x
   // 64 outputs / tiles; M K N: 64 4096 4096 8.9 / 10.0 / 16.5, 192 4096 4096 11.9 /
   // 10.8 / 18.6, 512 4096 4096 19.8 / 18.4 / 19.8, 512 7168 2 x 2048 25 / 23 / 30,
@@ -614,7 +627,8 @@ hipError_t launch_fp4_linear(const Fp4Shape& s, const uint8_t* prepared, const u
   // 256 x 256 tiles move half the bytes into LDS, 128 x 128 ones fill the chip
   // sooner, two a CU (us, 128 / 256; M K N: 2048 4096 4096, 512 tiles of 128, 33 /
   // 40; 1536 2048 7168, 672, 27 / 29; 2048 2048 7168, 896, 33 / 31; 4096 4096 4096,
-  // 1024, 55 / 49; 8192 7168 2 x 2048, 2048, 174 / 141).
+  // 1024, 55 / 49; 8192 7168 2 x 2048, 2048, 174 / 141).  The rule does not see K:
+  // with few steps the small ones stay ahead (8192 320 2560, 1280, 23.7 / 28.3).
   if ((M + 127) / 128 * (int64_t)((s.subtiles() + 7) / 8) <= 3 * 256)
     return launch_tile<Tile<128, 128, 2, 2, 2>>(s, prepared, t, M, out, st);
   return launch_tile<Tile<256, 256, 2, 2, 2>>(s, prepared, t, M, out, st);

@@ -482,6 +482,10 @@ using Deep = Tile<128, 128, 2, 2, S, S>;
 // all of its LDS (five slots / 3 and 2 and two a CU: 256 64 7168 512 86 / 97, 8 64
 // 4096 4096 44 / 48, 8 2000 512 264 9.9 / 9.4; where there are more, 4 8000 1024
 // 1024 39 / 31).
+// The rules count tiles, however full they are: large ones that are half empty
+// lose (256 x 256 / the small ones: 256 32768 1024 128 47 / 30, 256 4096 1024 128 23
+// / 19.5; gradient of x of 32 2060 2560 640 32 / 27; of W, below, of the first two
+// 35 / 30 and 23 / 19.5).
 hipError_t launch_grouped(const GroupedArgs& a, hipStream_t st) {
   const int64_t tiny = row_tiles(a, 16);
   if (!a.w_kn && tiny * ceil_div(a.N, 128) < 256) {

@@ -519,8 +519,10 @@ moe_fp4_status moe_fp4_dequantize(int32_t format, int32_t type, const uint8_t* c
  *     y[n] = sum_k q(x)[k] * W[n][k]
  * where q(x) is x as moe_fp4_quantize gives it, on the matrix instruction's
  * form for two FP4 operands, with fp32 sums (a sum below 2^-126 may count as
- * zero).  An activation where asked for
- * (the gated ones over gate and up rows), one rounding to bf16.  A block of x
+ * zero).  An activation where asked for (the gated ones over gate and up rows),
+ * one rounding to bf16.  M chooses the order of the sums and how the activation's
+ * quotient is taken (divided, or multiplied by a reciprocal that may be off by
+ * 2^-23 of itself), so that a token's last bit may change with M.  A block of x
  * that holds a NaN or an infinity makes its token's outputs NaN; other tokens
  * are not touched. */
 typedef struct {
