@@ -485,16 +485,18 @@ struct LinearWork {
     const ActParams act = {a.s.act.kind, a.s.act.alpha, a.s.act.beta, a.s.act.limit};
     constexpr int kCols = GATED ? 16 : 32;  // outputs of a fragment
     const int m0 = row0, N = a.s.N, n1 = (int)col0 / (GATED ? 2 : 1) + wn * T::FN * kCols;
+    // a buffer for each fragment: a whole tile's rows of a wide map pass 32 bits
+    // (8192 7168 2 x 2048: 148.3 us a call both ways)
+    const uint32_t ld = 2u * (uint32_t)N, row = (threadIdx.x & 31) * ld;
+    const uint8_t* const first = uniform(a.out + (int64_t)(m0 + wm * 32) * N + n1);
+    const uint64_t gap = 32ull * T::WM * ld;
+    const int left = __builtin_amdgcn_readfirstlane(a.M - m0 - wm * 32);
     auto put = [&](auto kind) __attribute__((always_inline)) {
       constexpr int kKind = decltype(kind)::value;
 #pragma unroll
       for (int t = 0; t < A; ++t) {
         hold<T>(acc, t);
-        // a buffer for each fragment: a whole tile's rows of a wide map pass 32 bits
-        // (8192 7168 2 x 2048: 145 us, 143 with one for the tile)
-        const int m = m0 + (t * T::WM + wm) * 32;
-        const TileOut o(a.out + (int64_t)m * N + n1, 2ll * N, max(min(32, a.M - m), 0));
-        const uint32_t row = (threadIdx.x & 31) * o.ld;
+        const TileOut o(first + t * gap, ld, max(min(32, left - t * 32 * T::WM), 0));
 #pragma unroll
         for (int f = 0; f < T::FN; ++f) {
           store_fragment(o, row + 2 * kCols * f, N - n1 - kCols * f, kCols / 8, [&](int i) __attribute__((always_inline)) {

@@ -447,7 +447,9 @@ struct TileOut {
   __amdgpu_buffer_rsrc_t buffer;
   uint32_t ld;
   __device__ TileOut(const void* first, int64_t ld_bytes, int rows) : ld((uint32_t)ld_bytes) {
-    buffer = __builtin_amdgcn_make_buffer_rsrc((void*)uniform(first), 0, (int)((uint32_t)rows * ld), 0x00020000);
+    // (a size that the compiler does not know to be uniform would cost a loop at each store)
+    buffer = __builtin_amdgcn_make_buffer_rsrc((void*)uniform(first), 0,
+                                               __builtin_amdgcn_readfirstlane((int)((uint32_t)rows * ld)), 0x00020000);
   }
   __device__ __forceinline__ void put(const u32x4& v, uint32_t off) const {
     __builtin_amdgcn_raw_buffer_store_b128(v, buffer, off, 0, 0);
