@@ -9,6 +9,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import dataclasses
+import math
 import os
 
 import torch
@@ -78,10 +79,18 @@ class Desc:
     limit: float = 0.0
     scales: str = "plain"
 
+    def _format(self):
+        return FORMATS.get(self.fmt, self.fmt) if isinstance(self.fmt, str) else self.fmt
+
+    def weights(self):
+        """Shapes of the weights, W13 and W2 (moe_fp4_prepare)."""
+        gated = self.fn not in ("relu2", FN_RELU2)
+        return (self.E, (1 + gated) * self.I, self.H), (self.E, self.H, self.I)
+
     def c(self) -> _Desc:
         act = ACT_FORMATS.get(self.act, self.act) if isinstance(self.act, str) else self.act
         fn = ACT_FNS.get(self.fn, self.fn) if isinstance(self.fn, str) else self.fn
-        return _Desc(FORMATS.get(self.fmt, self.fmt) if isinstance(self.fmt, str) else self.fmt,
+        return _Desc(self._format(),
                      self.E, self.H, self.I, self.k, self.max_tokens, act, fn,
                      self.alpha, self.beta, self.limit, SCALE_FORMATS.get(self.scales, self.scales)
                      if isinstance(self.scales, str) else self.scales)
@@ -285,6 +294,15 @@ class Fp4MoE:
         if stream is not None and dev.index is None:
             dev = torch.device(dev.type, torch.cuda.current_device())
         stream = as_stream(stream, dev)
+        n = prepared_bytes(desc)  # checks the descriptor
+        # the library takes addresses: fewer values would be read past their end
+        group = 32 if desc._format() == MXFP4 else 16
+        values = [math.prod(s) for s in desc.weights()]
+        for name, a, want in (("w13_codes", w13_codes, values[0] // 2), ("w13_scales", w13_scales, values[0] // group),
+                              ("w2_codes", w2_codes, values[1] // 2), ("w2_scales", w2_scales, values[1] // group),
+                              ("g13", g13, desc.E), ("g2", g2, desc.E)):
+            if a is not None and math.prod(a.shape) != want:
+                raise ValueError(f"{name}: want {want} values, got {list(a.shape)}")
 
         def dev_t(a, dtype):
             if a is None:
@@ -296,7 +314,7 @@ class Fp4MoE:
             tensors = [dev_t(a, torch.uint8) for a in (w13_codes, w13_scales, w2_codes, w2_scales)]
             g13 = dev_t(g13, torch.float32)
             g2 = dev_t(g2, torch.float32)
-            self.prepared = torch.empty(prepared_bytes(desc), dtype=torch.uint8, device=dev)
+            self.prepared = torch.empty(n, dtype=torch.uint8, device=dev)
             prepare(desc, *tensors, g13, g2, self.prepared, stream)
             del tensors
             self.workspace = torch.empty(workspace_bytes(desc, desc.max_tokens), dtype=torch.uint8, device=dev)
@@ -309,6 +327,9 @@ class Fp4MoE:
         global scale per expert and matrix."""
         from . import block, experts
 
+        for name, t, shape in zip(("w13", "w2"), (w13, w2), desc.weights()):
+            if t.shape != shape:
+                raise ValueError(f"{name}: want {list(shape)}, got {list(t.shape)}")
         dev = block._device(device)
         with preparing(as_stream(stream, dev), dev, w13, w2) as made:
             q13, q2 = (experts.fp4_quantize(t.to(dev).contiguous(), desc.fmt) for t in (w13, w2))

@@ -239,3 +239,24 @@ def test_layer_calls_follow_their_tensors_to_another_device(monkeypatch):
         for stream, address in ((None, 1001), (77, 77), (types.SimpleNamespace(cuda_stream=78), 78)):
             call(stream)
             assert seen.pop() == (name, 1, address) and current == [0]
+
+
+@pytest.mark.parametrize("fmt,fn", [("mxfp4", "silu"), ("nvfp4", "silu"), ("mxfp4", "relu2")])
+def test_layer_refuses_weights_of_another_shape(fmt, fn):
+    """The library knows the descriptor alone: smaller weights than it says would
+    be read past their end."""
+    E, H, I, G = 4, 128, 64, experts.GROUP[fmt]
+    desc = moe.Desc(fmt, E, H, I, 2, 8, fn=fn)
+    rows = I if fn == "relu2" else 2 * I
+    w13, w2 = torch.zeros(E, rows, H), torch.zeros(E, H, I)
+    for a, b in ((w13[:3], w2), (w13, w2[:3]), (w13[:, :I // 2], w2), (w13[..., :64], w2), (w13, w2[..., :32]),
+                 (w13.transpose(1, 2) if rows != H else w13[:, 1:], w2), (w13, w2.transpose(1, 2)), (w13[0], w2)):
+        with pytest.raises(ValueError, match="want"):
+            moe.Fp4MoE.from_float(desc, a, b, device="cuda:0")
+    parts = [torch.zeros(E, rows, H // 2, dtype=torch.uint8), torch.zeros(E, rows, H // G, dtype=torch.uint8),
+             torch.zeros(E, H, I // 2, dtype=torch.uint8), torch.zeros(E, H, I // G, dtype=torch.uint8)]
+    parts += [torch.ones(E), torch.ones(E)] if fmt == "nvfp4" else []
+    for i in range(len(parts)):
+        for short in (parts[i][:-1], parts[i].flatten()[1:], parts[i].numpy()[1:]):
+            with pytest.raises(ValueError, match="want"):
+                moe.Fp4MoE(desc, *parts[:i], short, *parts[i + 1:], device="cuda:0")
