@@ -76,7 +76,8 @@ def test_linear_of_very_many_features_and_tokens():
 
 # Gated: outputs past 2^31 bytes in a tile; and up to the most features, whose
 # weights' subtiles need 2^32 threads of the few-token kernel.
-@pytest.mark.parametrize("M,N", [(300, (1 << 22) + 8), (1, (1 << 26) - 16), (2, (1 << 26) - 8), (4, 1 << 26), (5, 1 << 26)])
+@pytest.mark.parametrize("M,N", [(300, (1 << 22) + 8), (1, (1 << 26) - 16), (2, (1 << 26) - 8), (4, 1 << 26), (5, 1 << 26),
+                                 (20, 1 << 26)])
 def test_gated_linear_of_very_many_features(M, N):
     lin, codes, scales = wide_map(M, N, "silu")
     x = rand(2, M, 32).bfloat16().cuda()
